@@ -330,3 +330,8 @@ def chunk_gated_delta_rule_bwd(q, k, v, g, beta, A, do, dht=None, scale=None,
                            _ptr(db), _ptr(dg), _ptr(dh0), _ptr(_check_cache(state_cache, pr, q)),
                            _ptr(ws), ws_bytes, ctypes.c_void_p(stream)))
     return dq, dk, dv, db, dg, dh0
+
+
+from .mixer import (  # noqa: E402  (needs the names above)
+    causal_conv_bwd, causal_conv_fwd, causal_conv_step, gated_delta_rule_step, layer_norm_bwd, layer_norm_fwd,
+    selective_scan_bwd, selective_scan_fwd, selective_scan_step)

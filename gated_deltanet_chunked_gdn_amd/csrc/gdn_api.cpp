@@ -16,6 +16,7 @@
 
 #include "../../include/gdn.h"
 #include "gdn_internal.h"
+#include "gdn_mixer.h"
 
 namespace {
 
@@ -257,6 +258,18 @@ thread_local std::vector<TimedLaunch> g_launches;
 }  // namespace
 
 namespace gdn {
+
+int set_error(int code, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return code;
+}
+void clear_error() { g_err.clear(); }
+int64_t compute_units() { return device_compute_units(); }
 
 KernelTimer::KernelTimer(const char *name, hipStream_t stream) : slot_(-1), stream_(stream) {
   if (!g_timing) return;

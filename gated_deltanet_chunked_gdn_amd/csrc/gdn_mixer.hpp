@@ -1,0 +1,107 @@
+// Device helpers of the sequence-mixer kernels.
+#pragma once
+
+#include "gdn_common.hpp"
+#include "gdn_mixer.h"
+
+namespace gdn {
+
+// Sequence n's tokens [first, end), clamped to the batch, so that a bad
+// cu_seqlens on the device cannot lead a kernel out of its buffers.
+struct Span {
+  int64_t first, end;
+};
+__device__ __forceinline__ Span seq_span(const Seqs &s, int n) {
+  if (!s.cu) return Span{(int64_t)n * s.T, (int64_t)(n + 1) * s.T};
+  int64_t a = s.cu[n], b = s.cu[n + 1];
+  a = a < 0 ? 0 : (a > s.tokens ? s.tokens : a);
+  b = b < a ? a : (b > s.tokens ? s.tokens : b);
+  return Span{a, b};
+}
+
+// The last sequence n with first(n) <= t (empty sequences in front of the one
+// that holds t are passed over).
+__device__ __forceinline__ int seq_of(const Seqs &s, int64_t t) {
+  if (!s.cu) return (int)(t / s.T);
+  return find_seq(s.cu, s.N, t);
+}
+
+// 16 bytes (VEC elements) or one element, as floats.
+template <typename E, int VEC>
+struct Vec {
+  float v[VEC];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+  }
+  __device__ __forceinline__ void load(const E *p) {
+    if constexpr (VEC == 1) {
+      v[0] = to_f32(*p);
+    } else {
+      const uint4 r = *reinterpret_cast<const uint4 *>(p);
+      const E *e = reinterpret_cast<const E *>(&r);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
+    }
+  }
+  __device__ __forceinline__ void store(E *p) const {
+    if constexpr (VEC == 1) {
+      *p = from_f32<E>(v[0]);
+    } else {
+      uint4 r;
+      E *e = reinterpret_cast<E *>(&r);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
+      *reinterpret_cast<uint4 *>(p) = r;
+    }
+  }
+};
+// one raw 16-byte (or single-element) load, converted later: a batch of these
+// stays in flight without holding its fp32 form
+template <typename E, int VEC>
+struct Raw {
+  E e[VEC];
+  __device__ __forceinline__ void load(const E *p) {
+    if constexpr (VEC == 1) {
+      e[0] = *p;
+    } else {
+      *reinterpret_cast<uint4 *>(e) = *reinterpret_cast<const uint4 *>(p);
+    }
+  }
+  __device__ __forceinline__ Vec<E, VEC> f() const {
+    Vec<E, VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = to_f32(e[i]);
+    return r;
+  }
+} __attribute__((aligned(sizeof(E) * VEC)));
+
+template <typename E>
+constexpr int vec_of() {
+  return 16 / (int)sizeof(E);
+}
+
+// 1 / (1 + exp(-z)): v_exp_f32 and v_rcp_f32 (each within an ulp or so); 0 and
+// 1 at the ends, since exp(-z) runs to infinity and to 0.
+__device__ __forceinline__ float sigmoidf(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+}
+// log(1 + exp(z)) = max(z, 0) + log1p(exp(-|z|)), finite for every finite z
+// and to fp32's relative accuracy where it is small (there log1p matters: the
+// step sizes of a state-space layer begin at 0.001)
+__device__ __forceinline__ float softplusf(float z) {
+  return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
+}
+
+// a weight held in the problem's type or in fp32
+__device__ __forceinline__ float load_w(const void *p, int64_t i, int wdtype) {
+  return wdtype == 0 ? static_cast<const float *>(p)[i] : (float)static_cast<const bf16 *>(p)[i];
+}
+__device__ __forceinline__ void store_w(void *p, int64_t i, float v, int wdtype) {
+  if (wdtype == 0)
+    static_cast<float *>(p)[i] = v;
+  else
+    static_cast<bf16 *>(p)[i] = (bf16)v;
+}
+
+}  // namespace gdn

@@ -1,0 +1,432 @@
+// The selective state-space scan over whole sequences, and its backward.  Per
+// v-head, with the state S (K x V, fp32), delta_t = softplus(dt_t + dt_bias)
+// (or dt_t + dt_bias) and g_t = delta_t A:
+//
+//   S_t = e^{g_t} S_{t-1} + delta_t b_t x_t^T,   y_t = S_t^T c_t + D x_t
+//
+// Backward, with Z_t the gradient of S_t (all that follows from it, token t's
+// own output included):
+//
+//   Z_t = c_t dy_t^T + Z'_t,  Z'_t = e^{g_{t+1}} Z_{t+1}
+//   dc_t = S_t dy_t,  db_t = delta_t Z_t x_t,  dx_t = delta_t Z_t^T b_t + D dy_t
+//   dg_t = <e^{g_t} S_{t-1}, Z_t> = dg_{t+1} + a_t - delta_t r_t,
+//     a_t = c_t . e^{g_t} S_{t-1} dy_t,  r_t = x_t . Z'_t^T b_t
+//     (a token's own product (c.b)(x.dy) is in both <S_t, c dy^T> and
+//     delta <b x^T, Z_t> and is left out of both, so that it cancels exactly)
+//   d delta_t = r_t + m_t + A dg_t,  m_t = (c_t . b_t)(x_t . dy_t)
+//
+// Sequences are cut into segments that run side by side: a pass over every
+// segment from a zero state, a scan of the segments' ends, and the pass that
+// writes the results from the true start states (backward: the same in
+// reverse order for Z).  The chain of dg is begun again from <S, Z> at every
+// segment's end, which keeps the sums short.
+//
+// The kernels of this file hold the state in fp32 registers, one column (or
+// row) of it a lane, and walk token by token: they are the form for fp32
+// problems.
+#include "gdn_internal.h"
+#include "gdn_scan.hpp"
+
+namespace gdn {
+namespace scan {
+namespace {
+
+constexpr int TB = 16;  // tokens staged at a time
+
+// What a sweep does.  Lane operand L (one value a lane and token), uniform
+// operands U (the update's other factor) and P (the output's factor):
+//   kOut  forward, lanes over V:  L = delta x, U = b, P = c, out = y
+//   kDc   forward, lanes over K:  L = delta b, U = x, P = dy, out = dc
+//   kDx   reverse, lanes over V:  L = dy, U = c, P = b, out -> dx, r, dD
+//   kDb   reverse, lanes over K:  L = c, U = dy, P = x, out -> db
+//   kLocal / kRLocal: the state alone, from zero (lanes over V)
+enum Mode { kLocal, kOut, kDc, kRLocal, kDx, kDb };
+
+struct Sweep {
+  const void *L, *U, *P;
+  int64_t ls, us, ps;  // elements from one token to the next
+  int l_v, u_v, p_v;   // operand lies with the v-heads (else the c/b heads)
+  int LD;              // lane dimension (K or V)
+};
+
+template <typename E, int RD, int MODE>
+__global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s) {
+  constexpr bool REV = MODE == kRLocal || MODE == kDx || MODE == kDb;
+  constexpr bool OUT = MODE != kLocal && MODE != kRLocal;
+  constexpr bool LANE_V = MODE != kDc && MODE != kDb;
+  __shared__ __align__(16) float us[TB][RD], ps[OUT ? TB : 1][RD];
+  __shared__ float del[TB], dec[TB];
+  const int lane = threadIdx.x, slices = (s.LD + 63) >> 6;
+  const int sl = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv;
+  const int64_t slot = blockIdx.x / slices / a.Hv;
+  const SlotLoc loc = locate(a, slot);
+  if (!loc.used) return;
+  const int hq = h / (a.Hv / a.Hq);
+  const int l = sl * 64 + lane;
+  const bool on = l < s.LD;
+  const int lc = on ? l : s.LD - 1;  // idle lanes of a 32-wide operand read along, and write nothing
+  const E *L = static_cast<const E *>(s.L) + (int64_t)(s.l_v ? h : hq) * s.LD + lc;
+  const E *U = static_cast<const E *>(s.U) + (int64_t)(s.u_v ? h : hq) * RD;
+  const E *P = OUT ? static_cast<const E *>(s.P) + (int64_t)(s.p_v ? h : hq) * RD : nullptr;
+  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.D ? a.D[h] : 0.f;
+  const int64_t kv = (int64_t)a.K * a.V;
+  const int64_t sr = LANE_V ? a.V : 1, so = LANE_V ? lc : (int64_t)lc * a.V;
+
+  float S[RD];
+  const float *src = nullptr;
+  if (MODE == kOut || MODE == kDc)
+    src = a.one_seg && MODE == kOut ? (a.h0 ? a.h0 + (loc.n * (int64_t)a.Hv + h) * kv : nullptr)
+                                    : w.start(a) + (slot * a.Hv + h) * kv;
+  if (MODE == kDx || MODE == kDb) src = w.zend(a) + (slot * a.Hv + h) * kv;
+#pragma unroll
+  for (int r = 0; r < RD; ++r) S[r] = src ? src[r * sr + so] : 0.f;
+
+  float total = 0.f, dD = 0.f;
+  const int64_t nt = loc.t1 - loc.t0;
+  for (int64_t b0 = 0; b0 < nt; b0 += TB) {
+    // token j of the block is t0 + b0 + j, or counted back from the end
+    const int nb = (int)(nt - b0 < TB ? nt - b0 : TB);
+    __syncthreads();
+    for (int i = lane; i < TB * RD; i += 64) {
+      const int j = i / RD, r = i % RD;
+      const int jc = j < nb ? j : nb - 1;
+      const int64_t t = REV ? loc.t1 - 1 - (b0 + jc) : loc.t0 + b0 + jc;
+      us[j][r] = to_f32(U[t * s.us + r]);
+      if (OUT) ps[j][r] = to_f32(P[t * s.ps + r]);
+    }
+    if (lane < nb) {
+      const int64_t t = REV ? loc.t1 - 1 - (b0 + lane) : loc.t0 + b0 + lane;
+      const float z = to_f32(static_cast<const E *>(a.dt)[t * a.Hv + h]) + bias;
+      const float d = a.softplus ? softplusf(z) : z;
+      del[lane] = d;
+      dec[lane] = d * A;
+    }
+    float lv[TB];
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const int jc = j < nb ? j : nb - 1;
+      const int64_t t = REV ? loc.t1 - 1 - (b0 + jc) : loc.t0 + b0 + jc;
+      lv[j] = to_f32(L[t * s.ls]);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < nb; ++j) {
+      const int64_t t = REV ? loc.t1 - 1 - (b0 + j) : loc.t0 + b0 + j;
+      const float delta = del[j], decay = expf(dec[j]);
+      total += dec[j];
+      float mine = 0.f;  // lv[j] with j in a register index the compiler can see
+#pragma unroll
+      for (int i = 0; i < TB; ++i) mine = i == j ? lv[i] : mine;
+      const float f = REV ? mine : delta * mine;
+      // kDc, kDx: the output without the token's own update, and u . p
+      constexpr bool OWN = MODE == kDc || MODE == kDx;
+      float out = 0.f, up = 0.f;
+#pragma unroll
+      for (int r = 0; r < RD; r += 4) {
+        const f32x4 u = *reinterpret_cast<const f32x4 *>(&us[j][r]);
+        f32x4 p = zero4();
+        if (OUT) p = *reinterpret_cast<const f32x4 *>(&ps[j][r]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float old = REV ? S[r + i] : decay * S[r + i], now = old + f * u[i];
+          if (OUT) out += (OWN ? old : now) * p[i];
+          if (OWN) up += u[i] * p[i];
+          S[r + i] = REV ? decay * now : now;
+        }
+      }
+      if (MODE == kOut) {
+        const float x = mine;
+        if (on) static_cast<E *>(a.y)[(t * a.Hv + h) * a.V + l] = from_f32<E>(out + skip * x);
+      } else if (MODE == kDc || MODE == kDb) {
+        float *part = MODE == kDc ? w.dc_part(a) : w.db_part(a);
+        if (on) part[(t * a.Hv + h) * a.K + l] = MODE == kDc ? out + f * up : delta * out;
+        if (MODE == kDc) {
+          const float c = to_f32(static_cast<const E *>(a.c)[t * a.cs + (int64_t)hq * a.K + lc]);
+          const float v = wave_sum(on ? c * out : 0.f);
+          if (lane == 0) w.a_part(a)[((int64_t)sl * a.Hv + h) * a.s.tokens + t] = v;
+        }
+      } else if (MODE == kDx) {
+        const float x = to_f32(static_cast<const E *>(a.x)[t * a.xs + (int64_t)h * a.V + lc]);
+        if (on) static_cast<E *>(a.dx)[(t * a.Hv + h) * a.V + l] = from_f32<E>(delta * (out + f * up) + skip * mine);
+        const float v = wave_sum(on ? x * out : 0.f), xd = wave_sum(on ? x * mine : 0.f);
+        if (lane == 0) {
+          const int64_t i = ((int64_t)sl * a.Hv + h) * a.s.tokens + t;
+          w.r_part(a)[i] = v;
+          w.m_part(a)[i] = xd * up;
+        }
+        dD += xd;
+      }
+    }
+  }
+  if (MODE == kLocal || MODE == kRLocal) {
+    float *dst = (MODE == kLocal ? w.start(a) : w.zend(a)) + (slot * a.Hv + h) * kv;
+    if (on)
+      for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
+    if (MODE == kLocal && lane == 0 && sl == 0) w.decay(a)[slot * a.Hv + h] = total;
+  }
+  if (MODE == kOut && a.one_seg && a.ht && on) {
+    float *dst = a.ht + (loc.n * (int64_t)a.Hv + h) * kv;
+    for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
+  }
+  if (MODE == kDx) {
+    if (lane == 0) w.dd_part(a)[((int64_t)sl * a.slots + slot) * a.Hv + h] = dD;
+  }
+}
+
+// The segments' local ends -> every segment's start state (in place), and the
+// sequence's last state.  One thread has 4 elements of one head's state.
+__global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float *hend) {
+  const int64_t kv4 = (int64_t)a.K * a.V / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
+  if (n >= a.s.N) return;
+  const Span sp = seq_span(a.s, (int)n);
+  const int64_t slot = sp.first / a.seg + n, ns = segs_of(sp, a.seg);
+  f32x4 cur = zero4();
+  const int64_t own = (n * a.Hv + h) * kv4 + e;
+  if (a.h0) cur = reinterpret_cast<const f32x4 *>(a.h0)[own];
+  f32x4 *H = reinterpret_cast<f32x4 *>(w.start(a)) + h * kv4 + e;
+  for (int64_t s = 0; s < ns; ++s) {
+    f32x4 *p = H + (slot + s) * a.Hv * kv4;
+    const float d = expf(w.decay(a)[(slot + s) * a.Hv + h]);
+    const f32x4 x = *p;
+    *p = cur;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cur[j] = d * cur[j] + x[j];
+  }
+  if (a.ht) reinterpret_cast<f32x4 *>(a.ht)[own] = cur;
+  if (hend) reinterpret_cast<f32x4 *>(hend)[own] = cur;
+}
+
+// In reverse: every segment's local gradient of its start state -> the
+// gradient of its last state from what follows it (in place), and dh0.
+__global__ __launch_bounds__(256) void rcarry_kernel(ScanArgs a, Layout w) {
+  const int64_t kv4 = (int64_t)a.K * a.V / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
+  if (n >= a.s.N) return;
+  const Span sp = seq_span(a.s, (int)n);
+  const int64_t slot = sp.first / a.seg + n, ns = segs_of(sp, a.seg);
+  f32x4 cur = zero4();
+  const int64_t own = (n * a.Hv + h) * kv4 + e;
+  if (a.dht) cur = reinterpret_cast<const f32x4 *>(a.dht)[own];
+  f32x4 *Z = reinterpret_cast<f32x4 *>(w.zend(a)) + h * kv4 + e;
+  for (int64_t s = ns - 1; s >= 0; --s) {
+    f32x4 *p = Z + (slot + s) * a.Hv * kv4;
+    const float d = expf(w.decay(a)[(slot + s) * a.Hv + h]);
+    const f32x4 x = *p;
+    *p = cur;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cur[j] = d * cur[j] + x[j];
+  }
+  if (a.dh0) reinterpret_cast<f32x4 *>(a.dh0)[own] = cur;
+}
+
+// dg from a_t, r_t and m_t, then ddt and the segment's part of dA, ddt_bias and
+// dD.  One wave has one segment of one head, 64 tokens at a time from its
+// end, begun from <S, Z> of its last state.
+template <typename E>
+__global__ __launch_bounds__(64) void gates_kernel(ScanArgs a, Layout w, int kslices, int vslices) {
+  const int lane = threadIdx.x, h = blockIdx.x % a.Hv;
+  const int64_t slot = blockIdx.x / a.Hv;
+  const SlotLoc loc = locate(a, slot);
+  float *part = w.head_part(a) + (slot * a.Hv + h) * 3;
+  if (!loc.used) {
+    if (lane < 3) part[lane] = 0.f;
+    return;
+  }
+  const int64_t kv4 = (int64_t)a.K * a.V / 4;
+  const f32x4 *se = reinterpret_cast<const f32x4 *>(
+      loc.last ? w.hend(a) + (loc.n * (int64_t)a.Hv + h) * kv4 * 4 : w.start(a) + ((slot + 1) * a.Hv + h) * kv4 * 4);
+  const f32x4 *ze = reinterpret_cast<const f32x4 *>(w.zend(a) + (slot * a.Hv + h) * kv4 * 4);
+  float x = 0.f;
+  for (int64_t i = lane; i < kv4; i += 64) {
+    const f32x4 p = se[i], q = ze[i];
+    x += p[0] * q[0] + p[1] * q[1] + p[2] * q[2] + p[3] * q[3];
+  }
+  float dg_next = wave_sum(x);
+  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  float dA = 0.f, dbias = 0.f;
+  for (int64_t e = loc.t1; e > loc.t0; e -= 64) {
+    const int64_t t = e - 1 - lane;  // lane 0 has the last token
+    const bool on = t >= loc.t0;
+    float av = 0.f, rv = 0.f, mv = 0.f, z = 0.f;
+    if (on) {
+      for (int s = 0; s < kslices; ++s) av += w.a_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
+      for (int s = 0; s < vslices; ++s) {
+        rv += w.r_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
+        mv += w.m_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
+      }
+      z = to_f32(static_cast<const E *>(a.dt)[t * a.Hv + h]) + bias;
+    }
+    const float delta = on ? (a.softplus ? softplusf(z) : z) : 0.f;
+    // dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 to fp32 where the token forgets all
+    // (e^-20 is far below half a step of its parts), and the chain begins
+    // again there: delta_t r_t, large where delta_t is, leaves no rounding.
+    int cut = on && delta * A < -20.f;
+    float dg = cut ? 0.f : on ? av - delta * rv : 0.f;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const float below = __shfl_up(dg, d);
+      const int cut_below = __shfl_up(cut, d);
+      if (lane >= d && !cut) {
+        dg += below;
+        cut = cut_below;
+      }
+    }
+    if (!cut) dg += dg_next;
+    dg_next = lane63(dg);
+    float dd = rv + mv + A * dg;
+    if (a.softplus) dd *= 1.f / (1.f + expf(-z));
+    if (on) {
+      static_cast<E *>(a.ddt)[t * a.Hv + h] = from_f32<E>(dd);
+      dA += delta * dg;
+      dbias += dd;
+    }
+  }
+  dA = wave_sum(dA);
+  dbias = wave_sum(dbias);
+  if (lane == 0) {
+    float dD = 0.f;
+    for (int s = 0; s < vslices; ++s) dD += w.dd_part(a)[((int64_t)s * a.slots + slot) * a.Hv + h];
+    part[0] = dA;
+    part[1] = dbias;
+    part[2] = dD;
+  }
+}
+
+// dA, ddt_bias, dD of a head: the segments' parts, 64 interleaved sums joined
+// in a fixed order.
+__global__ __launch_bounds__(64) void heads_kernel(ScanArgs a, Layout w) {
+  const int h = blockIdx.x;
+  float v[3] = {0.f, 0.f, 0.f};
+  for (int64_t s = threadIdx.x; s < a.slots; s += 64)
+    for (int k = 0; k < 3; ++k) v[k] += w.head_part(a)[(s * a.Hv + h) * 3 + k];
+  float *out[3] = {a.dA, a.ddt_bias, a.dD};
+  for (int k = 0; k < 3; ++k) {
+    const float t = wave_sum(v[k]);
+    if (threadIdx.x == 0 && out[k]) out[k][h] = t;
+  }
+}
+
+// dc, db: the sum over the heads of a group, 4 elements a thread.
+template <typename E>
+__global__ __launch_bounds__(256) void group_kernel(ScanArgs a, Layout w) {
+  const int64_t k4 = a.K / 4, n = a.s.tokens * a.Hq * k4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int R = a.Hv / a.Hq;
+  const int64_t e = i % k4, th = i / k4;  // th = token * Hq + hq
+  const f32x4 *pc = reinterpret_cast<const f32x4 *>(w.dc_part(a)) + th * R * k4 + e;
+  const f32x4 *pb = reinterpret_cast<const f32x4 *>(w.db_part(a)) + th * R * k4 + e;
+  f32x4 c = zero4(), b = zero4();
+  for (int r = 0; r < R; ++r) {
+    c += pc[r * k4];
+    b += pb[r * k4];
+  }
+  st4(static_cast<E *>(a.dc) + i * 4, c[0], c[1], c[2], c[3]);
+  st4(static_cast<E *>(a.db) + i * 4, b[0], b[1], b[2], b[3]);
+}
+
+template <typename E, int MODE>
+hipError_t sweep(const char *name, const ScanArgs &a, const Layout &w, const Sweep &s, int rd, hipStream_t st) {
+  const unsigned blocks = (unsigned)(a.slots * a.Hv * ((s.LD + 63) / 64));
+  KernelTimer kt(name, st);
+  if (rd == 32)
+    sweep_kernel<E, 32, MODE><<<blocks, 64, 0, st>>>(a, w, s);
+  else if (rd == 64)
+    sweep_kernel<E, 64, MODE><<<blocks, 64, 0, st>>>(a, w, s);
+  else
+    sweep_kernel<E, 128, MODE><<<blocks, 64, 0, st>>>(a, w, s);
+  return hipGetLastError();
+}
+
+unsigned carry_blocks(const ScanArgs &a) {
+  return (unsigned)(((int64_t)a.s.N * a.Hv * a.K * a.V / 4 + 255) / 256);
+}
+
+template <typename E>
+hipError_t fwd(const ScanArgs &a, hipStream_t st) {
+  const Layout w = layout(a, false);
+  hipError_t e = hipSuccess;
+  const Sweep out{a.x, a.b, a.c, a.xs, a.bs, a.cs, 1, 0, 0, a.V};
+  if (!a.one_seg) {
+    e = sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
+    if (e != hipSuccess) return e;
+    KernelTimer kt("scan_carry", st);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return sweep<E, kOut>("scan_out", a, w, out, a.K, st);
+}
+
+template <typename E>
+hipError_t bwd(const ScanArgs &a, hipStream_t st) {
+  const Layout w = layout(a, true);
+  const int64_t qs = (int64_t)a.Hv * a.V;  // dy is contiguous
+  const Sweep out{a.x, a.b, a.c, a.xs, a.bs, a.cs, 1, 0, 0, a.V};
+  const Sweep dc{a.b, a.x, a.dy, a.bs, a.xs, qs, 0, 1, 1, a.K};
+  const Sweep dx{a.dy, a.c, a.b, qs, a.cs, a.bs, 1, 0, 0, a.V};
+  const Sweep db{a.c, a.dy, a.x, a.cs, qs, a.xs, 0, 1, 1, a.K};
+  hipError_t e;
+#define GDN_DO(x) \
+  if ((e = (x)) != hipSuccess) return e
+  GDN_DO((sweep<E, kLocal>("scan_local", a, w, out, a.K, st)));
+  GDN_DO((sweep<E, kRLocal>("scan_rlocal", a, w, dx, a.K, st)));
+  {
+    KernelTimer kt("scan_carry", st);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, w.hend(a));
+    rcarry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w);
+    GDN_DO(hipGetLastError());
+  }
+  GDN_DO((sweep<E, kDc>("scan_dc", a, w, dc, a.V, st)));
+  GDN_DO((sweep<E, kDx>("scan_dx", a, w, dx, a.K, st)));
+  GDN_DO((sweep<E, kDb>("scan_db", a, w, db, a.V, st)));
+  {
+    KernelTimer kt("scan_gates", st);
+    gates_kernel<E><<<(unsigned)(a.slots * a.Hv), 64, 0, st>>>(a, w, (a.K + 63) / 64, (a.V + 63) / 64);
+    heads_kernel<<<a.Hv, 64, 0, st>>>(a, w);
+    GDN_DO(hipGetLastError());
+  }
+  if (a.s.tokens) {
+    KernelTimer kt("scan_group", st);
+    const int64_t n = a.s.tokens * a.Hq * (a.K / 4);
+    group_kernel<E><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, w);
+    GDN_DO(hipGetLastError());
+  }
+#undef GDN_DO
+  return hipSuccess;
+}
+
+}  // namespace
+}  // namespace scan
+
+// Forward segments: as long as the whole sequence unless that leaves compute
+// units without work, then a multiple of 64 tokens that gives about two waves
+// a SIMD over all heads.  Backward: 64 tokens, because the chain of dg
+// gathers the rounding of every a_t and r_t since the segment's end: over 256
+// tokens the sums over a head (ddt_bias) were off by 4e-5 of their value.
+ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
+  ScanArgs a = a0;
+  const int64_t per = (int64_t)a.Hv * ((a.V + 63) / 64);
+  int64_t want = (compute_units() * 8 + per - 1) / per;  // segments over the whole batch
+  if (want < a.s.N) want = a.s.N;
+  int64_t seg = (a.s.tokens + want - 1) / want;
+  seg = bwd ? 64 : (seg + 63) / 64 * 64;
+  if (seg < 64) seg = 64;
+  ScanPlan p;
+  p.seg = (int)seg;
+  a.slots = p.slots = a.s.tokens / seg + a.s.N;
+  a.one_seg = p.one_seg = !bwd && a.s.T <= seg;
+  p.ws = scan::layout(a, bwd).total;
+  return p;
+}
+
+hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
+  return a.dtype == 1 ? scan::fwd<bf16>(a, st) : scan::fwd<float>(a, st);
+}
+hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
+  return a.dtype == 1 ? scan::bwd<bf16>(a, st) : scan::bwd<float>(a, st);
+}
+
+}  // namespace gdn

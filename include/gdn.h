@@ -160,6 +160,133 @@ int gdn_chunk_fwd_noalloc(const gdn_problem_t *p, const void *q,
                           void *state_cache, void *stream);
 size_t gdn_chunk_fwd_noalloc_max_bytes(void);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the chunked gated delta rule in a sequence mixer: the
+ * short causal convolution in front of it, the selective state-space scan
+ * that takes the same place, the norm behind it, and all of them (and the
+ * delta rule itself) for single tokens.
+ *
+ * Layouts are token-major as above, T the total packed tokens with
+ * cu_seqlens.  Weights and their gradients are in the type that
+ * weight_dtype says (the problem's or fp32), every sum is held in fp32, and
+ * no result depends on the order in which workgroups run.
+ *
+ * cu_seqlens_host is optional here: given, it is checked as for the chunked
+ * calls; NULL, the device copy is taken as it is (no host read, so such a
+ * call can be captured into a graph).  The kernels clamp what they read from
+ * it to the batch, so a wrong one gives wrong results and no wild access.
+ * Rows past the last sequence of such a batch are left as they were.
+ *
+ * A *_stride is the distance in elements from one token (row of the batch
+ * for the steps) to the next, so that q, k, v or x may be a slice of a wider
+ * projection; 0 means contiguous.
+ *
+ * state_indices (device int32 [B], optional): the slot of each batch row in a
+ * state buffer of `slots` slots.  A row whose index is outside [0, slots) is
+ * padding: its output is zero and no state changes.  So is a row that names
+ * a slot that an earlier row names.  Without it row i has slot i and
+ * slots >= B is required.
+ * ------------------------------------------------------------------------ */
+
+/* y_t = act(bias + sum_j weight[:, j] x_{t-(W-1)+j}), per channel, tokens
+ * before a sequence's first from its initial state (or 0).
+ *   x, y, dy, dx  [B, T, D]       problem dtype (x_stride for x)
+ *   weight        [D, W], W in {2, 3, 4}; bias [D] or NULL; dweight, dbias
+ *                 as these: weight_dtype
+ *   initial_state, final_state, dfinal_state, dinitial_state
+ *                 [N, W - 1, D]   problem dtype, the last W - 1 inputs
+ * Every pointer is aligned to its element; rows of 16-byte pieces (D and
+ * x_stride a multiple of 8 in bf16, 4 in fp32, buffers 16-byte aligned) are
+ * the fast form. */
+typedef struct {
+  int32_t B, T, D, W, N; /* N: sequences (B without cu_seqlens) */
+  int32_t dtype, weight_dtype; /* gdn_dtype_t */
+  int32_t silu; /* 1: act(z) = z sigmoid(z); 0: none */
+  int64_t x_stride;
+  const int32_t *cu_seqlens, *cu_seqlens_host;
+} gdn_conv_t;
+/* Required: x weight y.  final_state NULL = not wanted. */
+int gdn_causal_conv_fwd(const gdn_conv_t *p, const void *x, const void *weight, const void *bias,
+                        const void *initial_state, void *y, void *final_state, void *stream);
+/* Required: x weight dy dx dweight; dbias iff bias; dinitial_state optional;
+ * dfinal_state NULL = zero. */
+size_t gdn_causal_conv_bwd_workspace_size(const gdn_conv_t *p);
+int gdn_causal_conv_bwd(const gdn_conv_t *p, const void *x, const void *weight, const void *bias,
+                        const void *dy, const void *initial_state, const void *dfinal_state, void *dx,
+                        void *dweight, void *dbias, void *dinitial_state, void *workspace,
+                        size_t ws_bytes, void *stream);
+/* One token of each batch row: x, y [B, D] (T = 1), state [slots, W - 1, D]
+ * moved on in place. */
+int gdn_causal_conv_step(const gdn_conv_t *p, const void *x, void *state, const void *weight,
+                         const void *bias, const int32_t *state_indices, int32_t slots, void *y,
+                         void *stream);
+
+/* The selective state-space scan: per v-head, with the state S (K x V, fp32)
+ * and delta_t = dt_t + dt_bias, through softplus if asked,
+ *   S_t = exp(delta_t A) S_{t-1} + delta_t b_t x_t^T,  y_t = S_t^T c_t + D x_t
+ *   c, b          [B, T, Hq, K]   problem dtype; v-head h reads head h / (Hv / Hq)
+ *   x, y, dy, dx  [B, T, Hv, V]   problem dtype
+ *   dt, ddt       [B, T, Hv]      problem dtype
+ *   A, D, dt_bias [Hv] fp32 (D, dt_bias optional), dA, dD, ddt_bias as these
+ *   initial_state, final_state, dht, dh0 [N, Hv, K, V] fp32
+ * K, V in {32, 64, 128} in bf16, {32, 64} in fp32.  c, b, x, y, dy, dx, dc,
+ * db and the states are 16-byte aligned, c_stride, b_stride, x_stride
+ * multiples of 16 bytes. */
+typedef struct {
+  int32_t B, T, Hq, Hv, K, V, N, dtype;
+  int32_t dt_softplus; /* 1: delta = softplus(dt + dt_bias) */
+  int64_t c_stride, b_stride, x_stride;
+  const int32_t *cu_seqlens, *cu_seqlens_host;
+} gdn_scan_t;
+size_t gdn_selective_scan_fwd_workspace_size(const gdn_scan_t *p);
+size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_t *p);
+/* Required: c b x dt A y. */
+int gdn_selective_scan_fwd(const gdn_scan_t *p, const void *c, const void *b, const void *x, const void *dt,
+                           const float *A, const float *D, const float *dt_bias, const float *h0, void *y,
+                           float *ht, void *workspace, size_t ws_bytes, void *stream);
+/* Required: c b x dt A dy dc db dx ddt dA; dD, ddt_bias and dh0 optional
+ * outputs; dht NULL = zero. */
+int gdn_selective_scan_bwd(const gdn_scan_t *p, const void *c, const void *b, const void *x, const void *dt,
+                           const float *A, const float *D, const float *dt_bias, const float *h0,
+                           const void *dy, const float *dht, void *dc, void *db, void *dx, void *ddt,
+                           float *dA, float *dD, float *ddt_bias, float *dh0, void *workspace,
+                           size_t ws_bytes, void *stream);
+/* One token of each batch row: c, b [B, Hq, K], x, y [B, Hv, V], dt [B, Hv]
+ * (T = 1, N = B), state [slots, Hv, K, V] fp32 in place.  K, V in {32, 64,
+ * 128} for both dtypes. */
+int gdn_selective_scan_step(const gdn_scan_t *p, const void *c, const void *b, const void *x, const void *dt,
+                            const float *A, const float *D, const float *dt_bias, float *state,
+                            const int32_t *state_indices, int32_t slots, void *y, void *stream);
+/* One token of the gated delta rule for each batch row (p: T = 1, N = B, no
+ * cu_seqlens, cp_mode ignored; K, V in {32, 64, 128} for both dtypes):
+ * q, k [B, Hq, K], v, o [B, Hv, V], g, beta [B, Hv], state [slots, Hv, K, V]
+ * fp32 in place. */
+int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, const void *v, const float *g,
+                        const void *beta, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        float *state, const int32_t *state_indices, int32_t slots, void *o, void *stream);
+
+/* Layer norm over the last dimension, with an optional output gate:
+ *   z = (x - mean) rstd weight + bias,  y = z silu(gate)
+ * rstd = (mean square of x - mean, + eps)^-1/2; with rms the mean is 0.
+ *   x, gate, y, dy, dx, dgate [rows, D] problem dtype, contiguous
+ *   weight, bias [D] weight_dtype or NULL; dweight, dbias as these
+ *   mean, rstd [rows] fp32 (mean not with rms) */
+typedef struct {
+  int64_t rows;
+  int32_t D, dtype, weight_dtype, rms;
+  float eps;
+} gdn_norm_t;
+/* Required: x y; mean, rstd NULL = not wanted. */
+int gdn_layer_norm_fwd(const gdn_norm_t *p, const void *x, const void *weight, const void *bias,
+                       const void *gate, void *y, float *mean, float *rstd, void *stream);
+/* Required: dy x rstd dx, mean without rms, dgate iff gate; dweight, dbias
+ * optional, each only with its weight or bias. */
+size_t gdn_layer_norm_bwd_workspace_size(const gdn_norm_t *p);
+int gdn_layer_norm_bwd(const gdn_norm_t *p, const void *dy, const void *x, const void *weight,
+                       const void *bias, const void *gate, const float *mean, const float *rstd,
+                       void *dx, void *dweight, void *dbias, void *dgate, void *workspace,
+                       size_t ws_bytes, void *stream);
+
 /* Number of context-parallel segments the forward would launch for this
  * problem (host-only planning query; 0 if invalid). */
 int64_t gdn_plan_segments(const gdn_problem_t *p);
