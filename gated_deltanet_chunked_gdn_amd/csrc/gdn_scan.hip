@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
   const int sl = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv;
   const int64_t slot = blockIdx.x / slices / a.Hv;
   const SlotLoc loc = locate(a, slot);
-  if (!loc.used) return;
+  if (!loc.used || (MODE == kLocal && loc.last && !w.need_last)) return;
   const int hq = h / (a.Hv / a.Hq);
   const int l = sl * 64 + lane;
   const bool on = l < s.LD;
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
       for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
     if (MODE == kLocal && lane == 0 && sl == 0) w.decay(a)[slot * a.Hv + h] = total;
   }
-  if (MODE == kOut && a.one_seg && a.ht && on) {
+  if (MODE == kOut && loc.last && a.ht && on) {
     float *dst = a.ht + (loc.n * (int64_t)a.Hv + h) * kv;
     for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
   }
@@ -173,8 +173,9 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
   }
 }
 
-// The segments' local ends -> every segment's start state (in place), and the
-// sequence's last state.  One thread has 4 elements of one head's state.
+// The segments' local ends -> every segment's start state (in place), and in
+// the backward the sequence's last state.  One thread has 4 elements of one
+// head's state.
 __global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float *hend) {
   const int64_t kv4 = (int64_t)a.K * a.V / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -188,13 +189,16 @@ __global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float 
   f32x4 *H = reinterpret_cast<f32x4 *>(w.start(a)) + h * kv4 + e;
   for (int64_t s = 0; s < ns; ++s) {
     f32x4 *p = H + (slot + s) * a.Hv * kv4;
-    const float d = expf(w.decay(a)[(slot + s) * a.Hv + h]);
-    const f32x4 x = *p;
+    f32x4 x = zero4();
+    float d = 0.f;
+    if (s < ns - 1 || w.need_last) {
+      x = *p;
+      d = expf(w.decay(a)[(slot + s) * a.Hv + h]);
+    }
     *p = cur;
 #pragma unroll
     for (int j = 0; j < 4; ++j) cur[j] = d * cur[j] + x[j];
   }
-  if (a.ht) reinterpret_cast<f32x4 *>(a.ht)[own] = cur;
   if (hend) reinterpret_cast<f32x4 *>(hend)[own] = cur;
 }
 
@@ -351,13 +355,13 @@ hipError_t fwd(const ScanArgs &a, hipStream_t st) {
   hipError_t e = hipSuccess;
   const Sweep out{a.x, a.b, a.c, a.xs, a.bs, a.cs, 1, 0, 0, a.V};
   if (!a.one_seg) {
-    e = sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
+    e = a.dtype == 1 ? launch_mma_local(a, w, st) : sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
     carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  return sweep<E, kOut>("scan_out", a, w, out, a.K, st);
+  return a.dtype == 1 ? launch_mma_out(a, w, st) : sweep<E, kOut>("scan_out", a, w, out, a.K, st);
 }
 
 template <typename E>
@@ -408,8 +412,9 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 // tokens the sums over a head (ddt_bias) were off by 4e-5 of their value.
 ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   ScanArgs a = a0;
-  const int64_t per = (int64_t)a.Hv * ((a.V + 63) / 64);
-  int64_t want = (compute_units() * 8 + per - 1) / per;  // segments over the whole batch
+  const int64_t per = (int64_t)a.Hv * ((a.V + 63) / 64);  // waves a segment
+  // bf16: a workgroup of four waves holds a compute unit
+  int64_t want = (compute_units() * (a.dtype == 1 ? 4 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
   seg = bwd ? 64 : (seg + 63) / 64 * 64;

@@ -10,6 +10,7 @@ namespace scan {
 struct Layout {
   size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_m = 0, o_dd = 0, o_head = 0, o_dc = 0, o_db = 0,
          total = 0;
+  bool need_last = false;  // the local pass runs a sequence's last segment too
   __host__ __device__ float *at(const ScanArgs &a, size_t o) const { return reinterpret_cast<float *>(a.ws + o); }
   // fp32 [slots][Hv][K][V]: a segment's state from zero, then its start state
   __host__ __device__ float *start(const ScanArgs &a) const { return at(a, o_start); }
@@ -57,9 +58,16 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_dc = piece(tok * a.K);
     w.o_db = piece(tok * a.K);
   }
+  w.need_last = bwd;
   w.total = off ? off : 256;
   return w;
 }
+
+// Column slices of a head group that a workgroup of the matrix kernels has.
+inline int slices_per_block(int per) { return per % 4 == 0 ? 4 : per % 2 == 0 ? 2 : 1; }
+// bf16, gdn_scan_mma.hip
+hipError_t launch_mma_local(const ScanArgs &a, const Layout &w, hipStream_t st);
+hipError_t launch_mma_out(const ScanArgs &a, const Layout &w, hipStream_t st);
 
 __host__ __device__ inline int64_t segs_of(const Span &sp, int seg) {
   const int64_t n = (sp.end - sp.first + seg - 1) / seg;
