@@ -75,11 +75,8 @@ struct StepArgs {
 };
 hipError_t launch_step(const StepArgs &a, hipStream_t st);
 
-// The selective scan over whole sequences.  A sequence is cut into segments
-// of `seg` tokens; segment s of sequence n has slot first(n) / seg + n + s,
-// first(n) its first token: distinct without a table, since floor(x / seg) + n
-// grows by at least ceil(len / seg) and at least 1 from one sequence to the
-// next.
+// The selective scan over whole sequences, cut into segments of `seg` tokens;
+// each has a slot in the workspace (gdn_scan.hpp).
 struct ScanArgs {
   Seqs s;
   int Hq, Hv, K, V, dtype, softplus;

@@ -182,7 +182,7 @@ __global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float 
   const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
   if (n >= a.s.N) return;
   const Span sp = seq_span(a.s, (int)n);
-  const int64_t slot = sp.first / a.seg + n, ns = segs_of(sp, a.seg);
+  const int64_t slot = first_slot(a.s, sp, (int)n, a.seg), ns = segs_of(sp, a.seg);
   f32x4 cur = zero4();
   const int64_t own = (n * a.Hv + h) * kv4 + e;
   if (a.h0) cur = reinterpret_cast<const f32x4 *>(a.h0)[own];
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256) void rcarry_kernel(ScanArgs a, Layout w) {
   const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
   if (n >= a.s.N) return;
   const Span sp = seq_span(a.s, (int)n);
-  const int64_t slot = sp.first / a.seg + n, ns = segs_of(sp, a.seg);
+  const int64_t slot = first_slot(a.s, sp, (int)n, a.seg), ns = segs_of(sp, a.seg);
   f32x4 cur = zero4();
   const int64_t own = (n * a.Hv + h) * kv4 + e;
   if (a.dht) cur = reinterpret_cast<const f32x4 *>(a.dht)[own];
@@ -412,16 +412,18 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 // tokens the sums over a head (ddt_bias) were off by 4e-5 of their value.
 ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   ScanArgs a = a0;
-  const int64_t per = (int64_t)a.Hv * ((a.V + 63) / 64);  // waves a segment
-  // bf16: a workgroup of four waves holds a compute unit
-  int64_t want = (compute_units() * (a.dtype == 1 ? 4 : 8) + per - 1) / per;  // segments over the whole batch
+  // workgroups a segment: of the matrix kernels (bf16) one holds a compute
+  // unit, of the sweeps' single waves eight do
+  const int slices = a.Hv / a.Hq * (a.V / 32);
+  const int64_t per = a.dtype == 1 ? (int64_t)a.Hq * (slices / scan::slices_per_block(slices)) : (int64_t)a.Hv * ((a.V + 63) / 64);
+  int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
   seg = bwd ? 64 : (seg + 63) / 64 * 64;
   if (seg < 64) seg = 64;
   ScanPlan p;
   p.seg = (int)seg;
-  a.slots = p.slots = a.s.tokens / seg + a.s.N;
+  a.slots = p.slots = a.s.cu ? a.s.tokens / seg + a.s.N : a.s.N * scan::segs_of(Span{0, a.s.T}, p.seg);
   a.one_seg = p.one_seg = !bwd && a.s.T <= seg;
   p.ws = scan::layout(a, bwd).total;
   return p;

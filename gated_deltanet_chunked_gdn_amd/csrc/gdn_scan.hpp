@@ -64,7 +64,7 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
 }
 
 // Column slices of a head group that a workgroup of the matrix kernels has.
-inline int slices_per_block(int per) { return per % 4 == 0 ? 4 : per % 2 == 0 ? 2 : 1; }
+inline int slices_per_block(int per) { return per % 8 == 0 ? 8 : per % 4 == 0 ? 4 : per % 2 == 0 ? 2 : 1; }
 // bf16, gdn_scan_mma.hip
 hipError_t launch_mma_local(const ScanArgs &a, const Layout &w, hipStream_t st);
 hipError_t launch_mma_out(const ScanArgs &a, const Layout &w, hipStream_t st);
@@ -74,6 +74,13 @@ __host__ __device__ inline int64_t segs_of(const Span &sp, int seg) {
   return n > 0 ? n : 1;  // an empty sequence has one empty segment
 }
 
+// The first slot of sequence n.  Packed: first / seg + n, distinct without a
+// table, since floor(x / seg) + n grows by at least ceil(len / seg) and at
+// least 1 from one sequence to the next.
+__host__ __device__ inline int64_t first_slot(const Seqs &s, const Span &sp, int n, int seg) {
+  return s.cu ? sp.first / seg + n : (int64_t)n * segs_of(sp, seg);
+}
+
 struct SlotLoc {
   int n;
   int64_t t0, t1;  // tokens of the segment
@@ -81,15 +88,19 @@ struct SlotLoc {
 };
 __device__ __forceinline__ SlotLoc locate(const ScanArgs &a, int64_t slot) {
   int lo = 0, hi = a.s.N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (seq_span(a.s, mid).first / a.seg + mid <= slot)
-      lo = mid;
-    else
-      hi = mid - 1;
+  if (!a.s.cu) {
+    lo = (int)(slot / segs_of(Span{0, a.s.T}, a.seg));
+  } else {
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_slot(a.s, seq_span(a.s, mid), mid, a.seg) <= slot)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
   }
   const Span sp = seq_span(a.s, lo);
-  const int64_t s = slot - (sp.first / a.seg + lo), ns = segs_of(sp, a.seg);
+  const int64_t s = slot - first_slot(a.s, sp, lo, a.seg), ns = segs_of(sp, a.seg);
   SlotLoc l;
   l.n = lo;
   l.used = s >= 0 && s < ns;

@@ -5,11 +5,14 @@
 //   y_i = 2^{gamma_i} S^T c_i + sum_{j <= i} (c_i . b_j) 2^{gamma_i - gamma_j} delta_j x_j + D x_i
 //   S'  = 2^{gamma_L} S + sum_j b_j (2^{gamma_L - gamma_j} delta_j x_j)^T
 //
-// A wave owns VW = min(V, 64) columns of one head's state and a segment's
-// chunks in order; the waves of a workgroup are column slices that share c
-// and b (the v-heads of a group, and the halves of a head of 128), which the
-// workgroup stages for the next chunk while it works on this one.  No wave
-// waits for another but at the one barrier a chunk.
+// A wave owns 32 columns of one head's state and a segment's chunks in order;
+// the waves of a workgroup (8 where the group has as many) are column slices
+// of a head group, which share c and b: the workgroup stages those for the
+// next chunk while it works on this one, and no wave waits for another but at
+// the one barrier a chunk.  (64 columns a wave form B C^T half as often, but
+// then the state needs the accumulation registers, which vector instructions
+// reach only by moves, and one wave a SIMD leaves its latencies open: 171 us
+// against the 8-wave form's time at 8192 tokens x 64 heads.)
 //
 // Everything is arranged so that accumulators are operands without moving
 // (gdn_slice.hpp): S tiles (rows k, lane v) give S^T for c; C B^T is formed
@@ -138,9 +141,9 @@ __device__ __forceinline__ Split split_scaled(const bf16x8 &x, const float *w) {
 
 template <int K, int V>
 struct Dims {
-  static constexpr int VW = V < 64 ? V : 64, VT = VW / 32, KT = K / 32;
+  static constexpr int VW = 32, KT = K / 32;
   static constexpr int KP = K + 16, VP = VW + 16;  // LDS row pitches
-  typedef f32x16 State[VT][KT];                    // rows k, lane v
+  typedef f32x16 State[KT];                        // rows k, lane v
 };
 
 template <int K, int V>
@@ -148,25 +151,23 @@ __device__ __forceinline__ void state_io(typename Dims<K, V>::State &S, float *p
   using D = Dims<K, V>;
   const int h = lane >> 5, c = lane & 31;
 #pragma unroll
-  for (int vt = 0; vt < D::VT; ++vt)
+  for (int kt = 0; kt < D::KT; ++kt)
 #pragma unroll
-    for (int kt = 0; kt < D::KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float *e = p + (32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)) * V + 32 * vt + c;
-        if (store)
-          *e = S[vt][kt][i];
-        else
-          S[vt][kt][i] = *e;
-      }
+    for (int i = 0; i < 16; ++i) {
+      float *e = p + (32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)) * V + c;
+      if (store)
+        *e = S[kt][i];
+      else
+        S[kt][i] = *e;
+    }
 }
 
 // OUT: y, from the segment's start state (and the sequence's last state);
 // else a segment's last state from zero and its decay, kept for carry_kernel.
 template <int K, int V, int NW, bool OUT>
-__global__ __launch_bounds__(64 * NW, 1) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
   using D = Dims<K, V>;
-  constexpr int VW = D::VW, VT = D::VT, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
+  constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
   __shared__ __align__(16) bf16 Kl[2][64 * KP], Ql[OUT ? 2 : 1][OUT ? 64 * KP : 8], Vl[NW][64 * VP];
   __shared__ __align__(16) Gates G[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), h2 = lane >> 5, r32 = lane & 31;
@@ -191,16 +192,15 @@ __global__ __launch_bounds__(64 * NW, 1) void mma_kernel(ScanArgs a, Layout w, i
     state_io<K, V>(S, const_cast<float *>(src) + v0, false, lane);
   } else {
 #pragma unroll
-    for (int i = 0; i < VT; ++i)
-#pragma unroll
-      for (int j = 0; j < KT; ++j) S[i][j] = zero16();
+    for (int j = 0; j < KT; ++j) S[j] = zero16();
   }
 
   const int nt = (int)(loc.t1 - loc.t0), nc = (nt + 63) >> 6;
   Rows<K, THREADS> kr, qr;
   Rows<VW, 64> vr;
   float z = 0.f;
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c, int tid) {
+    const int lane = tid & 63;
     const int64_t t = loc.t0 + 64 * (int64_t)c;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     kr.load(bp + t * a.bs, a.bs, rows, tid);
@@ -208,144 +208,114 @@ __global__ __launch_bounds__(64 * NW, 1) void mma_kernel(ScanArgs a, Layout w, i
     vr.load(xp + t * a.xs, a.xs, rows, lane);
     z = lane < rows ? (float)dtp[(t + lane) * a.Hv] : 0.f;
   };
-  auto commit = [&](int buf) {
+  auto commit = [&](int buf, int tid) {
+    const int lane = tid & 63;
     kr.store_pi(Kl[buf], KP, tid);
     if (OUT) qr.store_pi(Ql[buf], KP, tid);
     vr.store_pi(Vl[wave], VP, lane);
   };
   if (nc > 0) {
-    fetch(0);
-    commit(0);
+    fetch(0, tid);
+    commit(0, tid);
   }
   __syncthreads();
   float total = 0.f;
   for (int c = 0; c < nc; ++c) {
+    const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     Gates &g = G[wave];
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
-    if (c + 1 < nc) fetch(c + 1);
+    if (c + 1 < nc) fetch(c + 1, tid);
     const bf16 *k = Kl[c & 1], *q = Ql[OUT ? c & 1 : 0], *v = Vl[wave];
-    bf16x8 vf[VT][4];
-    {
-      const TrA tv(v, VP, lane);
+    bf16x8 vf[4];
+    const TrA tv(v, VP, lane);
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) vf[vt][s] = tv.at(s, vt, VP);
-    }
+    for (int s = 0; s < 4; ++s) vf[s] = tv.at(s, 0, VP);
     if (OUT) {
-      // Y^T = S^T C^T and (B C^T) of the three tiles with j <= i
-      f32x16 Y[2][VT], P00 = zero16(), P01 = zero16(), P11 = zero16();
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) Y[i][vt] = zero16();
-#pragma unroll
-      for (int s = 0; s < K / 16; ++s) {
-        const bf16x8 q0 = lds16(q + r32 * KP + 16 * s + 8 * h2), q1 = lds16(q + (32 + r32) * KP + 16 * s + 8 * h2);
-        const bf16x8 k0 = lds16(k + r32 * KP + 16 * s + 8 * h2), k1 = lds16(k + (32 + r32) * KP + 16 * s + 8 * h2);
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          const bf16x8 sf = slots(S[vt][s >> 1], s & 1);
-          Y[0][vt] = mma32(sf, q0, Y[0][vt]);
-          Y[1][vt] = mma32(sf, q1, Y[1][vt]);
-        }
-        P00 = mma32(k0, q0, P00);
-        P01 = mma32(k0, q1, P01);  // j in the first half, i in the second
-        P11 = mma32(k1, q1, P11);
-      }
-      const float g0 = g.gam[r32], g1 = g.gam[32 + r32];  // of token i in each half
-      const uint32_t f0 = upto(gt.m0, r32), f1 = upto(gt.m1, r32);
-      const float e0 = f0 ? 0.f : exp2_hw(g0), e1 = f1 ? 0.f : exp2_hw(g1), e01 = gt.m0 | f1 ? 0.f : exp2_hw(gt.t0 + g1);
-      const int l0 = last_bit(f0), l1 = last_bit(f1);  // the first token that token i sees
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          Y[0][vt][i] *= e0;
-          Y[1][vt][i] *= e01;
-        }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j0 = 8 * b + 4 * h2;
-        const f32x4 ga = *reinterpret_cast<const f32x4 *>(&g.gam[j0]), de = *reinterpret_cast<const f32x4 *>(&g.del[j0]);
-        const f32x4 gb = *reinterpret_cast<const f32x4 *>(&g.gam[32 + j0]), df = *reinterpret_cast<const f32x4 *>(&g.del[32 + j0]);
-        const f32x4 u = *reinterpret_cast<const f32x4 *>(&g.u[j0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = j0 + i;
-          P00[4 * b + i] = j <= r32 && j >= l0 ? P00[4 * b + i] * (exp2_hw(g0 - ga[i]) * de[i]) : 0.f;
-          P11[4 * b + i] = j <= r32 && j >= l1 ? P11[4 * b + i] * (exp2_hw(g1 - gb[i]) * df[i]) : 0.f;
-          P01[4 * b + i] *= e1 * u[i];
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16x8 p00 = slots(P00, s), p01 = slots(P01, s), p11 = slots(P11, s);
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          Y[0][vt] = mma32(vf[vt][s], p00, Y[0][vt]);
-          Y[1][vt] = mma32(vf[vt][s], p01, Y[1][vt]);
-          Y[1][vt] = mma32(vf[vt][2 + s], p11, Y[1][vt]);
-        }
-      }
-      const int64_t t = loc.t0 + 64 * (int64_t)c;
-      bf16 *yp = static_cast<bf16 *>(a.y) + (t * a.Hv + h) * V + v0;
+      bf16 *yp = static_cast<bf16 *>(a.y) + ((loc.t0 + 64 * (int64_t)c) * a.Hv + h) * V + v0;
       const int64_t ys = (int64_t)a.Hv * V;
       const auto yr = raw_buffer(yp, (uint32_t)(((rows - 1) * ys + VW) * 2));
+      // 32 tokens i at a time: Y^T = S^T C^T and (B C^T) of the tiles with j <= i
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 32 * i + r32;
-        const bf16 *xrow = v + row * VP;
+      for (int it = 0; it < 2; ++it) {
+        f32x16 Y = zero16(), Pd = zero16(), Po = zero16();  // diagonal tile; j in the first half, i in the second
+        const bf16 *qi = q + (32 * it + r32) * KP + 8 * h2, *kd = k + (32 * it + r32) * KP + 8 * h2,
+                   *ko = k + r32 * KP + 8 * h2;
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          uint2 o[4];
+        for (int s = 0; s < K / 16; ++s) {
+          const bf16x8 qf = lds16(qi + 16 * s);
+          Y = mma32(slots(S[s >> 1], s & 1), qf, Y);
+          Pd = mma32(lds16(kd + 16 * s), qf, Pd);
+          if (it) Po = mma32(lds16(ko + 16 * s), qf, Po);
+          if ((s & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        const float gi = g.gam[32 * it + r32];  // of token i, from its half's start
+        const uint32_t f = upto(it ? gt.m1 : gt.m0, r32);
+        const float ei = f ? 0.f : exp2_hw(gi), e0 = it == 0 ? ei : gt.m0 | f ? 0.f : exp2_hw(gt.t0 + gi);
+        const int first = last_bit(f);  // the first token of the half that token i sees
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            // columns 32 vt + 8 b + 4 h: in the pi layout 8 h past those of h = 0
-            const bf16x4 xv = *reinterpret_cast<const bf16x4 *>(xrow + pi_pos(32 * vt + 8 * b) + 8 * h2);
-            bf16x4 r;
+        for (int i = 0; i < 16; ++i) Y[i] *= e0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = (bf16)(Y[i][vt][4 * b + e] + skip * (float)xv[e]);
-            o[b] = __builtin_bit_cast(uint2, r);
-          }
+        for (int b = 0; b < 4; ++b) {
+          const int j0 = 8 * b + 4 * h2;
+          const f32x4 gj = *reinterpret_cast<const f32x4 *>(&g.gam[32 * it + j0]);
+          const f32x4 dj = *reinterpret_cast<const f32x4 *>(&g.del[32 * it + j0]);
+          const f32x4 uj = *reinterpret_cast<const f32x4 *>(&g.u[j0]);
 #pragma unroll
-          for (int b = 0; b < 4; b += 2) {
-            // halves: lanes h = 0 get columns 8 b .. 8 b + 7, lanes h = 1 the next 8
-            const auto p = __builtin_amdgcn_permlane32_swap(o[b].x, o[b + 1].x, false, false);
-            const auto r = __builtin_amdgcn_permlane32_swap(o[b].y, o[b + 1].y, false, false);
-            buf_store16(make_uint4(p[0], r[0], p[1], r[1]), yr,
-                        row < rows ? (uint32_t)(row * ys * 2 + (32 * vt + 8 * b + 8 * h2) * 2) : 0xFFFFFFF0u);
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + i;
+            Pd[4 * b + i] = j <= r32 && j >= first ? Pd[4 * b + i] * (exp2_hw(gi - gj[i]) * dj[i]) : 0.f;
+            if (it) Po[4 * b + i] *= ei * uj[i];
           }
         }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (it) Y = mma32(vf[s], slots(Po, s), Y);
+          Y = mma32(vf[2 * it + s], slots(Pd, s), Y);
+        }
+        const int row = 32 * it + r32;
+        const bf16 *xrow = v + row * VP;
+        uint2 o[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          // columns 8 b + 4 h: in the pi layout 8 h past those of h = 0
+          const bf16x4 xv = *reinterpret_cast<const bf16x4 *>(xrow + pi_pos(8 * b) + 8 * h2);
+          bf16x4 r;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[e] = (bf16)(Y[4 * b + e] + skip * (float)xv[e]);
+          o[b] = __builtin_bit_cast(uint2, r);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; b += 2) {
+          // halves: lanes h = 0 get columns 8 b .. 8 b + 7, lanes h = 1 the next 8
+          const auto p = __builtin_amdgcn_permlane32_swap(o[b].x, o[b + 1].x, false, false);
+          const auto r = __builtin_amdgcn_permlane32_swap(o[b].y, o[b + 1].y, false, false);
+          buf_store16(make_uint4(p[0], r[0], p[1], r[1]), yr,
+                      row < rows ? (uint32_t)(row * ys * 2 + (8 * b + 8 * h2) * 2) : 0xFFFFFFF0u);
+        }
+        // (the second half's reads, moved up into the first, would spill)
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     // S = 2^{gamma_L} S + B^T (w X)
     const float eL = gt.all();
 #pragma unroll
-    for (int vt = 0; vt < VT; ++vt)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) S[vt][kt][i] *= eL;
+      for (int i = 0; i < 16; ++i) S[kt][i] *= eL;
     const TrA tk(k, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      Split x[VT];
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt) x[vt] = split_scaled(vf[vt][s], &g.w[16 * s + 4 * h2]);
+      const Split x = split_scaled(vf[s], &g.w[16 * s + 4 * h2]);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 kf = tk.at(s, kt, KP);
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          S[vt][kt] = mma32(kf, x[vt].hi, S[vt][kt]);
-          S[vt][kt] = mma32(kf, x[vt].lo, S[vt][kt]);
-        }
+        S[kt] = mma32(kf, x.hi, S[kt]);
+        S[kt] = mma32(kf, x.lo, S[kt]);
       }
     }
-    if (c + 1 < nc) commit((c + 1) & 1);
+    if (c + 1 < nc) commit((c + 1) & 1, tid);
     __syncthreads();
   }
   if (!OUT) {
@@ -362,7 +332,9 @@ hipError_t go(const char *name, const ScanArgs &a, const Layout &w, hipStream_t 
   const int nw = slices_per_block(per);
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   KernelTimer kt(name, st);
-  if (nw == 4)
+  if (nw == 8)
+    mma_kernel<K, V, 8, OUT><<<blocks, 512, 0, st>>>(a, w, per / 8);
+  else if (nw == 4)
     mma_kernel<K, V, 4, OUT><<<blocks, 256, 0, st>>>(a, w, per / 4);
   else if (nw == 2)
     mma_kernel<K, V, 2, OUT><<<blocks, 128, 0, st>>>(a, w, per / 2);
