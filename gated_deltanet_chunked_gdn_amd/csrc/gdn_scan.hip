@@ -355,13 +355,39 @@ hipError_t fwd(const ScanArgs &a, hipStream_t st) {
   hipError_t e = hipSuccess;
   const Sweep out{a.x, a.b, a.c, a.xs, a.bs, a.cs, 1, 0, 0, a.V};
   if (!a.one_seg) {
-    e = a.dtype == 1 ? launch_mma_local(a, w, st) : sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
+    e = sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
     carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  return a.dtype == 1 ? launch_mma_out(a, w, st) : sweep<E, kOut>("scan_out", a, w, out, a.K, st);
+  return sweep<E, kOut>("scan_out", a, w, out, a.K, st);
+}
+
+hipError_t fwd_mma(const ScanArgs &a, hipStream_t st) {
+  const Layout w = layout(a, false);
+  if (!a.one_seg) {
+    hipError_t e = launch_mma_local(a, w, st);
+    if (e != hipSuccess) return e;
+    KernelTimer kt("scan_carry", st);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return launch_mma_out(a, w, st);
+}
+
+hipError_t bwd_mma(const ScanArgs &a, hipStream_t st) {
+  const Layout w = layout(a, true);
+  hipError_t e;
+  if ((e = launch_mma_local(a, w, st)) != hipSuccess || (e = launch_mma_rlocal(a, w, st)) != hipSuccess) return e;
+  {
+    KernelTimer kt("scan_carry", st);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
+    rcarry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if ((e = launch_mma_states(a, w, st)) != hipSuccess) return e;
+  return launch_mma_grad(a, w, st);
 }
 
 template <typename E>
@@ -407,7 +433,7 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 
 // Forward segments: as long as the whole sequence unless that leaves compute
 // units without work, then a multiple of 64 tokens that gives about two waves
-// a SIMD over all heads.  Backward: 64 tokens, because the chain of dg
+// a SIMD over all heads.  fp32 backward: 64 tokens, because the chain of dg
 // gathers the rounding of every a_t and r_t since the segment's end: over 256
 // tokens the sums over a head (ddt_bias) were off by 4e-5 of their value.
 ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
@@ -419,21 +445,21 @@ ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
-  seg = bwd ? 64 : (seg + 63) / 64 * 64;
+  seg = bwd && a.dtype != 1 ? 64 : (seg + 63) / 64 * 64;
   if (seg < 64) seg = 64;
   ScanPlan p;
   p.seg = (int)seg;
-  a.slots = p.slots = a.s.cu ? a.s.tokens / seg + a.s.N : a.s.N * scan::segs_of(Span{0, a.s.T}, p.seg);
+  a.slots = p.slots = scan::slots_of(a.s, p.seg);
   a.one_seg = p.one_seg = !bwd && a.s.T <= seg;
   p.ws = scan::layout(a, bwd).total;
   return p;
 }
 
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
-  return a.dtype == 1 ? scan::fwd<bf16>(a, st) : scan::fwd<float>(a, st);
+  return a.dtype == 1 ? scan::fwd_mma(a, st) : scan::fwd<float>(a, st);
 }
 hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
-  return a.dtype == 1 ? scan::bwd<bf16>(a, st) : scan::bwd<float>(a, st);
+  return a.dtype == 1 ? scan::bwd_mma(a, st) : scan::bwd<float>(a, st);
 }
 
 }  // namespace gdn

@@ -1,0 +1,648 @@
+// Backward of the selective scan for bf16 problems, on matrix instructions.
+//
+// With S the state entering a chunk of 64 tokens, Z the gradient of the state
+// leaving it, gamma the log2 decays summed from the chunk's first token,
+// E_ij = 2^{gamma_i - gamma_j}, G_ij = c_i . b_j, M_ij = dy_i . x_j, p_i =
+// 2^{gamma_i}, w_j = 2^{gamma_L - gamma_j}, and all sums over j <= i:
+//
+//   dx_j = delta_j (sum_i E_ij G_ij dy_i + w_j Z^T b_j) + D dy_j
+//   dc_i = sum_heads (sum_j E_ij delta_j M_ij b_j + p_i S dy_i)
+//   db_j = sum_heads delta_j (sum_i E_ij M_ij c_i + w_j Z x_j)
+//   Z_in = 2^{gamma_L} Z + sum_i p_i c_i dy_i^T          (the chunk before's Z)
+//
+// and for the gates, with W_ij = E_ij G_ij M_ij,
+//
+//   a_i = sum_{j < i} W_ij delta_j + p_i c_i . S dy_i
+//   r_j = sum_{i > j} W_ij + w_j b_j . Z x_j,   m_j = W_jj
+//   dg_t = <S', Z> + sum_{s >= t} (a_s - delta_s r_s),  S' the state leaving
+//   d delta_t = r_t + m_t + A dg_t
+//
+// Two kernels share this.  grad_kernel walks a segment's chunks from its end
+// with Z in accumulators (32 columns of a head a wave, as the forward): dx,
+// the gates' sums, and Z of every chunk, rounded to bf16, for the other.
+// pair_kernel has dc and db: one chunk of one head group a workgroup, the
+// heads in turn, so that their sums stay in registers.
+//
+// The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
+// enters them is held to fp32: S and Z as operands in two bf16 parts, G and M
+// from the inputs as they are, <S', Z> afresh in every chunk.  (One part
+// would leave ddt_bias 5e-4 off; <S', Z> carried along over two chunks, 3e-5.)
+// dx, dc and db are bf16 themselves and take their operands rounded.
+#include "gdn_internal.h"
+#include "gdn_scan_mma.hpp"
+
+namespace gdn {
+namespace scan {
+namespace {
+
+// Sum over the 32 lanes of a half of 16 registers each: lane l ends with the
+// sum of register l & 15.
+__device__ __forceinline__ float fold16(float (&r)[16], int lane) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const bool b = lane & 1;
+    r[n] = (b ? r[2 * n + 1] : r[2 * n]) + dpp_mov<0xB1>(b ? r[2 * n] : r[2 * n + 1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const bool b = lane & 2;
+    r[n] = (b ? r[2 * n + 1] : r[2 * n]) + dpp_mov<0x4E>(b ? r[2 * n] : r[2 * n + 1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const bool b = lane & 4;
+    r[n] = (b ? r[2 * n + 1] : r[2 * n]) + __shfl_xor(b ? r[2 * n] : r[2 * n + 1], 4);
+  }
+  const bool b = lane & 8;
+  float v = (b ? r[1] : r[0]) + __shfl_xor(b ? r[0] : r[1], 8);
+  v += __shfl_xor(v, 16);
+  return v;
+}
+
+// fp32 dot product of two bf16x8, added to c
+__device__ __forceinline__ float dot8(const bf16x8 &a, const bf16x8 &b, float c) {
+  return dot_piece<bf16>(__builtin_bit_cast(uint4, a), __builtin_bit_cast(uint4, b), c);
+}
+
+// Token of this lane's tile: sum over the 32 columns of acc (rows column,
+// lane token) times the token's row of a pi-layout matrix.
+__device__ __forceinline__ float row_dot(const f32x16 &acc, const bf16 *row, int h2) {
+  float v = 0.f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const bf16x4 x = *reinterpret_cast<const bf16x4 *>(row + pi_pos(8 * b) + 8 * h2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v += acc[4 * b + e] * (float)x[e];
+  }
+  return v + __shfl_xor(v, 32);
+}
+
+// Writes rows of 32 columns (acc + skip * row of `add`, rows column, lane
+// token) as 16-byte pieces.
+__device__ __forceinline__ void put_rows(const f32x16 &acc, float skip, const bf16 *add, __amdgpu_buffer_rsrc_t out,
+                                         uint32_t off, int h2) {
+  uint2 o[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    bf16x4 x = {};
+    if (add) x = *reinterpret_cast<const bf16x4 *>(add + pi_pos(8 * b) + 8 * h2);
+    bf16x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = (bf16)(acc[4 * b + e] + skip * (float)x[e]);
+    o[b] = __builtin_bit_cast(uint2, r);
+  }
+#pragma unroll
+  for (int b = 0; b < 4; b += 2) {
+    // halves: lanes h = 0 get columns 8 b .. 8 b + 7, lanes h = 1 the next 8
+    const auto p = __builtin_amdgcn_permlane32_swap(o[b].x, o[b + 1].x, false, false);
+    const auto r = __builtin_amdgcn_permlane32_swap(o[b].y, o[b + 1].y, false, false);
+    buf_store16(make_uint4(p[0], r[0], p[1], r[1]), out, off + (off == kOutside ? 0u : (uint32_t)(16 * b + 16 * h2)));
+  }
+}
+
+// The next forgetting token of the half above j (32: none)
+__device__ __forceinline__ int next_bit(uint32_t m) { return m ? __builtin_ctz(m) : 32; }
+
+template <int K, int V, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+  using D = Dims<K, V>;
+  constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
+  __shared__ __align__(16) bf16 Ql[64 * KP], Kl[64 * KP], Xl[NW][64 * VP], Dl[NW][64 * VP];
+  __shared__ __align__(16) Gates G[NW];
+  __shared__ float Sa[NW][64], Sr[NW][64], Sm[NW][64];
+  const int tid0 = threadIdx.x, wave = wave_of(tid0);
+  const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
+  const int blk = (int)(item % blocks_per_group), hq = (int)(item / blocks_per_group % a.Hq);
+  const int64_t slot = item / blocks_per_group / a.Hq;
+  const SlotLoc loc = locate(a, slot);
+  if (!loc.used) return;
+  const int slice = blk * NW + wave;
+  const int h = hq * (a.Hv / a.Hq) + slice * VW / V, v0 = slice * VW % V, vs = v0 / 32;
+  const int64_t kv = (int64_t)K * V, ys = (int64_t)a.Hv * V;
+  const float A2 = a.A[h] * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.D ? a.D[h] : 0.f;
+  const bf16 *cp = static_cast<const bf16 *>(a.c) + hq * K, *bp = static_cast<const bf16 *>(a.b) + hq * K;
+  const bf16 *xp = static_cast<const bf16 *>(a.x) + (int64_t)h * V + v0;
+  const bf16 *dp = static_cast<const bf16 *>(a.dy) + (int64_t)h * V + v0;
+  const bf16 *dtp = static_cast<const bf16 *>(a.dt) + h;
+  const int nt = (int)(loc.t1 - loc.t0), nc = (nt + 63) >> 6;
+  if (nc == 0) return;
+
+  typename D::State Z;
+  state_io<K, V>(Z, w.zend(a) + (slot * a.Hv + h) * kv + v0, false, tid0 & 63);
+  bf16x8 sh[K / 16], sl[K / 16];
+  Rows<K, THREADS> kr, qr;
+  Rows<VW, 64> xr, dr;
+  float z = 0.f;
+  const int64_t first_chunk = w.chunk(a, loc, 0);
+  auto state_at = [&](int c, int lane) {
+    return (((first_chunk + c) * a.Hv + h) * (V / 32) + vs) * (K * 32) + lane * 8;
+  };
+  auto fetch = [&](int c, int tid) {
+    const int lane = tid & 63;
+    const int64_t t = loc.t0 + 64 * (int64_t)c;
+    const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
+    kr.load(bp + t * a.bs, a.bs, rows, tid);
+    qr.load(cp + t * a.cs, a.cs, rows, tid);
+    xr.load(xp + t * a.xs, a.xs, rows, lane);
+    dr.load(dp + t * ys, ys, rows, lane);
+    z = lane < rows ? (float)dtp[(t + lane) * a.Hv] : 0.f;
+    const int64_t at = state_at(c, lane);
+#pragma unroll
+    for (int s = 0; s < K / 16; ++s) {
+      sh[s] = *reinterpret_cast<const bf16x8 *>(w.s_hi(a) + at + s * 512);
+      sl[s] = *reinterpret_cast<const bf16x8 *>(w.s_lo(a) + at + s * 512);
+    }
+  };
+  auto commit = [&](int tid) {
+    const int lane = tid & 63;
+    kr.store_pi(Kl, KP, tid);
+    qr.store_pi(Ql, KP, tid);
+    xr.store_pi(Xl[wave], VP, lane);
+    dr.store_pi(Dl[wave], VP, lane);
+  };
+  fetch(nc - 1, tid0);
+  commit(tid0);
+  __syncthreads();
+  for (int c = nc - 1; c >= 0; --c) {
+    const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
+    const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
+    const int64_t t0 = loc.t0 + 64 * (int64_t)c;
+    Gates &g = G[wave];
+    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
+    const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
+    const float eL = gt.all();
+    // U^T = S^T C^T and Y^T = Z^T B^T (rows v, lane token), <S, Z>, and Z out
+    f32x16 Y[2] = {zero16(), zero16()}, U[2] = {zero16(), zero16()};
+    float xd = 0.f;
+    {
+      const int64_t at = state_at(c, lane);
+      const bf16 *q0 = q + r32 * KP + 8 * h2, *k0 = k + r32 * KP + 8 * h2;
+#pragma unroll
+      for (int s = 0; s < K / 16; ++s) {
+        const Split zf = split(Z[s >> 1], s & 1);
+        *reinterpret_cast<bf16x8 *>(w.z(a) + at + s * 512) = zf.hi;
+        xd = dot8(sh[s], zf.hi, xd);
+        xd = dot8(sh[s], zf.lo, xd);
+        xd = dot8(sl[s], zf.hi, xd);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bf16x8 qf = lds16(q0 + 32 * i * KP + 16 * s), kf = lds16(k0 + 32 * i * KP + 16 * s);
+          U[i] = mma32(sh[s], qf, U[i]);
+          U[i] = mma32(sl[s], qf, U[i]);
+          Y[i] = mma32(zf.hi, kf, Y[i]);
+          Y[i] = mma32(zf.lo, kf, Y[i]);
+        }
+        if (s & 1) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    float xo = wave_sum(xd) * eL;
+    float ri[2];
+    {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 32 * i + r32;
+        const float ai = row_dot(U[i], dy + tok * VP, h2) * g.p[tok];
+        if (h2 == 0) Sa[wave][tok] = ai;
+        ri[i] = row_dot(Y[i], x + tok * VP, h2) * g.w1[tok];
+        sum += ri[i] * g.del[tok];
+      }
+      // (both halves hold the same 32 + 32 values)
+      xo += 0.5f * wave_sum(sum);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    bf16x8 df[4];  // dy^T: lane v, tokens
+    {
+      const TrA td(dy, VP, lane);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) df[s] = td.at(s, 0, VP);
+    }
+    float ar[2][16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ar[0][i] = ar[1][i] = 0.f;
+    float dD = 0.f;
+    const auto out = raw_buffer(static_cast<bf16 *>(a.dx) + (t0 * a.Hv + h) * V + v0, (uint32_t)(((rows - 1) * ys + VW) * 2));
+#pragma unroll
+    for (int jt = 0; jt < 2; ++jt) {
+      const int tj = 32 * jt + r32;  // token j of this lane
+      const float gj = g.gam[tj], dj = g.del[tj];
+      const int lim = next_bit(above(jt ? gt.m1 : gt.m0, r32));  // the first token of the half that no longer sees j
+      f32x16 T = Y[jt];
+      const float wj = g.w1[tj];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) T[i] *= wj;
+      float rs = 0.f, ms = 0.f;
+#pragma unroll
+      for (int it = jt; it < 2; ++it) {
+        f32x16 P = zero16(), M = zero16();
+        const bf16 *qi = q + (32 * it + r32) * KP + 8 * h2, *kj = k + tj * KP + 8 * h2;
+#pragma unroll
+        for (int s = 0; s < K / 16; ++s) P = mma32(lds16(qi + 16 * s), lds16(kj + 16 * s), P);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          M = mma32(lds16(dy + (32 * it + r32) * VP + 8 * h2 + 16 * s), lds16(x + tj * VP + 8 * h2 + 16 * s), M);
+        const float uj = it == jt ? 0.f : g.u1[r32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int i0 = 8 * b + 4 * h2;
+          // rows i: log2 decays (diagonal tile) or decays from the second half's start
+          const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &g.gam[32 * it + i0] : &g.e[i0]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e;
+            float E;
+            if (it == jt)
+              E = i >= r32 && i < lim ? exp2_hw(gi[e] - gj) : 0.f;
+            else
+              E = gi[e] * uj;
+            const float p = P[4 * b + e] * E, wm = p * M[4 * b + e];
+            P[4 * b + e] = p;
+            const bool diag = it == jt && i == r32;
+            if (it == jt) {
+              ms += diag ? wm : 0.f;
+              dD += diag ? M[4 * b + e] : 0.f;
+            }
+            const float wx = diag ? 0.f : wm;
+            rs += wx;
+            ar[it][4 * b + e] += wx * dj;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) T = mma32(df[2 * it + s], slots(P, s), T);
+      }
+      rs += __shfl_xor(rs, 32);
+      ms += __shfl_xor(ms, 32);
+      if (h2 == 0) {
+        Sr[wave][tj] = rs + ri[jt];
+        Sm[wave][tj] = ms;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) T[i] *= dj;
+      put_rows(T, skip, dy + tj * VP, out, tj < rows ? (uint32_t)(tj * ys * 2) : kOutside, h2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const float v = fold16(ar[it], lane);
+      const int i = 32 * it + 8 * ((lane & 15) >> 2) + 4 * h2 + (lane & 3);
+      if (!(lane & 16)) Sa[wave][i] += v;
+    }
+    wave_lds_fence();
+    dD = wave_sum(dD);
+    {
+      const int64_t hs = (int64_t)vs * a.Hv + h;
+      if (lane < rows) {
+        w.a_part(a)[hs * a.s.tokens + t0 + lane] = Sa[wave][lane];
+        w.r_part(a)[hs * a.s.tokens + t0 + lane] = Sr[wave][lane];
+        w.m_part(a)[hs * a.s.tokens + t0 + lane] = Sm[wave][lane];
+      }
+      if (lane == 0) {
+        const int64_t i = ((int64_t)vs * w.chunks + first_chunk + c) * a.Hv + h;
+        w.x_part(a)[i] = xo;
+        w.dd_part(a)[i] = dD;
+      }
+    }
+    if (c > 0) fetch(c - 1, tid);
+    __builtin_amdgcn_sched_barrier(0);
+    // Z = 2^{gamma_L} Z + C^T (p dY)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) Z[kt][i] *= eL;
+    const TrA tq(q, KP, lane);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const Split y = split_scaled(df[s], &g.p[16 * s + 4 * h2]);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const bf16x8 qf = tq.at(s, kt, KP);
+        Z[kt] = mma32(qf, y.hi, Z[kt]);
+        Z[kt] = mma32(qf, y.lo, Z[kt]);
+      }
+    }
+    if (c > 0) {
+      __syncthreads();  // every wave is done with c and b
+      commit(tid);
+      __syncthreads();
+    }
+  }
+}
+
+// dc and db of one chunk and head group.  Waves are (k tile, dc or db), units
+// are 64 (or 32) columns of a head, one after the other; six of the waves also
+// gather sum_heads E delta M, a tile each for every second unit, which meets
+// the tokens of the chunk at the end.
+template <int K, int V>
+struct Pair {
+  static constexpr int KT = K / 32, WAVES = 8, THREADS = 512;
+  static constexpr int UC = V < 64 ? V : 64;  // columns of a unit
+  static constexpr int KP = K + 16, UP = UC + 16, NP = 64 + 16;
+};
+
+template <int K, int V>
+__global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
+  using C = Pair<K, V>;
+  constexpr int KT = C::KT, UC = C::UC, KP = C::KP, UP = C::UP, NP = C::NP, THREADS = C::THREADS;
+  __shared__ __align__(16) bf16 Ql[64 * KP], Kl[64 * KP], Sl[UC * KP], Zl[UC * KP], Xl[64 * UP], Dl[64 * UP];
+  __shared__ __align__(16) bf16 N[2][64 * NP];
+  __shared__ __align__(16) Gates G;
+  __shared__ __align__(16) float Np[3][16][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), h2 = lane >> 5, r32 = lane & 31;
+  const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
+  const int hq = (int)(item % a.Hq);
+  const int64_t slot = item / a.Hq;
+  const SlotLoc loc = locate(a, slot);  // (a.seg = 64 here)
+  const int rows = (int)(loc.t1 - loc.t0);
+  if (!loc.used || rows <= 0) return;
+  const int64_t t0 = loc.t0, ys = (int64_t)a.Hv * V;
+  const int R = a.Hv / a.Hq, units = R * (V / UC);
+
+  Rows<K, THREADS> kr, qr;
+  kr.load(static_cast<const bf16 *>(a.b) + t0 * a.bs + hq * K, a.bs, rows, tid);
+  qr.load(static_cast<const bf16 *>(a.c) + t0 * a.cs + hq * K, a.cs, rows, tid);
+  constexpr int SP = UC * K / 8 / THREADS > 0 ? UC * K / 8 / THREADS : 1;  // state pieces a thread
+  uint4 sr[SP], zr[SP];
+  constexpr int XT = 64 * UC / 8;  // threads that move x and dy pieces
+  static_assert(XT <= THREADS, "one piece a thread");
+  uint4 xr = make_uint4(0, 0, 0, 0), dr = xr;
+  float z = 0.f;
+  auto fetch = [&](int u) {
+    const int h = hq * R + u * UC / V, v0 = u * UC % V;
+    const int64_t st = ((slot * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32);
+#pragma unroll
+    for (int i = 0; i < SP; ++i) {
+      const int pc = tid + i * THREADS;
+      if (pc < UC * K / 8) {
+        sr[i] = *reinterpret_cast<const uint4 *>(w.s_hi(a) + st + pc * 8);
+        zr[i] = *reinterpret_cast<const uint4 *>(w.z(a) + st + pc * 8);
+      }
+    }
+    const int row = tid / (UC / 8), col = tid % (UC / 8);
+    xr = dr = make_uint4(0, 0, 0, 0);
+    if (tid < XT && row < rows) {
+      xr = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.x) + (t0 + row) * a.xs + (int64_t)h * V + v0 + col * 8);
+      dr = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.dy) + (t0 + row) * ys + (int64_t)h * V + v0 + col * 8);
+    }
+    z = lane < rows ? (float)static_cast<const bf16 *>(a.dt)[(t0 + lane) * a.Hv + h] : 0.f;
+  };
+  auto commit = [&] {
+#pragma unroll
+    for (int i = 0; i < SP; ++i) {
+      // piece (column slice, s, lane): column, and its place in the column's row of k
+      const int pc = tid + i * THREADS, l = pc & 63, s = pc / 64 % (K / 16), cs = pc / 64 / (K / 16);
+      if (pc < UC * K / 8) {
+        const int at = (32 * cs + (l & 31)) * KP + 16 * s + 8 * (l >> 5);
+        *reinterpret_cast<uint4 *>(Sl + at) = sr[i];
+        *reinterpret_cast<uint4 *>(Zl + at) = zr[i];
+      }
+    }
+    const int row = tid / (UC / 8), col = tid % (UC / 8);
+    if (tid < XT) {
+      put_pi(Xl + row * UP, col, xr);
+      put_pi(Dl + row * UP, col, dr);
+    }
+  };
+  fetch(0);
+  kr.store_pi(Kl, KP, tid);
+  qr.store_pi(Ql, KP, tid);
+
+  const bool has_out = wave < 2 * KT, is_db = wave >= KT;
+  const int kt = wave % KT;
+  f32x16 acc[2] = {zero16(), zero16()};  // rows k, lane token
+  // wave 0..5: tile (it, jt) of N (rows i, lane j), units of one parity
+  const int nt = wave % 3, it = nt > 0, jt = nt > 1;
+  f32x16 Nacc = zero16();
+  for (int u = 0; u < units; ++u) {
+    const int h = hq * R + u * UC / V;
+    __syncthreads();  // the last unit's reads are done
+    commit();
+    GateTotals gt;
+    if (wave == 0) {
+      const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+      gt = gates(G, z + bias, a.A[h] * kLog2e, a.softplus, lane < rows, lane);
+      if (lane == 0) {
+        Np[0][0][0] = __builtin_bit_cast(float, gt.m0);
+        Np[0][0][1] = __builtin_bit_cast(float, gt.m1);
+      }
+    }
+    __syncthreads();
+    gt.m0 = __builtin_bit_cast(uint32_t, Np[0][0][0]);
+    gt.m1 = __builtin_bit_cast(uint32_t, Np[0][0][1]);
+    if (u + 1 < units) fetch(u + 1);
+    if (has_out) {
+      const TrA ts((is_db ? Zl : Sl), KP, lane);
+      const bf16 *y = (is_db ? Xl : Dl) + r32 * UP + 8 * h2;
+      f32x16 P[2] = {zero16(), zero16()};
+#pragma unroll
+      for (int s = 0; s < UC / 16; ++s) {
+        const bf16x8 sf = ts.at(s, kt, KP);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) P[i] = mma32(sf, lds16(y + 32 * i * UP + 16 * s), P[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f = is_db ? G.w[32 * i + r32] : G.p[32 * i + r32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] += f * P[i][e];
+      }
+    }
+    if (wave < 6 && (u & 1) == (wave >= 3)) {
+      f32x16 M = zero16();
+      const bf16 *yi = Dl + (32 * it + r32) * UP + 8 * h2, *xj = Xl + (32 * jt + r32) * UP + 8 * h2;
+#pragma unroll
+      for (int s = 0; s < UC / 16; ++s) M = mma32(lds16(yi + 16 * s), lds16(xj + 16 * s), M);
+      const float gj = G.gam[32 * jt + r32], dj = G.del[32 * jt + r32], uj = G.u[r32];
+      const int lim = next_bit(above(jt ? gt.m1 : gt.m0, r32));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int i0 = 8 * b + 4 * h2;
+        const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &G.gam[32 * it + i0] : &G.e[i0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = i0 + e;
+          float E;
+          if (it == jt)
+            E = i >= r32 && i < lim ? exp2_hw(gi[e] - gj) * dj : 0.f;
+          else
+            E = gi[e] * uj;
+          Nacc[4 * b + e] += E * M[4 * b + e];
+        }
+      }
+    }
+  }
+  // N of all heads, rounded to bf16, by rows i and by rows j
+  __syncthreads();
+  if (wave >= 3 && wave < 6) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) Np[nt][e][lane] = Nacc[e];
+  }
+  for (int i = tid; i < 32 * NP; i += THREADS) {  // the tile with j > i
+    N[0][i] = (bf16)0.f;
+    N[1][32 * NP + i] = (bf16)0.f;
+  }
+  __syncthreads();
+  if (wave < 3) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      bf16x4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = Nacc[4 * b + e] + Np[nt][4 * b + e][lane];
+        r[e] = (bf16)v;
+        const int i = 32 * it + 8 * b + 4 * h2 + e, j = 32 * jt + r32;
+        // N[0]: rows i, position of j in the pi layout
+        N[0][i * NP + pi_pos(j & ~3) + (j & 3)] = r[e];
+      }
+      // N[1]: rows j, four consecutive i
+      *reinterpret_cast<bf16x4 *>(&N[1][(32 * jt + r32) * NP + pi_pos(32 * it + 8 * b) + 8 * h2]) = r;
+    }
+  }
+  __syncthreads();
+  if (!has_out) return;
+  // dc^T += B^T N^T (lane i, over j <= i); db^T += C^T N (lane j, over i >= j)
+  const TrA tb(is_db ? Ql : Kl, KP, lane);
+  const bf16 *nr = N[is_db ? 1 : 0] + r32 * NP + 8 * h2;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const bf16x8 f = tb.at(s, kt, KP);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc[i] = mma32(f, lds16(nr + 32 * i * NP + 16 * s), acc[i]);
+  }
+  bf16 *dst = static_cast<bf16 *>(is_db ? a.db : a.dc) + (t0 * a.Hq + hq) * K + 32 * kt;
+  const int64_t qs = (int64_t)a.Hq * K;
+  const auto out = raw_buffer(dst, (uint32_t)(((rows - 1) * qs + 32) * 2));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int tok = 32 * i + r32;
+    put_rows(acc[i], 0.f, nullptr, out, tok < rows ? (uint32_t)(tok * qs * 2) : kOutside, h2);
+  }
+}
+
+// The gates of one chunk and head: dg from the chunk's <S', Z> and its a, r,
+// then ddt and the chunk's parts of dA, ddt_bias, dD.  Lanes are tokens, lane
+// 0 the last.
+__global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + wave_of(threadIdx.x);
+  const int h = (int)(unit % a.Hv);
+  const int64_t slot = unit / a.Hv;
+  if (slot >= w.chunks) return;
+  const SlotLoc loc = locate(a, slot);  // (a.seg = 64 here)
+  float *part = w.head_part(a) + (slot * a.Hv + h) * 3;
+  const int rows = (int)(loc.t1 - loc.t0);
+  if (!loc.used || rows <= 0) {
+    if (lane < 3) part[lane] = 0.f;
+    return;
+  }
+  const int slices = a.V / 32;
+  const bool on = lane < rows;
+  const int64_t t = loc.t1 - 1 - (on ? lane : 0);
+  float av = 0.f, rv = 0.f, mv = 0.f, x = 0.f, dD = 0.f;
+  for (int s = 0; s < slices; ++s) {
+    const int64_t i = ((int64_t)s * a.Hv + h) * a.s.tokens + t;
+    av += w.a_part(a)[i];
+    rv += w.r_part(a)[i];
+    mv += w.m_part(a)[i];
+    const int64_t j = ((int64_t)s * w.chunks + slot) * a.Hv + h;
+    x += w.x_part(a)[j];
+    dD += w.dd_part(a)[j];
+  }
+  const float A = a.A[h];
+  const float z = (float)static_cast<const bf16 *>(a.dt)[t * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
+  const float delta = a.softplus ? softplusf(z) : z;
+  // dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 to fp32 where the token forgets all,
+  // and the chain begins again there: delta_t r_t, large where delta_t is,
+  // leaves no rounding behind.
+  int cut = on && delta * A * kLog2e < kForget;
+  float dg = cut || !on ? 0.f : av - delta * rv;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const float below = __shfl_up(dg, d);
+    const int cut_below = __shfl_up(cut, d);
+    if (lane >= d && !cut) {
+      dg += below;
+      cut = cut_below;
+    }
+  }
+  if (!cut) dg += x;
+  float dd = rv + mv + A * dg;
+  if (a.softplus) dd *= 1.f / (1.f + expf(-z));
+  if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)dd;
+  const float dA = wave_sum(on ? delta * dg : 0.f), dbias = wave_sum(on ? dd : 0.f);
+  if (lane == 0) {
+    part[0] = dA;
+    part[1] = dbias;
+    part[2] = dD;
+  }
+}
+
+// dA, ddt_bias, dD of a head: the chunks' parts in a fixed order.
+__global__ __launch_bounds__(256) void chunk_heads_kernel(ScanArgs a, Layout w) {
+  __shared__ float red[3][4];
+  const int h = blockIdx.x, lane = threadIdx.x & 63;
+  float v[3] = {0.f, 0.f, 0.f};
+  for (int64_t s = threadIdx.x; s < w.chunks; s += 256)
+    for (int k = 0; k < 3; ++k) v[k] += w.head_part(a)[(s * a.Hv + h) * 3 + k];
+  for (int k = 0; k < 3; ++k) {
+    const float t = wave_sum(v[k]);
+    if (lane == 0) red[k][threadIdx.x >> 6] = t;
+  }
+  __syncthreads();
+  float *out[3] = {a.dA, a.ddt_bias, a.dD};
+  if (threadIdx.x < 3 && out[threadIdx.x]) {
+    const float *r = red[threadIdx.x];
+    out[threadIdx.x][h] = (r[0] + r[1]) + (r[2] + r[3]);
+  }
+}
+
+template <int K, int V>
+hipError_t go(const ScanArgs &a, const Layout &w, hipStream_t st) {
+  const int per = a.Hv / a.Hq * (V / 32);  // column slices of a group
+  const int nw = slices_per_block(per);
+  const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
+  {
+    KernelTimer kt("scan_grad", st);
+    if (nw == 8)
+      grad_kernel<K, V, 8><<<blocks, 512, 0, st>>>(a, w, per / 8);
+    else if (nw == 4)
+      grad_kernel<K, V, 4><<<blocks, 256, 0, st>>>(a, w, per / 4);
+    else if (nw == 2)
+      grad_kernel<K, V, 2><<<blocks, 128, 0, st>>>(a, w, per / 2);
+    else
+      grad_kernel<K, V, 1><<<blocks, 64, 0, st>>>(a, w, per);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  ScanArgs c = a;
+  c.seg = 64;
+  c.slots = w.chunks;
+  {
+    KernelTimer kt("scan_pair", st);
+    pair_kernel<K, V><<<(unsigned)(w.chunks * a.Hq), 512, 0, st>>>(c, w);
+  }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  KernelTimer kt("scan_gates", st);
+  chunk_gates_kernel<<<(unsigned)((w.chunks * a.Hv + 3) / 4), 256, 0, st>>>(c, w);
+  chunk_heads_kernel<<<a.Hv, 256, 0, st>>>(c, w);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mma_grad(const ScanArgs &a, const Layout &w, hipStream_t st) {
+  switch (a.K * 1000 + a.V) {
+    case 32032: return go<32, 32>(a, w, st);
+    case 32064: return go<32, 64>(a, w, st);
+    case 32128: return go<32, 128>(a, w, st);
+    case 64032: return go<64, 32>(a, w, st);
+    case 64064: return go<64, 64>(a, w, st);
+    case 64128: return go<64, 128>(a, w, st);
+    case 128032: return go<128, 32>(a, w, st);
+    case 128064: return go<128, 64>(a, w, st);
+    default: return go<128, 128>(a, w, st);
+  }
+}
+
+}  // namespace scan
+}  // namespace gdn

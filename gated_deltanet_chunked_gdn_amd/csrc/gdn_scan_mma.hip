@@ -24,148 +24,23 @@
 // The state is held to fp32: its update takes b as it is and the weighted x
 // as the sum of two bf16 parts (2^-18 of it is lost).
 #include "gdn_internal.h"
-#include "gdn_scan.hpp"
-#include "gdn_slice.hpp"
+#include "gdn_scan_mma.hpp"
 
 namespace gdn {
 namespace scan {
 namespace {
 
-using slice::f32x16;
-using slice::lds16;
-using slice::mma32;
-using slice::pi_pos;
-using slice::put_pi;
-using slice::slots;
-using slice::TrA;
-using slice::zero16;
+// What a pass over a segment's chunks does:
+//   kLocal   the segment's last state from zero and its decay (for carry_kernel)
+//   kOut     y, from the segment's start state, and the sequence's last state
+//   kStates  the state entering every chunk, as two bf16 parts (backward)
+//   kRLocal  reverse: the gradient of the segment's first state from its own
+//            outputs; a.b, a.x hold c and dy: Z = 2^{gamma_L} Z + C^T (2^{gamma} dY)
+enum { kLocal, kOut, kStates, kRLocal };
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Inclusive prefix sums inside each half (32 lanes) of the wave.
-__device__ __forceinline__ float half_incl_scan(float x) {
-  x += dpp_mov<0x111>(x);       // row_shr:1
-  x += dpp_mov<0x112>(x);       // row_shr:2
-  x += dpp_mov<0x114>(x);       // row_shr:4
-  x += dpp_mov<0x118>(x);       // row_shr:8
-  x += dpp_mov<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
-  return x;
-}
-__device__ __forceinline__ float lane_f(float x, int l) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
-}
-
-// Pieces of 16 bytes of one chunk's rows (64 x COLS bf16) in the registers of
-// THREADS threads; rows past the sequence read as zeros.
-template <int COLS, int THREADS>
-struct Rows {
-  static constexpr int N = 64 * COLS / 8 / THREADS;
-  uint4 r[N];
-  __device__ __forceinline__ void load(const bf16 *p, int64_t stride, int rows, int tid) {
-    const uint32_t bytes = rows > 0 ? (uint32_t)(((rows - 1) * stride + COLS) * 2) : 0u;
-    const auto rsrc = raw_buffer(p, bytes);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int pc = tid + i * THREADS, row = pc / (COLS / 8), col = pc % (COLS / 8);
-      // (a row past the end may still lie inside the byte range of the last
-      // row's neighbours in a wider tensor: it is sent past the range)
-      r[i] = buf_load16(rsrc, row < rows ? (uint32_t)(row * stride * 2 + col * 16) : 0xFFFFFFF0u);
-    }
-  }
-  __device__ __forceinline__ void store_pi(bf16 *lds, int pitch, int tid) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int pc = tid + i * THREADS, row = pc / (COLS / 8), col = pc % (COLS / 8);
-      put_pi(lds + row * pitch, col, r[i]);
-    }
-  }
-};
-
-// What a wave keeps of a chunk's steps in LDS, by token: log2 decays summed
-// from the token's half (32 tokens), delta, the weight of the token in the
-// chunk's last state, and (first half) in the half's last state.
-//
-// A token whose own decay is below 2^kForget ends all that is before it to
-// fp32 (2^-27 of a term is an eighth of its half step).  It counts as an
-// exact 0 and stays out of the sums, where it would cost the differences
-// between later tokens their digits; m0, m1 mark such tokens of the halves.
-constexpr float kForget = -27.f;
-struct Gates {
-  float gam[64], del[64], w[64], u[32];
-};
-struct GateTotals {
-  float t0, t1;     // the halves' sums of log2 decays
-  uint32_t m0, m1;  // tokens that forget
-  __device__ __forceinline__ float all() const { return m0 | m1 ? 0.f : exp2_hw(t0 + t1); }
-};
-// bits 0 .. i, and the bits above i
-__device__ __forceinline__ uint32_t upto(uint32_t m, int i) { return m & (0xFFFFFFFFu >> (31 - i)); }
-__device__ __forceinline__ uint32_t above(uint32_t m, int i) { return m & ~(0xFFFFFFFFu >> (31 - i)); }
-__device__ __forceinline__ int last_bit(uint32_t m) { return m ? 31 - __builtin_clz(m) : 0; }
-
-__device__ __forceinline__ GateTotals gates(Gates &s, float z, float A2, bool softplus, bool live, int lane) {
-  const float d = live ? (softplus ? softplusf(z) : z) : 0.f;
-  const float g = d * A2;
-  const bool cut = g < kForget;
-  const unsigned long long m = __ballot(cut);
-  const float gam = half_incl_scan(cut ? 0.f : g);
-  GateTotals t{lane_f(gam, 31), lane_f(gam, 63), (uint32_t)m, (uint32_t)(m >> 32)};
-  const int i = lane & 31;
-  const uint32_t later = lane < 32 ? above(t.m0, i) : above(t.m1, i);
-  s.gam[lane] = gam;
-  s.del[lane] = d;
-  s.w[lane] = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? (t.t0 - gam) + t.t1 : t.t1 - gam) * d;
-  if (lane < 32) s.u[lane] = later ? 0.f : exp2_hw(t.t0 - gam) * d;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  return t;
-}
-
-// bf16 parts hi + lo of x[e] * w[e]
-struct Split {
-  bf16x8 hi, lo;
-};
-__device__ __forceinline__ Split split_scaled(const bf16x8 &x, const float *w) {
-  const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w), w1 = *reinterpret_cast<const f32x4 *>(w + 8);
-  Split r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float f = (float)x[e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
-    r.hi[e] = (bf16)f;
-    r.lo[e] = (bf16)(f - (float)r.hi[e]);
-  }
-  return r;
-}
-
-template <int K, int V>
-struct Dims {
-  static constexpr int VW = 32, KT = K / 32;
-  static constexpr int KP = K + 16, VP = VW + 16;  // LDS row pitches
-  typedef f32x16 State[KT];                        // rows k, lane v
-};
-
-template <int K, int V>
-__device__ __forceinline__ void state_io(typename Dims<K, V>::State &S, float *p, bool store, int lane) {
-  using D = Dims<K, V>;
-  const int h = lane >> 5, c = lane & 31;
-#pragma unroll
-  for (int kt = 0; kt < D::KT; ++kt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float *e = p + (32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)) * V + c;
-      if (store)
-        *e = S[kt][i];
-      else
-        S[kt][i] = *e;
-    }
-}
-
-// OUT: y, from the segment's start state (and the sequence's last state);
-// else a segment's last state from zero and its decay, kept for carry_kernel.
-template <int K, int V, int NW, bool OUT>
+template <int K, int V, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+  constexpr bool OUT = MODE == kOut, REV = MODE == kRLocal;
   using D = Dims<K, V>;
   constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
   __shared__ __align__(16) bf16 Kl[2][64 * KP], Ql[OUT ? 2 : 1][OUT ? 64 * KP : 8], Vl[NW][64 * VP];
@@ -175,7 +50,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
   const int blk = (int)(item % blocks_per_group), hq = (int)(item / blocks_per_group % a.Hq);
   const int64_t slot = item / blocks_per_group / a.Hq;
   const SlotLoc loc = locate(a, slot);
-  if (!loc.used || (!OUT && loc.last && !w.need_last)) return;
+  if (!loc.used || (MODE == kLocal && loc.last && !w.need_last)) return;
   const int slice = blk * NW + wave;  // of the group's columns
   const int h = hq * (a.Hv / a.Hq) + slice * VW / V, v0 = slice * VW % V;
   const int64_t kv = (int64_t)K * V;
@@ -188,6 +63,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
   const float *src = nullptr;
   if (OUT)
     src = a.one_seg ? (a.h0 ? a.h0 + (loc.n * (int64_t)a.Hv + h) * kv : nullptr) : w.start(a) + (slot * a.Hv + h) * kv;
+  if (MODE == kStates) src = w.start(a) + (slot * a.Hv + h) * kv;
   if (src) {
     state_io<K, V>(S, const_cast<float *>(src) + v0, false, lane);
   } else {
@@ -199,8 +75,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
   Rows<K, THREADS> kr, qr;
   Rows<VW, 64> vr;
   float z = 0.f;
-  auto fetch = [&](int c, int tid) {
-    const int lane = tid & 63;
+  auto fetch = [&](int step, int tid) {
+    const int lane = tid & 63, c = REV ? nc - 1 - step : step;
     const int64_t t = loc.t0 + 64 * (int64_t)c;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     kr.load(bp + t * a.bs, a.bs, rows, tid);
@@ -220,14 +96,24 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
   }
   __syncthreads();
   float total = 0.f;
-  for (int c = 0; c < nc; ++c) {
+  for (int step = 0; step < nc; ++step) {
+    const int c = REV ? nc - 1 - step : step;
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     Gates &g = G[wave];
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
-    if (c + 1 < nc) fetch(c + 1, tid);
-    const bf16 *k = Kl[c & 1], *q = Ql[OUT ? c & 1 : 0], *v = Vl[wave];
+    if (step + 1 < nc) fetch(step + 1, tid);
+    const bf16 *k = Kl[step & 1], *q = Ql[OUT ? step & 1 : 0], *v = Vl[wave];
+    if (MODE == kStates) {
+      const int64_t at = ((w.chunk(a, loc, c) * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32) + lane * 8;
+#pragma unroll
+      for (int s = 0; s < K / 16; ++s) {
+        const Split x = split(S[s >> 1], s & 1);
+        *reinterpret_cast<bf16x8 *>(w.s_hi(a) + at + s * 512) = x.hi;
+        *reinterpret_cast<bf16x8 *>(w.s_lo(a) + at + s * 512) = x.lo;
+      }
+    }
     bf16x8 vf[4];
     const TrA tv(v, VP, lane);
 #pragma unroll
@@ -292,7 +178,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
           const auto p = __builtin_amdgcn_permlane32_swap(o[b].x, o[b + 1].x, false, false);
           const auto r = __builtin_amdgcn_permlane32_swap(o[b].y, o[b + 1].y, false, false);
           buf_store16(make_uint4(p[0], r[0], p[1], r[1]), yr,
-                      row < rows ? (uint32_t)(row * ys * 2 + (8 * b + 8 * h2) * 2) : 0xFFFFFFF0u);
+                      row < rows ? (uint32_t)(row * ys * 2 + (8 * b + 8 * h2) * 2) : kOutside);
         }
         // (the second half's reads, moved up into the first, would spill)
         __builtin_amdgcn_sched_barrier(0);
@@ -307,7 +193,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     const TrA tk(k, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const Split x = split_scaled(vf[s], &g.w[16 * s + 4 * h2]);
+      const Split x = split_scaled(vf[s], (REV ? g.p : g.w) + 16 * s + 4 * h2);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 kf = tk.at(s, kt, KP);
@@ -315,55 +201,68 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
         S[kt] = mma32(kf, x.lo, S[kt]);
       }
     }
-    if (c + 1 < nc) commit((c + 1) & 1, tid);
+    if (step + 1 < nc) commit((step + 1) & 1, tid);
     __syncthreads();
   }
-  if (!OUT) {
-    state_io<K, V>(S, w.start(a) + (slot * a.Hv + h) * kv + v0, true, lane);
-    if (lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
-  } else if (a.ht && loc.last) {
+  if (MODE == kLocal || REV) {
+    if (REV && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
+    float *dst = (REV ? w.zend(a) : w.start(a)) + (slot * a.Hv + h) * kv + v0;
+    state_io<K, V>(S, dst, true, lane);
+    if (MODE == kLocal && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
+  } else if (OUT && a.ht && loc.last) {
     state_io<K, V>(S, a.ht + (loc.n * (int64_t)a.Hv + h) * kv + v0, true, lane);
   }
 }
 
-template <int K, int V, bool OUT>
+template <int K, int V, int MODE>
 hipError_t go(const char *name, const ScanArgs &a, const Layout &w, hipStream_t st) {
   const int per = a.Hv / a.Hq * (V / Dims<K, V>::VW);  // column slices of a group
   const int nw = slices_per_block(per);
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   KernelTimer kt(name, st);
   if (nw == 8)
-    mma_kernel<K, V, 8, OUT><<<blocks, 512, 0, st>>>(a, w, per / 8);
+    mma_kernel<K, V, 8, MODE><<<blocks, 512, 0, st>>>(a, w, per / 8);
   else if (nw == 4)
-    mma_kernel<K, V, 4, OUT><<<blocks, 256, 0, st>>>(a, w, per / 4);
+    mma_kernel<K, V, 4, MODE><<<blocks, 256, 0, st>>>(a, w, per / 4);
   else if (nw == 2)
-    mma_kernel<K, V, 2, OUT><<<blocks, 128, 0, st>>>(a, w, per / 2);
+    mma_kernel<K, V, 2, MODE><<<blocks, 128, 0, st>>>(a, w, per / 2);
   else
-    mma_kernel<K, V, 1, OUT><<<blocks, 64, 0, st>>>(a, w, per);
+    mma_kernel<K, V, 1, MODE><<<blocks, 64, 0, st>>>(a, w, per);
   return hipGetLastError();
 }
-template <bool OUT>
+template <int MODE>
 hipError_t pick(const char *name, const ScanArgs &a, const Layout &w, hipStream_t st) {
   switch (a.K * 1000 + a.V) {
-    case 32032: return go<32, 32, OUT>(name, a, w, st);
-    case 32064: return go<32, 64, OUT>(name, a, w, st);
-    case 32128: return go<32, 128, OUT>(name, a, w, st);
-    case 64032: return go<64, 32, OUT>(name, a, w, st);
-    case 64064: return go<64, 64, OUT>(name, a, w, st);
-    case 64128: return go<64, 128, OUT>(name, a, w, st);
-    case 128032: return go<128, 32, OUT>(name, a, w, st);
-    case 128064: return go<128, 64, OUT>(name, a, w, st);
-    default: return go<128, 128, OUT>(name, a, w, st);
+    case 32032: return go<32, 32, MODE>(name, a, w, st);
+    case 32064: return go<32, 64, MODE>(name, a, w, st);
+    case 32128: return go<32, 128, MODE>(name, a, w, st);
+    case 64032: return go<64, 32, MODE>(name, a, w, st);
+    case 64064: return go<64, 64, MODE>(name, a, w, st);
+    case 64128: return go<64, 128, MODE>(name, a, w, st);
+    case 128032: return go<128, 32, MODE>(name, a, w, st);
+    case 128064: return go<128, 64, MODE>(name, a, w, st);
+    default: return go<128, 128, MODE>(name, a, w, st);
   }
 }
 
 }  // namespace
 
 hipError_t launch_mma_local(const ScanArgs &a, const Layout &w, hipStream_t st) {
-  return pick<false>("scan_local", a, w, st);
+  return pick<kLocal>("scan_local", a, w, st);
 }
 hipError_t launch_mma_out(const ScanArgs &a, const Layout &w, hipStream_t st) {
-  return pick<true>("scan_out", a, w, st);
+  return pick<kOut>("scan_out", a, w, st);
+}
+hipError_t launch_mma_states(const ScanArgs &a, const Layout &w, hipStream_t st) {
+  return pick<kStates>("scan_states", a, w, st);
+}
+hipError_t launch_mma_rlocal(const ScanArgs &a0, const Layout &w, hipStream_t st) {
+  ScanArgs a = a0;
+  a.b = a0.c;
+  a.bs = a0.cs;
+  a.x = a0.dy;
+  a.xs = (int64_t)a.Hv * a.V;
+  return pick<kRLocal>("scan_rlocal", a, w, st);
 }
 
 }  // namespace scan

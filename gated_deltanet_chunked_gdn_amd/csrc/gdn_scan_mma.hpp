@@ -1,0 +1,174 @@
+// Pieces shared by the selective scan's matrix kernels (forward and local
+// passes in gdn_scan_mma.hip, the backward in gdn_scan_bwd.hip).
+#pragma once
+
+#include "gdn_scan.hpp"
+#include "gdn_slice.hpp"
+
+namespace gdn {
+namespace scan {
+
+using slice::f32x16;
+using slice::lds16;
+using slice::mma32;
+using slice::pi_pos;
+using slice::put_pi;
+using slice::slots;
+using slice::TrA;
+using slice::zero16;
+
+// A byte offset that lies past every buffer: loads read 0, stores are dropped.
+constexpr uint32_t kOutside = 0xFFFFFFF0u;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Inclusive prefix sums inside each half (32 lanes) of the wave.
+__device__ __forceinline__ float half_incl_scan(float x) {
+  x += dpp_mov<0x111>(x);       // row_shr:1
+  x += dpp_mov<0x112>(x);       // row_shr:2
+  x += dpp_mov<0x114>(x);       // row_shr:4
+  x += dpp_mov<0x118>(x);       // row_shr:8
+  x += dpp_mov<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+  return x;
+}
+__device__ __forceinline__ float lane_f(float x, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
+}
+
+// Pieces of 16 bytes of one chunk's rows (64 x COLS bf16) in the registers of
+// THREADS threads; rows past the sequence read as zeros.
+template <int COLS, int THREADS>
+struct Rows {
+  static constexpr int PIECES = 64 * COLS / 8;
+  static constexpr int N = (PIECES + THREADS - 1) / THREADS;
+  uint4 r[N];
+  __device__ __forceinline__ void load(const bf16 *p, int64_t stride, int rows, int tid) {
+    const uint32_t bytes = rows > 0 ? (uint32_t)(((rows - 1) * stride + COLS) * 2) : 0u;
+    const auto rsrc = raw_buffer(p, bytes);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = tid + i * THREADS, row = pc / (COLS / 8), col = pc % (COLS / 8);
+      // (a row past the end may still lie inside the byte range of the last
+      // row's neighbours in a wider tensor: it is sent past the range)
+      // (so are pieces past the chunk's, where THREADS are more)
+      r[i] = buf_load16(rsrc, row < rows ? (uint32_t)(row * stride * 2 + col * 16) : kOutside);
+    }
+  }
+  __device__ __forceinline__ void store_pi(bf16 *lds, int pitch, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = tid + i * THREADS, row = pc / (COLS / 8), col = pc % (COLS / 8);
+      if (PIECES % THREADS == 0 || pc < PIECES) put_pi(lds + row * pitch, col, r[i]);
+    }
+  }
+};
+
+// LDS written by a wave is read by other lanes of it after this.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+// What a wave keeps of a chunk's steps in LDS, by token: log2 decays summed
+// from the token's half (32 tokens), delta, the decay from the token to the
+// chunk's last (w1) and times delta (w), that of the first half's tokens to
+// the half's last (u1) and times delta (u), from the second half's first token
+// to its tokens (e), and from the chunk's first token to the token (p).
+//
+// A token whose own decay is below 2^kForget ends all that is before it to
+// fp32 (2^-27 of a term is an eighth of its half step).  It counts as an
+// exact 0 and stays out of the sums, where it would cost the differences
+// between later tokens their digits; m0, m1 mark such tokens of the halves.
+constexpr float kForget = -27.f;
+struct Gates {
+  float gam[64], del[64], w[64], w1[64], p[64], u[32], u1[32], e[32];
+};
+struct GateTotals {
+  float t0, t1;     // the halves' sums of log2 decays
+  uint32_t m0, m1;  // tokens that forget
+  __device__ __forceinline__ float all() const { return m0 | m1 ? 0.f : exp2_hw(t0 + t1); }
+};
+// bits 0 .. i, and the bits above i
+__device__ __forceinline__ uint32_t upto(uint32_t m, int i) { return m & (0xFFFFFFFFu >> (31 - i)); }
+__device__ __forceinline__ uint32_t above(uint32_t m, int i) { return m & ~(0xFFFFFFFFu >> (31 - i)); }
+__device__ __forceinline__ int last_bit(uint32_t m) { return m ? 31 - __builtin_clz(m) : 0; }
+
+__device__ __forceinline__ GateTotals gates(Gates &s, float z, float A2, bool softplus, bool live, int lane) {
+  const float d = live ? (softplus ? softplusf(z) : z) : 0.f;
+  const float g = d * A2;
+  const bool cut = g < kForget;
+  const unsigned long long m = __ballot(cut);
+  const float gam = half_incl_scan(cut ? 0.f : g);
+  GateTotals t{lane_f(gam, 31), lane_f(gam, 63), (uint32_t)m, (uint32_t)(m >> 32)};
+  const int i = lane & 31;
+  const uint32_t later = lane < 32 ? above(t.m0, i) : above(t.m1, i);
+  s.gam[lane] = gam;
+  s.del[lane] = d;
+  const uint32_t before = upto(lane < 32 ? t.m0 : t.m1, i) | (lane < 32 ? 0u : t.m0);
+  s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam : t.t0 + gam);
+  const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? (t.t0 - gam) + t.t1 : t.t1 - gam);
+  s.w1[lane] = w1;
+  s.w[lane] = w1 * d;
+  if (lane < 32) {
+    const float u1 = later ? 0.f : exp2_hw(t.t0 - gam);
+    s.u1[lane] = u1;
+    s.u[lane] = u1 * d;
+  } else {
+    s.e[lane - 32] = upto(t.m1, i) ? 0.f : exp2_hw(gam);
+  }
+  wave_lds_fence();
+  return t;
+}
+
+// bf16 parts hi + lo of x[e] * w[e]
+struct Split {
+  bf16x8 hi, lo;
+};
+__device__ __forceinline__ Split split_scaled(const bf16x8 &x, const float *w) {
+  const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w), w1 = *reinterpret_cast<const f32x4 *>(w + 8);
+  Split r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float f = (float)x[e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
+    r.hi[e] = (bf16)f;
+    r.lo[e] = (bf16)(f - (float)r.hi[e]);
+  }
+  return r;
+}
+
+// bf16 parts of operand slots 8 s .. 8 s + 7 of an accumulator tile
+__device__ __forceinline__ Split split(const f32x16 &x, int s) {
+  Split r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    r.hi[e] = (bf16)x[8 * s + e];
+    r.lo[e] = (bf16)(x[8 * s + e] - (float)r.hi[e]);
+  }
+  return r;
+}
+
+template <int K, int V>
+struct Dims {
+  static constexpr int VW = 32, KT = K / 32;
+  static constexpr int KP = K + 16, VP = VW + 16;  // LDS row pitches
+  typedef f32x16 State[KT];                        // rows k, lane v
+};
+
+template <int K, int V>
+__device__ __forceinline__ void state_io(typename Dims<K, V>::State &S, float *p, bool store, int lane) {
+  using D = Dims<K, V>;
+  const int h = lane >> 5, c = lane & 31;
+#pragma unroll
+  for (int kt = 0; kt < D::KT; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float *e = p + (32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)) * V + c;
+      if (store)
+        *e = S[kt][i];
+      else
+        S[kt][i] = *e;
+    }
+}
+
+}  // namespace scan
+}  // namespace gdn

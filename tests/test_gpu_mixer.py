@@ -157,6 +157,8 @@ SCANS = [
     ("f32", 1, 0, 2, 2, 64, 32, [0, 1, 64, 90], True, True, True, True),
     ("f32", 2, 33, 1, 3, 64, 64, None, False, False, True, False),
     ("bf16", 1, 1100, 1, 2, 64, 32, None, True, True, True, True),
+    ("bf16", 1, 150, 2, 8, 32, 64, None, True, True, True, True),
+    ("bf16", 1, 0, 1, 3, 32, 32, [64, 0, 2, 31], False, True, True, False),
 ]
 
 
