@@ -285,18 +285,15 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, Geo g) {
 }
 
 // dw, dbias: the partials of all workgroups, added in order.
-__global__ __launch_bounds__(kThreads) void conv_sum_kernel(ConvArgs a, int64_t tiles) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t n = (int64_t)(a.W + 1) * a.D;
-  if (i >= n) return;
-  float v = 0.f;
-  for (int64_t t = 0; t < tiles; ++t) v += a.partial[t * n + i];
-  const int j = (int)(i / a.D);
-  const int64_t c = i % a.D;
-  if (j < a.W)
-    store_w(a.dw, c * a.W + j, v, a.wdtype);
-  else if (a.db)
-    store_w(a.db, c, v, a.wdtype);
+__global__ __launch_bounds__(kSumThreads) void conv_sum_kernel(ConvArgs a, int64_t tiles) {
+  sum_parts(a.partial, tiles, (int64_t)(a.W + 1) * a.D, [&](int64_t i, float v) {
+    const int j = (int)(i / a.D);
+    const int64_t c = i % a.D;
+    if (j < a.W)
+      store_w(a.dw, c * a.W + j, v, a.wdtype);
+    else if (a.db)
+      store_w(a.db, c, v, a.wdtype);
+  });
 }
 
 // One token: y from the state's rows and x, the state moved on by one row.
@@ -410,7 +407,7 @@ struct GoBwd {
     }
     KernelTimer kt("conv_bwd_sum", st);
     const int64_t n = (int64_t)(W + 1) * a.D;
-    conv_sum_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, g.tiles);
+    conv_sum_kernel<<<sum_blocks(n), kSumThreads, 0, st>>>(a, g.tiles);
     return hipGetLastError();
   }
 };

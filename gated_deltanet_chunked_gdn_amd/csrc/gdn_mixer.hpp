@@ -104,4 +104,55 @@ __device__ __forceinline__ void store_w(void *p, int64_t i, float v, int wdtype)
     static_cast<bf16 *>(p)[i] = (bf16)v;
 }
 
+// VEC weights from column c on (1 or 0, `def`, without a weight)
+template <int VEC>
+__device__ __forceinline__ void load_ws(float (&r)[VEC], const void *p, int64_t c, int wdtype, float def) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r[i] = def;
+  } else if constexpr (VEC == 1) {
+    r[0] = load_w(p, c, wdtype);
+  } else if (wdtype == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + c + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[i + j] = x[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const bf16x4 x = *reinterpret_cast<const bf16x4 *>(static_cast<const bf16 *>(p) + c + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[i + j] = (float)x[j];
+    }
+  }
+}
+
+// Sums of `n` columns over `parts` rows, in an order that does not depend on
+// the launch: a workgroup of 512 has 32 columns, 16 rows at a time (a single
+// thread a column takes a load's latency for every row: 234 us for 1024 rows
+// of 256 columns), and joins its 16 sums in LDS.  put(column, sum).
+constexpr int kSumThreads = 512;
+__host__ __device__ inline unsigned sum_blocks(int64_t n) { return (unsigned)((n + 31) / 32); }
+template <typename F>
+__device__ __forceinline__ void sum_parts(const float *part, int64_t parts, int64_t n, F put) {
+  __shared__ float red[16][32];
+  const int col = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + col;
+  float v = 0.f;
+  if (i < n) {
+#pragma unroll 4
+    for (int64_t p = g; p < parts; p += 16) v += part[p * n + i];
+  }
+  red[g][col] = v;
+  __syncthreads();
+  if (g == 0 && i < n) {
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += red[k][col];
+    put(i, v);
+  }
+}
+
 }  // namespace gdn

@@ -40,69 +40,108 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
   return v;
 }
 
+// Two such sums at once.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float &u, float &v, float *red) {
+  u = group_sum<(TPR < 16 ? TPR : 16)>(u);
+  v = group_sum<(TPR < 16 ? TPR : 16)>(v);
+  if constexpr (TPR >= 32) u += __shfl_xor(u, 16), v += __shfl_xor(v, 16);
+  if constexpr (TPR >= 64) u += __shfl_xor(u, 32), v += __shfl_xor(v, 32);
+  if constexpr (TPR > 64) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[2 * w] = u, red[2 * w + 1] = v;
+    __syncthreads();
+    u = v = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) u += red[2 * i], v += red[2 * i + 1];
+  }
+}
+
 __device__ __forceinline__ float silu_of(float z, float &s) {
   s = sigmoidf(z);
   return z * s;
 }
 
 // TPR lanes hold a row, NV pieces of VEC elements each: piece v of lane l is
-// columns (v TPR + l) VEC ...
+// columns (v TPR + l) VEC ...  A workgroup walks rows with its columns'
+// weights in registers (read again for every row, one by one, they took five
+// times the row's own time), the next row's loads under the current one's sums.
 template <typename E, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArgs a) {
   constexpr int RPB = (TPR > 256 ? TPR : 256) / TPR;
   __shared__ float red[16];
   const int lane = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool live = row < a.rows;  // (TPR > 64: a workgroup has one row, always live)
-  const int64_t r = live ? row : a.rows - 1;
-  const E *x = static_cast<const E *>(a.x) + r * a.D;
-  Vec<E, VEC> xv[NV];
-  float s = 0.f;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * TPR + lane) * VEC;
-    if (c < a.D)
-      xv[v].load(x + c);
-    else
-      xv[v].zero();
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) s += xv[v].v[i];
-  }
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  const E *x = static_cast<const E *>(a.x), *gate = static_cast<const E *>(a.gate);
   const float inv = 1.f / (float)a.D;
-  const float mean = a.rms ? 0.f : row_sum<TPR>(s, red) * inv;
-  float q = 0.f;
+  float w[NV][VEC], b[NV][VEC];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * TPR + lane) * VEC;
     if (c >= a.D) continue;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float d = xv[v].v[i] - mean;
-      q += d * d;
-    }
+    load_ws(w[v], a.w, c, a.wdtype, 1.f);
+    load_ws(b[v], a.b, c, a.wdtype, 0.f);
   }
-  const float rstd = 1.f / __builtin_sqrtf(row_sum<TPR>(q, red) * inv + a.eps);
-  if (!live) return;
-  if (lane == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
+  Raw<E, VEC> xr[NV], gr[NV];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * TPR + lane) * VEC;
-    if (c >= a.D) continue;
-    Vec<E, VEC> g;
-    if (a.gate) g.load(static_cast<const E *>(a.gate) + row * a.D + c);
-    Vec<E, VEC> out;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float z = (xv[v].v[i] - mean) * rstd;
-      if (a.w) z *= load_w(a.w, c + i, a.wdtype);
-      if (a.b) z += load_w(a.b, c + i, a.wdtype);
-      if (a.gate) z *= g.v[i] * sigmoidf(g.v[i]);
-      out.v[i] = z;
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + lane) * VEC;
+      if (c >= a.D) continue;
+      xr[v].load(x + row * a.D + c);
+      if (gate) gr[v].load(gate + row * a.D + c);
     }
-    out.store(static_cast<E *>(a.y) + row * a.D + c);
+  };
+  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  if (row >= a.rows) return;  // (TPR > 64: a workgroup has one row)
+  fetch(row);
+  for (;;) {
+    Vec<E, VEC> xv[NV], g[NV];
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const bool in = (v * TPR + lane) * VEC < a.D;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        xv[v].v[i] = in ? to_f32(xr[v].e[i]) : 0.f;
+        g[v].v[i] = in && gate ? to_f32(gr[v].e[i]) : 0.f;
+        s += xv[v].v[i];
+      }
+    }
+    const int64_t next = row + step;
+    if (next < a.rows) fetch(next);
+    const float mean = a.rms ? 0.f : row_sum<TPR>(s, red) * inv;
+    float q = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const bool in = (v * TPR + lane) * VEC < a.D;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float d = in ? xv[v].v[i] - mean : 0.f;
+        q += d * d;
+      }
+    }
+    const float rstd = 1.f / __builtin_sqrtf(row_sum<TPR>(q, red) * inv + a.eps);
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + lane) * VEC;
+      if (c >= a.D) continue;
+      Vec<E, VEC> out;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        float z = (xv[v].v[i] - mean) * rstd * w[v][i] + b[v][i];
+        if (gate) z *= g[v].v[i] * sigmoidf(g[v].v[i]);
+        out.v[i] = z;
+      }
+      out.store(static_cast<E *>(a.y) + row * a.D + c);
+    }
+    if (next >= a.rows) break;
+    row = next;
   }
 }
 
@@ -164,26 +203,42 @@ template <typename E, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormArgs a, int64_t per) {
   constexpr int THREADS = TPR > 256 ? TPR : 256;
   constexpr int RPB = THREADS / TPR;
-  __shared__ float red[16];
+  __shared__ float red[32];
   __shared__ float cols[RPB > 1 ? THREADS : 1];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const float inv = 1.f / (float)a.D;
   float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TPR + lane) * VEC;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int c = (v * TPR + lane) * VEC + i;
-      w[v][i] = a.w && c < a.D ? load_w(a.w, c, a.wdtype) : (c < a.D ? 1.f : 0.f);
-      b[v][i] = a.b && c < a.D ? load_w(a.b, c, a.wdtype) : 0.f;
-      dw[v][i] = db[v][i] = 0.f;
-    }
+    for (int i = 0; i < VEC; ++i) w[v][i] = b[v][i] = dw[v][i] = db[v][i] = 0.f;
+    if (c >= a.D) continue;
+    load_ws(w[v], a.w, c, a.wdtype, 1.f);
+    load_ws(b[v], a.b, c, a.wdtype, 0.f);
+  }
   const int64_t r0 = (int64_t)blockIdx.x * per;
   const int64_t r1 = r0 + per < a.rows ? r0 + per : a.rows;
+  Raw<E, VEC> xr[NV], yr[NV], gr[NV];
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](int64_t rb) {
+    const int64_t row = rb + sub < r1 ? rb + sub : r1 - 1;
+    nmean = a.rms ? 0.f : a.mean[row];
+    nrstd = a.rstd[row];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + lane) * VEC;
+      if (c >= a.D) continue;
+      xr[v].load(static_cast<const E *>(a.x) + row * a.D + c);
+      yr[v].load(static_cast<const E *>(a.dy) + row * a.D + c);
+      if (a.gate) gr[v].load(static_cast<const E *>(a.gate) + row * a.D + c);
+    }
+  };
+  fetch(r0);
   for (int64_t rb = r0; rb < r1; rb += RPB) {
     const bool live = rb + sub < r1;
     const int64_t row = live ? rb + sub : r1 - 1;
-    const float mean = a.rms ? 0.f : a.mean[row], rstd = a.rstd[row];
+    const float mean = nmean, rstd = nrstd;
     Vec<E, VEC> xh[NV], t[NV];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -192,28 +247,25 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormArg
       xh[v].zero();
       t[v].zero();
       if (c >= a.D) continue;
-      Vec<E, VEC> x, dy, g, dgate;
-      x.load(static_cast<const E *>(a.x) + row * a.D + c);
-      dy.load(static_cast<const E *>(a.dy) + row * a.D + c);
-      g.zero();
-      if (a.gate) g.load(static_cast<const E *>(a.gate) + row * a.D + c);
+      Vec<E, VEC> dgate;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const Elem e = elem(a, x.v[i], dy.v[i], g.v[i], w[v][i], b[v][i], mean, rstd);
+        const Elem e = elem(a, to_f32(xr[v].e[i]), to_f32(yr[v].e[i]), a.gate ? to_f32(gr[v].e[i]) : 0.f, w[v][i], b[v][i],
+                            mean, rstd);
         xh[v].v[i] = e.xh;
         t[v].v[i] = e.t;
         dgate.v[i] = e.dgate;
         s1 += e.t;
         s2 += e.t * e.xh;
-        if (live) {
-          dw[v][i] += e.dz * e.xh;
-          db[v][i] += e.dz;
-        }
+        dw[v][i] += live ? e.dz * e.xh : 0.f;
+        db[v][i] += live ? e.dz : 0.f;
       }
       if (a.gate && live) dgate.store(static_cast<E *>(a.dgate) + row * a.D + c);
     }
-    s1 = a.rms ? 0.f : row_sum<TPR>(s1, red) * inv;
-    s2 = row_sum<TPR>(s2, red) * inv;
+    if (rb + RPB < r1) fetch(rb + RPB);
+    row_sum2<TPR>(s1, s2, red);
+    s1 = a.rms ? 0.f : s1 * inv;
+    s2 *= inv;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * TPR + lane) * VEC;
@@ -294,16 +346,14 @@ __global__ __launch_bounds__(256) void norm_bwd_cols_kernel(NormArgs a, const fl
 }
 
 // dw, db from the workgroups' partials, added in order.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs a, int64_t parts) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= 2 * (int64_t)a.D) return;
-  float v = 0.f;
-  for (int64_t p = 0; p < parts; ++p) v += a.partial[p * 2 * a.D + i];
-  if (i < a.D) {
-    if (a.dw) store_w(a.dw, i, v, a.wdtype);
-  } else if (a.db) {
-    store_w(a.db, i - a.D, v, a.wdtype);
-  }
+__global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs a, int64_t parts) {
+  sum_parts(a.partial, parts, 2 * (int64_t)a.D, [&](int64_t i, float v) {
+    if (i < a.D) {
+      if (a.dw) store_w(a.dw, i, v, a.wdtype);
+    } else if (a.db) {
+      store_w(a.db, i - a.D, v, a.wdtype);
+    }
+  });
 }
 
 // The widest row whose pieces a workgroup holds in registers (16 elements of
@@ -318,7 +368,11 @@ template <typename E, int VEC, int TPR, int NV>
 hipError_t go_fwd(const NormArgs &a, hipStream_t st) {
   constexpr int T = TPR > 256 ? TPR : 256, RPB = T / TPR;
   KernelTimer kt("norm_fwd", st);
-  norm_fwd_kernel<E, VEC, TPR, NV><<<(unsigned)((a.rows + RPB - 1) / RPB), T, 0, st>>>(a);
+  // as many workgroups as the compute units hold at once (2048 threads each)
+  int64_t blocks = compute_units() * (2048 / T);
+  const int64_t most = (a.rows + RPB - 1) / RPB;
+  if (blocks > most) blocks = most;
+  norm_fwd_kernel<E, VEC, TPR, NV><<<(unsigned)blocks, T, 0, st>>>(a);
   return hipGetLastError();
 }
 template <typename E, int VEC, int TPR, int NV>
@@ -358,10 +412,12 @@ hipError_t held_bwd(const NormArgs &a, bool wide, hipStream_t st) {
 }  // namespace
 
 // Workgroups of the backward, each with its partial of the column sums: four
-// a compute unit, and at least 16 rows each so that the partials stay small.
+// a compute unit, but at least 16 rows each while every compute unit has one,
+// so that the partials stay small.
 int64_t norm_bwd_parts(int64_t rows) {
   int64_t p = compute_units() * 4;
-  const int64_t most = (rows + 15) / 16;
+  int64_t most = (rows + 15) / 16;
+  if (most < compute_units()) most = rows < compute_units() ? rows : compute_units();
   p = p < most ? p : most;
   if (p < 1) p = 1;
   const int64_t per = (rows + p - 1) / p;
@@ -382,7 +438,7 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
     return hipGetLastError();
   }
   const int vec = a.dtype == 1 ? 8 : 4;
-  return held_fwd(a, a.D % vec == 0 && al16(a.x) && al16(a.y) && al16(a.gate), st);
+  return held_fwd(a, a.D % vec == 0 && al16(a.x) && al16(a.w) && al16(a.b) && al16(a.y) && al16(a.gate), st);
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
@@ -404,12 +460,12 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
       e = hipGetLastError();
     } else {
       const int vec = a.dtype == 1 ? 8 : 4;
-      e = held_bwd(a, a.D % vec == 0 && al16(a.x) && al16(a.dy) && al16(a.gate) && al16(a.dx) && al16(a.dgate), st);
+      e = held_bwd(a, a.D % vec == 0 && al16(a.x) && al16(a.w) && al16(a.b) && al16(a.dy) && al16(a.gate) && al16(a.dx) && al16(a.dgate), st);
     }
   }
   if (e != hipSuccess || (!a.dw && !a.db)) return e;
   KernelTimer kt("norm_bwd_sum", st);
-  norm_sum_kernel<<<(unsigned)((2 * (int64_t)a.D + 255) / 256), 256, 0, st>>>(a, a.rows ? parts : 0);
+  norm_sum_kernel<<<sum_blocks(2 * (int64_t)a.D), kSumThreads, 0, st>>>(a, a.rows ? parts : 0);
   return hipGetLastError();
 }
 
