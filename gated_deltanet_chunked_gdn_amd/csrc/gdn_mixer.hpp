@@ -26,7 +26,19 @@ __device__ __forceinline__ int seq_of(const Seqs &s, int64_t t) {
   return find_seq(s.cu, s.N, t);
 }
 
-// 16 bytes (VEC elements) or one element, as floats.
+// The raw form of VEC elements (one, or 8 or 16 bytes of them).
+template <int BYTES>
+struct RawOf;
+template <>
+struct RawOf<16> {
+  typedef uint4 type;
+};
+template <>
+struct RawOf<8> {
+  typedef uint2 type;
+};
+
+// VEC elements as floats.
 template <typename E, int VEC>
 struct Vec {
   float v[VEC];
@@ -38,7 +50,8 @@ struct Vec {
     if constexpr (VEC == 1) {
       v[0] = to_f32(*p);
     } else {
-      const uint4 r = *reinterpret_cast<const uint4 *>(p);
+      typedef typename RawOf<VEC * (int)sizeof(E)>::type R;
+      const R r = *reinterpret_cast<const R *>(p);
       const E *e = reinterpret_cast<const E *>(&r);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
@@ -48,15 +61,16 @@ struct Vec {
     if constexpr (VEC == 1) {
       *p = from_f32<E>(v[0]);
     } else {
-      uint4 r;
+      typedef typename RawOf<VEC * (int)sizeof(E)>::type R;
+      R r;
       E *e = reinterpret_cast<E *>(&r);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) e[i] = from_f32<E>(v[i]);
-      *reinterpret_cast<uint4 *>(p) = r;
+      *reinterpret_cast<R *>(p) = r;
     }
   }
 };
-// one raw 16-byte (or single-element) load, converted later: a batch of these
+// one raw load, converted later: a batch of these
 // stays in flight without holding its fp32 form
 template <typename E, int VEC>
 struct Raw {
@@ -65,7 +79,8 @@ struct Raw {
     if constexpr (VEC == 1) {
       e[0] = *p;
     } else {
-      *reinterpret_cast<uint4 *>(e) = *reinterpret_cast<const uint4 *>(p);
+      typedef typename RawOf<VEC * (int)sizeof(E)>::type R;
+      *reinterpret_cast<R *>(e) = *reinterpret_cast<const R *>(p);
     }
   }
   __device__ __forceinline__ Vec<E, VEC> f() const {

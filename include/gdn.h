@@ -195,9 +195,9 @@ size_t gdn_chunk_fwd_noalloc_max_bytes(void);
  *                 as these: weight_dtype
  *   initial_state, final_state, dfinal_state, dinitial_state
  *                 [N, W - 1, D]   problem dtype, the last W - 1 inputs
- * Every pointer is aligned to its element; rows of 16-byte pieces (D and
- * x_stride a multiple of 8 in bf16, 4 in fp32, buffers 16-byte aligned) are
- * the fast form. */
+ * Every pointer is aligned to its element; D and x_stride in multiples of 4
+ * (the step in bf16: 8) and rows aligned to as many elements are the fast
+ * form. */
 typedef struct {
   int32_t B, T, D, W, N; /* N: sequences (B without cu_seqlens) */
   int32_t dtype, weight_dtype; /* gdn_dtype_t */
