@@ -31,7 +31,7 @@ struct SlotLoc {
 // Byte offsets of the workspace's pieces (each at a 256-byte boundary).
 struct Layout {
   size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
-         o_dc = 0, o_db = 0, o_shi = 0, o_slo = 0, o_z = 0, total = 0;
+         o_dc = 0, o_db = 0, o_ai = 0, o_shi = 0, o_slo = 0, o_z = 0, total = 0;
   int64_t chunks = 0;      // slots of 64-token chunks (bf16 backward)
   bool need_last = false;  // the local pass runs a sequence's last segment too
   __host__ __device__ float *at(const ScanArgs &a, size_t o) const { return reinterpret_cast<float *>(a.ws + o); }
@@ -49,6 +49,8 @@ struct Layout {
   __host__ __device__ float *a_part(const ScanArgs &a) const { return at(a, o_a); }
   __host__ __device__ float *r_part(const ScanArgs &a) const { return at(a, o_r); }
   __host__ __device__ float *m_part(const ScanArgs &a) const { return at(a, o_m); }
+  // bf16: what of a_t comes from the state entering the chunk
+  __host__ __device__ float *ai_part(const ScanArgs &a) const { return at(a, o_ai); }
   // parts of dD: [slices][slots, bf16: chunks][Hv]
   __host__ __device__ float *dd_part(const ScanArgs &a) const { return at(a, o_dd); }
   // [slices][chunks][Hv]: parts of <S, Z> of every chunk's last state (bf16)
@@ -103,6 +105,7 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_a = piece(tok * slices * 4);
     w.o_r = piece(tok * slices * 4);
     w.o_m = piece(tok * slices * 4);
+    w.o_ai = piece(tok * slices * 4);
     w.o_dd = piece(ch * slices * 4);
     w.o_x = piece(ch * slices * 4);
     w.o_head = piece(ch * 3 * 4);

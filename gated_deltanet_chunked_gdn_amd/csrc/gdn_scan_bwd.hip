@@ -17,7 +17,8 @@
 //   dg_t = <S', Z> + sum_{s >= t} (a_s - delta_s r_s),  S' the state leaving
 //   d delta_t = r_t + m_t + A dg_t
 //
-// Two kernels share this.  grad_kernel walks a segment's chunks from its end
+// The pass that forms the states (kStates, gdn_scan_mma.hip) also has the
+// state's part of a_i.  Two kernels share the rest.  grad_kernel walks a segment's chunks from its end
 // with Z in accumulators (32 columns of a head a wave, as the forward): dx,
 // the gates' sums, and Z of every chunk, rounded to bf16, for the other.
 // pair_kernel has dc and db: one chunk of one head group a workgroup, the
@@ -67,14 +68,10 @@ __device__ __forceinline__ float dot8(const bf16x8 &a, const bf16x8 &b, float c)
 // Token of this lane's tile: sum over the 32 columns of acc (rows column,
 // lane token) times the token's row of a pi-layout matrix.
 __device__ __forceinline__ float row_dot(const f32x16 &acc, const bf16 *row, int h2) {
-  float v = 0.f;
+  bf16x4 x[4];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const bf16x4 x = *reinterpret_cast<const bf16x4 *>(row + pi_pos(8 * b) + 8 * h2);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v += acc[4 * b + e] * (float)x[e];
-  }
-  return v + __shfl_xor(v, 32);
+  for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const bf16x4 *>(row + pi_pos(8 * b) + 8 * h2);
+  return acc_dot(acc, x);
 }
 
 // Writes rows of 32 columns (acc + skip * row of `add`, rows column, lane
@@ -130,22 +127,28 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
   typename D::State Z;
   state_io<K, V>(Z, w.zend(a) + (slot * a.Hv + h) * kv + v0, false, tid0 & 63);
   bf16x8 sh[K / 16], sl[K / 16];
-  Rows<K, THREADS> kr, qr;
-  Rows<VW, 64> xr, dr;
+  // one chunk's rows on their way to LDS.  (An object of the loop's body: one
+  // outside it, loaded under a condition, would hold its registers throughout.)
+  struct In {
+    Rows<K, THREADS> k, q;
+    Rows<VW, 64> x, dy;
+  };
   float z = 0.f;
   const int64_t first_chunk = w.chunk(a, loc, 0);
   auto state_at = [&](int c, int lane) {
     return (((first_chunk + c) * a.Hv + h) * (V / 32) + vs) * (K * 32) + lane * 8;
   };
-  auto fetch = [&](int c, int tid) {
+  auto fetch = [&](In &r, int c, int tid) {
     const int lane = tid & 63;
     const int64_t t = loc.t0 + 64 * (int64_t)c;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
-    kr.load(bp + t * a.bs, a.bs, rows, tid);
-    qr.load(cp + t * a.cs, a.cs, rows, tid);
-    xr.load(xp + t * a.xs, a.xs, rows, lane);
-    dr.load(dp + t * ys, ys, rows, lane);
+    r.k.load(bp + t * a.bs, a.bs, rows, tid);
+    r.q.load(cp + t * a.cs, a.cs, rows, tid);
+    r.x.load(xp + t * a.xs, a.xs, rows, lane);
+    r.dy.load(dp + t * ys, ys, rows, lane);
     z = lane < rows ? (float)dtp[(t + lane) * a.Hv] : 0.f;
+  };
+  auto fetch_state = [&](int c, int lane) {
     const int64_t at = state_at(c, lane);
 #pragma unroll
     for (int s = 0; s < K / 16; ++s) {
@@ -153,15 +156,19 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
       sl[s] = *reinterpret_cast<const bf16x8 *>(w.s_lo(a) + at + s * 512);
     }
   };
-  auto commit = [&](int tid) {
+  auto commit = [&](const In &r, int tid) {
     const int lane = tid & 63;
-    kr.store_pi(Kl, KP, tid);
-    qr.store_pi(Ql, KP, tid);
-    xr.store_pi(Xl[wave], VP, lane);
-    dr.store_pi(Dl[wave], VP, lane);
+    r.k.store_pi(Kl, KP, tid);
+    r.q.store_pi(Ql, KP, tid);
+    r.x.store_pi(Xl[wave], VP, lane);
+    r.dy.store_pi(Dl[wave], VP, lane);
   };
-  fetch(nc - 1, tid0);
-  commit(tid0);
+  {
+    In r;
+    fetch(r, nc - 1, tid0);
+    fetch_state(nc - 1, tid0 & 63);
+    commit(r, tid0);
+  }
   __syncthreads();
   for (int c = nc - 1; c >= 0; --c) {
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
@@ -171,12 +178,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
     const float eL = gt.all();
-    // U^T = S^T C^T and Y^T = Z^T B^T (rows v, lane token), <S, Z>, and Z out
-    f32x16 Y[2] = {zero16(), zero16()}, U[2] = {zero16(), zero16()};
+    // Y^T = Z^T B^T (rows v, lane token), <S, Z>, and Z out
+    f32x16 Y[2] = {zero16(), zero16()};
     float xd = 0.f;
     {
       const int64_t at = state_at(c, lane);
-      const bf16 *q0 = q + r32 * KP + 8 * h2, *k0 = k + r32 * KP + 8 * h2;
+      const bf16 *k0 = k + r32 * KP + 8 * h2;
 #pragma unroll
       for (int s = 0; s < K / 16; ++s) {
         const Split zf = split(Z[s >> 1], s & 1);
@@ -186,9 +193,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
         xd = dot8(sl[s], zf.hi, xd);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const bf16x8 qf = lds16(q0 + 32 * i * KP + 16 * s), kf = lds16(k0 + 32 * i * KP + 16 * s);
-          U[i] = mma32(sh[s], qf, U[i]);
-          U[i] = mma32(sl[s], qf, U[i]);
+          const bf16x8 kf = lds16(k0 + 32 * i * KP + 16 * s);
           Y[i] = mma32(zf.hi, kf, Y[i]);
           Y[i] = mma32(zf.lo, kf, Y[i]);
         }
@@ -202,8 +207,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tok = 32 * i + r32;
-        const float ai = row_dot(U[i], dy + tok * VP, h2) * g.p[tok];
-        if (h2 == 0) Sa[wave][tok] = ai;
         ri[i] = row_dot(Y[i], x + tok * VP, h2) * g.w1[tok];
         sum += ri[i] * g.del[tok];
       }
@@ -237,7 +240,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
         f32x16 P = zero16(), M = zero16();
         const bf16 *qi = q + (32 * it + r32) * KP + 8 * h2, *kj = k + tj * KP + 8 * h2;
 #pragma unroll
-        for (int s = 0; s < K / 16; ++s) P = mma32(lds16(qi + 16 * s), lds16(kj + 16 * s), P);
+        for (int s = 0; s < K / 16; ++s) {
+          P = mma32(lds16(qi + 16 * s), lds16(kj + 16 * s), P);
+          if ((s & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
           M = mma32(lds16(dy + (32 * it + r32) * VP + 8 * h2 + 16 * s), lds16(x + tj * VP + 8 * h2 + 16 * s), M);
@@ -269,6 +275,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) T = mma32(df[2 * it + s], slots(P, s), T);
+        __builtin_amdgcn_sched_barrier(0);
       }
       rs += __shfl_xor(rs, 32);
       ms += __shfl_xor(ms, 32);
@@ -286,7 +293,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     for (int it = 0; it < 2; ++it) {
       const float v = fold16(ar[it], lane);
       const int i = 32 * it + 8 * ((lane & 15) >> 2) + 4 * h2 + (lane & 3);
-      if (!(lane & 16)) Sa[wave][i] += v;
+      if (!(lane & 16)) Sa[wave][i] = v;
     }
     wave_lds_fence();
     dD = wave_sum(dD);
@@ -303,7 +310,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
         w.dd_part(a)[i] = dD;
       }
     }
-    if (c > 0) fetch(c - 1, tid);
+    In in;
+    if (c > 0) fetch(in, c - 1, tid);
     __builtin_amdgcn_sched_barrier(0);
     // Z = 2^{gamma_L} Z + C^T (p dY)
 #pragma unroll
@@ -320,10 +328,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
         Z[kt] = mma32(qf, y.hi, Z[kt]);
         Z[kt] = mma32(qf, y.lo, Z[kt]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    // (before the update, the state's registers would not fit beside it)
+    fetch_state(c > 0 ? c - 1 : 0, lane);
     if (c > 0) {
       __syncthreads();  // every wave is done with c and b
-      commit(tid);
+      commit(in, tid);
       __syncthreads();
     }
   }
@@ -541,7 +552,7 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   float av = 0.f, rv = 0.f, mv = 0.f, x = 0.f, dD = 0.f;
   for (int s = 0; s < slices; ++s) {
     const int64_t i = ((int64_t)s * a.Hv + h) * a.s.tokens + t;
-    av += w.a_part(a)[i];
+    av += w.a_part(a)[i] + w.ai_part(a)[i];
     rv += w.r_part(a)[i];
     mv += w.m_part(a)[i];
     const int64_t j = ((int64_t)s * w.chunks + slot) * a.Hv + h;

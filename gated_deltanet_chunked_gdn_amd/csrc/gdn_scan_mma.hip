@@ -33,17 +33,18 @@ namespace {
 // What a pass over a segment's chunks does:
 //   kLocal   the segment's last state from zero and its decay (for carry_kernel)
 //   kOut     y, from the segment's start state, and the sequence's last state
-//   kStates  the state entering every chunk, as two bf16 parts (backward)
+//   kStates  the state entering every chunk, as two bf16 parts, and the part
+//            of a_i that comes from it, p_i c_i . S dy_i (backward)
 //   kRLocal  reverse: the gradient of the segment's first state from its own
 //            outputs; a.b, a.x hold c and dy: Z = 2^{gamma_L} Z + C^T (2^{gamma} dY)
 enum { kLocal, kOut, kStates, kRLocal };
 
 template <int K, int V, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
-  constexpr bool OUT = MODE == kOut, REV = MODE == kRLocal;
+  constexpr bool OUT = MODE == kOut, REV = MODE == kRLocal, QROWS = OUT || MODE == kStates;
   using D = Dims<K, V>;
   constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
-  __shared__ __align__(16) bf16 Kl[2][64 * KP], Ql[OUT ? 2 : 1][OUT ? 64 * KP : 8], Vl[NW][64 * VP];
+  __shared__ __align__(16) bf16 Kl[2][64 * KP], Ql[QROWS ? 2 : 1][QROWS ? 64 * KP : 8], Vl[NW][64 * VP];
   __shared__ __align__(16) Gates G[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), h2 = lane >> 5, r32 = lane & 31;
   const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
@@ -72,27 +73,32 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
   }
 
   const int nt = (int)(loc.t1 - loc.t0), nc = (nt + 63) >> 6;
-  Rows<K, THREADS> kr, qr;
-  Rows<VW, 64> vr;
+  // one chunk's rows on their way to LDS.  (An object of the loop's body: one
+  // outside it, loaded under a condition, would hold its registers throughout.)
+  struct In {
+    Rows<K, THREADS> k, q;
+    Rows<VW, 64> v;
+  };
   float z = 0.f;
-  auto fetch = [&](int step, int tid) {
+  auto fetch = [&](In &r, int step, int tid) {
     const int lane = tid & 63, c = REV ? nc - 1 - step : step;
     const int64_t t = loc.t0 + 64 * (int64_t)c;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
-    kr.load(bp + t * a.bs, a.bs, rows, tid);
-    if (OUT) qr.load(cp + t * a.cs, a.cs, rows, tid);
-    vr.load(xp + t * a.xs, a.xs, rows, lane);
+    r.k.load(bp + t * a.bs, a.bs, rows, tid);
+    if (QROWS) r.q.load(cp + t * a.cs, a.cs, rows, tid);
+    r.v.load(xp + t * a.xs, a.xs, rows, lane);
     z = lane < rows ? (float)dtp[(t + lane) * a.Hv] : 0.f;
   };
-  auto commit = [&](int buf, int tid) {
+  auto commit = [&](const In &r, int buf, int tid) {
     const int lane = tid & 63;
-    kr.store_pi(Kl[buf], KP, tid);
-    if (OUT) qr.store_pi(Ql[buf], KP, tid);
-    vr.store_pi(Vl[wave], VP, lane);
+    r.k.store_pi(Kl[buf], KP, tid);
+    if (QROWS) r.q.store_pi(Ql[buf], KP, tid);
+    r.v.store_pi(Vl[wave], VP, lane);
   };
   if (nc > 0) {
-    fetch(0, tid);
-    commit(0, tid);
+    In r;
+    fetch(r, 0, tid);
+    commit(r, 0, tid);
   }
   __syncthreads();
   float total = 0.f;
@@ -103,15 +109,39 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     Gates &g = G[wave];
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
-    if (step + 1 < nc) fetch(step + 1, tid);
-    const bf16 *k = Kl[step & 1], *q = Ql[OUT ? step & 1 : 0], *v = Vl[wave];
+    In in;
+    if (step + 1 < nc) fetch(in, step + 1, tid);
+    const bf16 *k = Kl[step & 1], *q = Ql[QROWS ? step & 1 : 0], *v = Vl[wave];
     if (MODE == kStates) {
       const int64_t at = ((w.chunk(a, loc, c) * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32) + lane * 8;
+      bf16x4 dyv[2][4];  // dy of this lane's tokens, columns 8 b + 4 h ..
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 32 * i + r32 < rows ? 32 * i + r32 : rows - 1;
+        const bf16 *p = static_cast<const bf16 *>(a.dy) + ((loc.t0 + 64 * (int64_t)c + tok) * a.Hv + h) * V + v0 + 4 * h2;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) dyv[i][b] = *reinterpret_cast<const bf16x4 *>(p + 8 * b);
+      }
+      f32x16 U[2] = {zero16(), zero16()};  // U^T = S^T C^T
 #pragma unroll
       for (int s = 0; s < K / 16; ++s) {
         const Split x = split(S[s >> 1], s & 1);
         *reinterpret_cast<bf16x8 *>(w.s_hi(a) + at + s * 512) = x.hi;
         *reinterpret_cast<bf16x8 *>(w.s_lo(a) + at + s * 512) = x.lo;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bf16x8 qf = lds16(q + (32 * i + r32) * KP + 16 * s + 8 * h2);
+          U[i] = mma32(x.hi, qf, U[i]);
+          U[i] = mma32(x.lo, qf, U[i]);
+        }
+        if (s & 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      const int64_t t0 = loc.t0 + 64 * (int64_t)c;
+      float *ai = w.ai_part(a) + ((int64_t)(v0 / 32) * a.Hv + h) * a.s.tokens + t0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float v = acc_dot(U[i], dyv[i]) * g.p[32 * i + r32];
+        if (h2 == 0 && 32 * i + r32 < rows) ai[32 * i + r32] = v;
       }
     }
     bf16x8 vf[4];
@@ -201,7 +231,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
         S[kt] = mma32(kf, x.lo, S[kt]);
       }
     }
-    if (step + 1 < nc) commit((step + 1) & 1, tid);
+    if (step + 1 < nc) commit(in, (step + 1) & 1, tid);
     __syncthreads();
   }
   if (MODE == kLocal || REV) {

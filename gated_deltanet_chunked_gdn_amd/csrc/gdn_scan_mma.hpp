@@ -147,6 +147,17 @@ __device__ __forceinline__ Split split(const f32x16 &x, int s) {
   return r;
 }
 
+// Sum over the 32 columns of an accumulator tile (rows column, lane token)
+// times the token's values of columns 8 b + 4 h ..
+__device__ __forceinline__ float acc_dot(const f32x16 &acc, const bf16x4 (&x)[4]) {
+  float v = 0.f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v += acc[4 * b + e] * (float)x[b][e];
+  return v + __shfl_xor(v, 32);
+}
+
 template <int K, int V>
 struct Dims {
   static constexpr int VW = 32, KT = K / 32;
