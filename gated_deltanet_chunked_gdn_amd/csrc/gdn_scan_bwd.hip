@@ -351,14 +351,28 @@ struct Pair {
   static constexpr int KP = K + 16, UP = UC + 16, NP = 64 + 16;
 };
 
+// One unit is worked on in one LDS buffer, the next is written into the other
+// (its gates by a wave that has no tile of N), the two after it are on their
+// way in registers: one barrier a unit.  With one unit ahead and one buffer
+// every unit waited for its own loads and gates (180 us at 2 x 4096 tokens x
+// 64 heads, 2.2 TB/s).
 template <int K, int V>
 __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   using C = Pair<K, V>;
   constexpr int KT = C::KT, UC = C::UC, KP = C::KP, UP = C::UP, NP = C::NP, THREADS = C::THREADS;
-  __shared__ __align__(16) bf16 Ql[64 * KP], Kl[64 * KP], Sl[UC * KP], Zl[UC * KP], Xl[64 * UP], Dl[64 * UP];
-  __shared__ __align__(16) bf16 N[2][64 * NP];
-  __shared__ __align__(16) Gates G;
-  __shared__ __align__(16) float Np[3][16][64];
+  struct Buf {
+    bf16 s[UC * KP], z[UC * KP], x[64 * UP], dy[64 * UP];
+  };
+  struct Tiles {  // after the units
+    bf16 n[2][64 * NP];
+    float part[3][16][64];
+  };
+  __shared__ __align__(16) bf16 Ql[64 * KP], Kl[64 * KP];
+  __shared__ __align__(16) char room[2 * sizeof(Buf) > sizeof(Tiles) ? 2 * sizeof(Buf) : sizeof(Tiles)];
+  __shared__ __align__(16) Gates G[2];
+  __shared__ uint32_t Gm[2][2];
+  Buf *const B = reinterpret_cast<Buf *>(room);
+  Tiles &Tl = *reinterpret_cast<Tiles *>(room);
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), h2 = lane >> 5, r32 = lane & 31;
   const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
   const int hq = (int)(item % a.Hq);
@@ -369,54 +383,57 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   const int64_t t0 = loc.t0, ys = (int64_t)a.Hv * V;
   const int R = a.Hv / a.Hq, units = R * (V / UC);
 
-  Rows<K, THREADS> kr, qr;
-  kr.load(static_cast<const bf16 *>(a.b) + t0 * a.bs + hq * K, a.bs, rows, tid);
-  qr.load(static_cast<const bf16 *>(a.c) + t0 * a.cs + hq * K, a.cs, rows, tid);
-  constexpr int SP = UC * K / 8 / THREADS > 0 ? UC * K / 8 / THREADS : 1;  // state pieces a thread
-  uint4 sr[SP], zr[SP];
+  constexpr int PIECES = UC * K / 8;  // of a state
+  constexpr int SP = (PIECES + THREADS - 1) / THREADS;
   constexpr int XT = 64 * UC / 8;  // threads that move x and dy pieces
   static_assert(XT <= THREADS, "one piece a thread");
-  uint4 xr = make_uint4(0, 0, 0, 0), dr = xr;
-  float z = 0.f;
-  auto fetch = [&](int u) {
+  struct In {
+    uint4 s[SP], z[SP], x, dy;
+    float dt;
+  };
+  const int xrow = tid / (UC / 8), xcol = tid % (UC / 8);
+  auto fetch = [&](In &r, int u) {
     const int h = hq * R + u * UC / V, v0 = u * UC % V;
     const int64_t st = ((slot * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32);
+    const auto rs = raw_buffer(w.s_hi(a) + st, PIECES * 16), rz = raw_buffer(w.z(a) + st, PIECES * 16);
 #pragma unroll
     for (int i = 0; i < SP; ++i) {
-      const int pc = tid + i * THREADS;
-      if (pc < UC * K / 8) {
-        sr[i] = *reinterpret_cast<const uint4 *>(w.s_hi(a) + st + pc * 8);
-        zr[i] = *reinterpret_cast<const uint4 *>(w.z(a) + st + pc * 8);
+      r.s[i] = buf_load16(rs, (tid + i * THREADS) * 16);
+      r.z[i] = buf_load16(rz, (tid + i * THREADS) * 16);
+    }
+    const auto rx = raw_buffer(static_cast<const bf16 *>(a.x) + t0 * a.xs + (int64_t)h * V + v0, (uint32_t)(((rows - 1) * a.xs + UC) * 2));
+    const auto ry = raw_buffer(static_cast<const bf16 *>(a.dy) + t0 * ys + (int64_t)h * V + v0, (uint32_t)(((rows - 1) * ys + UC) * 2));
+    const bool in = xrow < rows;  // (rows < 64: threads past XT have xrow >= 64)
+    r.x = buf_load16(rx, in ? (uint32_t)(xrow * a.xs * 2 + xcol * 16) : kOutside);
+    r.dy = buf_load16(ry, in ? (uint32_t)(xrow * ys * 2 + xcol * 16) : kOutside);
+    r.dt = lane < rows ? (float)static_cast<const bf16 *>(a.dt)[(t0 + lane) * a.Hv + h] : 0.f;
+  };
+  // unit u into its buffer, and its gates
+  auto commit = [&](const In &r, int u) {
+    Buf &b = B[u & 1];
+    if (wave == 7) {
+      const int h = hq * R + u * UC / V;
+      const GateTotals t = gates(G[u & 1], r.dt + (a.dt_bias ? a.dt_bias[h] : 0.f), a.A[h] * kLog2e, a.softplus, lane < rows, lane);
+      if (lane == 0) {
+        Gm[u & 1][0] = t.m0;
+        Gm[u & 1][1] = t.m1;
       }
     }
-    const int row = tid / (UC / 8), col = tid % (UC / 8);
-    xr = dr = make_uint4(0, 0, 0, 0);
-    if (tid < XT && row < rows) {
-      xr = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.x) + (t0 + row) * a.xs + (int64_t)h * V + v0 + col * 8);
-      dr = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.dy) + (t0 + row) * ys + (int64_t)h * V + v0 + col * 8);
-    }
-    z = lane < rows ? (float)static_cast<const bf16 *>(a.dt)[(t0 + lane) * a.Hv + h] : 0.f;
-  };
-  auto commit = [&] {
 #pragma unroll
     for (int i = 0; i < SP; ++i) {
       // piece (column slice, s, lane): column, and its place in the column's row of k
       const int pc = tid + i * THREADS, l = pc & 63, s = pc / 64 % (K / 16), cs = pc / 64 / (K / 16);
-      if (pc < UC * K / 8) {
+      if (PIECES % THREADS == 0 || pc < PIECES) {
         const int at = (32 * cs + (l & 31)) * KP + 16 * s + 8 * (l >> 5);
-        *reinterpret_cast<uint4 *>(Sl + at) = sr[i];
-        *reinterpret_cast<uint4 *>(Zl + at) = zr[i];
+        *reinterpret_cast<uint4 *>(b.s + at) = r.s[i];
+        *reinterpret_cast<uint4 *>(b.z + at) = r.z[i];
       }
     }
-    const int row = tid / (UC / 8), col = tid % (UC / 8);
     if (tid < XT) {
-      put_pi(Xl + row * UP, col, xr);
-      put_pi(Dl + row * UP, col, dr);
+      put_pi(b.x + xrow * UP, xcol, r.x);
+      put_pi(b.dy + xrow * UP, xcol, r.dy);
     }
   };
-  fetch(0);
-  kr.store_pi(Kl, KP, tid);
-  qr.store_pi(Ql, KP, tid);
 
   const bool has_out = wave < 2 * KT, is_db = wave >= KT;
   const int kt = wave % KT;
@@ -424,23 +441,14 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   // wave 0..5: tile (it, jt) of N (rows i, lane j), units of one parity
   const int nt = wave % 3, it = nt > 0, jt = nt > 1;
   f32x16 Nacc = zero16();
-  for (int u = 0; u < units; ++u) {
-    const int h = hq * R + u * UC / V;
-    __syncthreads();  // the last unit's reads are done
-    commit();
-    GateTotals gt;
-    if (wave == 0) {
-      const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-      gt = gates(G, z + bias, a.A[h] * kLog2e, a.softplus, lane < rows, lane);
-      if (lane == 0) {
-        Np[0][0][0] = __builtin_bit_cast(float, gt.m0);
-        Np[0][0][1] = __builtin_bit_cast(float, gt.m1);
-      }
-    }
-    __syncthreads();
-    gt.m0 = __builtin_bit_cast(uint32_t, Np[0][0][0]);
-    gt.m1 = __builtin_bit_cast(uint32_t, Np[0][0][1]);
-    if (u + 1 < units) fetch(u + 1);
+  // unit u; `in` holds u + 1 and takes u + 3
+  auto work = [&](In &in, int u) {
+    __syncthreads();  // unit u is in LDS, the other buffer's reads are done
+    if (u + 1 < units) commit(in, u + 1);
+    fetch(in, u + 3 < units ? u + 3 : units - 1);
+    const Buf &b_ = B[u & 1];
+    const Gates &g = G[u & 1];
+    const bf16 *Sl = b_.s, *Zl = b_.z, *Xl = b_.x, *Dl = b_.dy;
     if (has_out) {
       const TrA ts((is_db ? Zl : Sl), KP, lane);
       const bf16 *y = (is_db ? Xl : Dl) + r32 * UP + 8 * h2;
@@ -453,7 +461,7 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float f = is_db ? G.w[32 * i + r32] : G.p[32 * i + r32];
+        const float f = is_db ? g.w[32 * i + r32] : g.p[32 * i + r32];
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][e] += f * P[i][e];
       }
@@ -463,12 +471,12 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
       const bf16 *yi = Dl + (32 * it + r32) * UP + 8 * h2, *xj = Xl + (32 * jt + r32) * UP + 8 * h2;
 #pragma unroll
       for (int s = 0; s < UC / 16; ++s) M = mma32(lds16(yi + 16 * s), lds16(xj + 16 * s), M);
-      const float gj = G.gam[32 * jt + r32], dj = G.del[32 * jt + r32], uj = G.u[r32];
-      const int lim = next_bit(above(jt ? gt.m1 : gt.m0, r32));
+      const float gj = g.gam[32 * jt + r32], dj = g.del[32 * jt + r32], uj = g.u[r32];
+      const int lim = next_bit(above(Gm[u & 1][jt], r32));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int i0 = 8 * b + 4 * h2;
-        const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &G.gam[32 * it + i0] : &G.e[i0]);
+        const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &g.gam[32 * it + i0] : &g.e[i0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = i0 + e;
@@ -481,16 +489,32 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
         }
       }
     }
+  };
+  {
+    In in0, in1;
+    fetch(in0, 0);
+    fetch(in1, units > 1 ? 1 : 0);
+    Rows<K, THREADS> kr, qr;
+    kr.load(static_cast<const bf16 *>(a.b) + t0 * a.bs + hq * K, a.bs, rows, tid);
+    qr.load(static_cast<const bf16 *>(a.c) + t0 * a.cs + hq * K, a.cs, rows, tid);
+    kr.store_pi(Kl, KP, tid);
+    qr.store_pi(Ql, KP, tid);
+    commit(in0, 0);
+    fetch(in0, units > 2 ? 2 : units - 1);
+    for (int u = 0; u < units; u += 2) {
+      work(in1, u);
+      if (u + 1 < units) work(in0, u + 1);
+    }
   }
   // N of all heads, rounded to bf16, by rows i and by rows j
   __syncthreads();
   if (wave >= 3 && wave < 6) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) Np[nt][e][lane] = Nacc[e];
+    for (int e = 0; e < 16; ++e) Tl.part[nt][e][lane] = Nacc[e];
   }
   for (int i = tid; i < 32 * NP; i += THREADS) {  // the tile with j > i
-    N[0][i] = (bf16)0.f;
-    N[1][32 * NP + i] = (bf16)0.f;
+    Tl.n[0][i] = (bf16)0.f;
+    Tl.n[1][32 * NP + i] = (bf16)0.f;
   }
   __syncthreads();
   if (wave < 3) {
@@ -499,21 +523,21 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
       bf16x4 r;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float v = Nacc[4 * b + e] + Np[nt][4 * b + e][lane];
+        const float v = Nacc[4 * b + e] + Tl.part[nt][4 * b + e][lane];
         r[e] = (bf16)v;
         const int i = 32 * it + 8 * b + 4 * h2 + e, j = 32 * jt + r32;
         // N[0]: rows i, position of j in the pi layout
-        N[0][i * NP + pi_pos(j & ~3) + (j & 3)] = r[e];
+        Tl.n[0][i * NP + pi_pos(j & ~3) + (j & 3)] = r[e];
       }
       // N[1]: rows j, four consecutive i
-      *reinterpret_cast<bf16x4 *>(&N[1][(32 * jt + r32) * NP + pi_pos(32 * it + 8 * b) + 8 * h2]) = r;
+      *reinterpret_cast<bf16x4 *>(&Tl.n[1][(32 * jt + r32) * NP + pi_pos(32 * it + 8 * b) + 8 * h2]) = r;
     }
   }
   __syncthreads();
   if (!has_out) return;
   // dc^T += B^T N^T (lane i, over j <= i); db^T += C^T N (lane j, over i >= j)
   const TrA tb(is_db ? Ql : Kl, KP, lane);
-  const bf16 *nr = N[is_db ? 1 : 0] + r32 * NP + 8 * h2;
+  const bf16 *nr = Tl.n[is_db ? 1 : 0] + r32 * NP + 8 * h2;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const bf16x8 f = tb.at(s, kt, KP);
