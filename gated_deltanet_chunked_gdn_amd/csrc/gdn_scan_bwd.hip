@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     Rows<K, THREADS> k, q;
     Rows<VW, 64> x, dy;
   };
-  float z = 0.f;
+  bf16 z = (bf16)0.f;  // dt of this lane's token
   const int64_t first_chunk = w.chunk(a, loc, 0);
   auto state_at = [&](int c, int lane) {
     return (((first_chunk + c) * a.Hv + h) * (V / 32) + vs) * (K * 32) + lane * 8;
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     r.q.load(cp + t * a.cs, a.cs, rows, tid);
     r.x.load(xp + t * a.xs, a.xs, rows, lane);
     r.dy.load(dp + t * ys, ys, rows, lane);
-    z = lane < rows ? (float)dtp[(t + lane) * a.Hv] : 0.f;
+    z = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
   };
   auto fetch_state = [&](int c, int lane) {
     const int64_t at = state_at(c, lane);
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     const int64_t t0 = loc.t0 + 64 * (int64_t)c;
     Gates &g = G[wave];
-    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
+    const GateTotals gt = gates(g, (float)z + bias, A2, a.softplus, lane < rows, lane);
     const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
     const float eL = gt.all();
     // Y^T = Z^T B^T (rows v, lane token), <S, Z>, and Z out
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
       }
     }
     In in;
-    if (c > 0) fetch(in, c - 1, tid);
+    fetch(in, c > 0 ? c - 1 : 0, tid);
     __builtin_amdgcn_sched_barrier(0);
     // Z = 2^{gamma_L} Z + C^T (p dY)
 #pragma unroll
@@ -389,7 +389,8 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   static_assert(XT <= THREADS, "one piece a thread");
   struct In {
     uint4 s[SP], z[SP], x, dy;
-    float dt;
+    bf16 dt;
+    float A, bias;
   };
   const int xrow = tid / (UC / 8), xcol = tid % (UC / 8);
   auto fetch = [&](In &r, int u) {
@@ -406,14 +407,15 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
     const bool in = xrow < rows;  // (rows < 64: threads past XT have xrow >= 64)
     r.x = buf_load16(rx, in ? (uint32_t)(xrow * a.xs * 2 + xcol * 16) : kOutside);
     r.dy = buf_load16(ry, in ? (uint32_t)(xrow * ys * 2 + xcol * 16) : kOutside);
-    r.dt = lane < rows ? (float)static_cast<const bf16 *>(a.dt)[(t0 + lane) * a.Hv + h] : 0.f;
+    r.dt = load_dt(static_cast<const bf16 *>(a.dt) + t0 * a.Hv + h, a.Hv, rows, lane);
+    r.A = a.A[h];
+    r.bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   };
   // unit u into its buffer, and its gates
   auto commit = [&](const In &r, int u) {
     Buf &b = B[u & 1];
     if (wave == 7) {
-      const int h = hq * R + u * UC / V;
-      const GateTotals t = gates(G[u & 1], r.dt + (a.dt_bias ? a.dt_bias[h] : 0.f), a.A[h] * kLog2e, a.softplus, lane < rows, lane);
+      const GateTotals t = gates(G[u & 1], (float)r.dt + r.bias, r.A * kLog2e, a.softplus, lane < rows, lane);
       if (lane == 0) {
         Gm[u & 1][0] = t.m0;
         Gm[u & 1][1] = t.m1;

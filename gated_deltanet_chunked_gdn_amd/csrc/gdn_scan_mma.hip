@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     Rows<K, THREADS> k, q;
     Rows<VW, 64> v;
   };
-  float z = 0.f;
+  bf16 z = (bf16)0.f;  // dt of this lane's token
   auto fetch = [&](In &r, int step, int tid) {
     const int lane = tid & 63, c = REV ? nc - 1 - step : step;
     const int64_t t = loc.t0 + 64 * (int64_t)c;
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     r.k.load(bp + t * a.bs, a.bs, rows, tid);
     if (QROWS) r.q.load(cp + t * a.cs, a.cs, rows, tid);
     r.v.load(xp + t * a.xs, a.xs, rows, lane);
-    z = lane < rows ? (float)dtp[(t + lane) * a.Hv] : 0.f;
+    z = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
   };
   auto commit = [&](const In &r, int buf, int tid) {
     const int lane = tid & 63;
@@ -107,10 +107,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     Gates &g = G[wave];
-    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
+    const GateTotals gt = gates(g, (float)z + bias, A2, a.softplus, lane < rows, lane);
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
     In in;
-    if (step + 1 < nc) fetch(in, step + 1, tid);
+    fetch(in, step + 1 < nc ? step + 1 : step, tid);
     const bf16 *k = Kl[step & 1], *q = Ql[QROWS ? step & 1 : 0], *v = Vl[wave];
     if (MODE == kStates) {
       const int64_t at = ((w.chunk(a, loc, c) * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32) + lane * 8;

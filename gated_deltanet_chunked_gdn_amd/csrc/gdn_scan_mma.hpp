@@ -69,6 +69,14 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
+// dt of lane's token of a chunk (0 past its rows), as it is: converted where
+// it is loaded, or loaded under a branch, it would be waited for there, and
+// with it every load issued before.
+__device__ __forceinline__ bf16 load_dt(const bf16 *dt, int64_t stride, int rows, int lane) {
+  const auto r = raw_buffer(dt, (uint32_t)(((rows - 1) * stride + 1) * 2));
+  return buf_load_elem<bf16>(r, (uint32_t)(lane * stride * 2));
+}
+
 // What a wave keeps of a chunk's steps in LDS, by token: log2 decays summed
 // from the token's half (32 tokens), delta, the decay from the token to the
 // chunk's last (w1) and times delta (w), that of the first half's tokens to
