@@ -132,8 +132,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
   struct In {
     Rows<K, THREADS> k, q;
     Rows<VW, 64> x, dy;
+    bf16 dt;  // of this lane's token
   };
-  bf16 z = (bf16)0.f;  // dt of this lane's token
+  float z = 0.f;
   const int64_t first_chunk = w.chunk(a, loc, 0);
   auto state_at = [&](int c, int lane) {
     return (((first_chunk + c) * a.Hv + h) * (V / 32) + vs) * (K * 32) + lane * 8;
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     r.q.load(cp + t * a.cs, a.cs, rows, tid);
     r.x.load(xp + t * a.xs, a.xs, rows, lane);
     r.dy.load(dp + t * ys, ys, rows, lane);
-    z = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
+    r.dt = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
   };
   auto fetch_state = [&](int c, int lane) {
     const int64_t at = state_at(c, lane);
@@ -162,6 +163,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     r.q.store_pi(Ql, KP, tid);
     r.x.store_pi(Xl[wave], VP, lane);
     r.dy.store_pi(Dl[wave], VP, lane);
+    z = settle((float)r.dt);
   };
   {
     In r;
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     const int64_t t0 = loc.t0 + 64 * (int64_t)c;
     Gates &g = G[wave];
-    const GateTotals gt = gates(g, (float)z + bias, A2, a.softplus, lane < rows, lane);
+    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
     const float eL = gt.all();
     // Y^T = Z^T B^T (rows v, lane token), <S, Z>, and Z out
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
             const int i = i0 + e;
             float E;
             if (it == jt)
-              E = i >= r32 && i < lim ? exp2_hw(gi[e] - gj) : 0.f;
+              E = exp2_if(i >= r32 && i < lim, gi[e] - gj);
             else
               E = gi[e] * uj;
             const float p = P[4 * b + e] * E, wm = p * M[4 * b + e];
@@ -484,7 +486,7 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
           const int i = i0 + e;
           float E;
           if (it == jt)
-            E = i >= r32 && i < lim ? exp2_hw(gi[e] - gj) * dj : 0.f;
+            E = exp2_if(i >= r32 && i < lim, gi[e] - gj) * dj;
           else
             E = gi[e] * uj;
           Nacc[4 * b + e] += E * M[4 * b + e];

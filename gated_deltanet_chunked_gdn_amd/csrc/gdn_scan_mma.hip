@@ -78,8 +78,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
   struct In {
     Rows<K, THREADS> k, q;
     Rows<VW, 64> v;
+    bf16 dt;  // of this lane's token
   };
-  bf16 z = (bf16)0.f;  // dt of this lane's token
+  float z = 0.f;
   auto fetch = [&](In &r, int step, int tid) {
     const int lane = tid & 63, c = REV ? nc - 1 - step : step;
     const int64_t t = loc.t0 + 64 * (int64_t)c;
@@ -87,13 +88,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     r.k.load(bp + t * a.bs, a.bs, rows, tid);
     if (QROWS) r.q.load(cp + t * a.cs, a.cs, rows, tid);
     r.v.load(xp + t * a.xs, a.xs, rows, lane);
-    z = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
+    r.dt = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
   };
   auto commit = [&](const In &r, int buf, int tid) {
     const int lane = tid & 63;
     r.k.store_pi(Kl[buf], KP, tid);
     if (QROWS) r.q.store_pi(Ql[buf], KP, tid);
     r.v.store_pi(Vl[wave], VP, lane);
+    z = settle((float)r.dt);
   };
   if (nc > 0) {
     In r;
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     Gates &g = G[wave];
-    const GateTotals gt = gates(g, (float)z + bias, A2, a.softplus, lane < rows, lane);
+    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
     In in;
     fetch(in, step + 1 < nc ? step + 1 : step, tid);
@@ -181,7 +183,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + i;
-            Pd[4 * b + i] = j <= r32 && j >= first ? Pd[4 * b + i] * (exp2_hw(gi - gj[i]) * dj[i]) : 0.f;
+            Pd[4 * b + i] *= exp2_if(j <= r32 && j >= first, gi - gj[i]) * dj[i];
             if (it) Po[4 * b + i] *= ei * uj[i];
           }
         }

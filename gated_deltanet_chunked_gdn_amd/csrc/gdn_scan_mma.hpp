@@ -64,6 +64,17 @@ struct Rows {
   }
 };
 
+// 2^x where `in`, else 0, without a branch (the compiler makes one of a
+// select around the exponential: 32 a chunk, each a wait of its own).
+__device__ __forceinline__ float exp2_if(bool in, float x) { return exp2_hw(in ? x : -1000.f); }
+// x, ready here: a value on its way from memory is waited for where it is
+// next to the loads it came with, not in the next round of a loop, where the
+// wait would cover every store since.
+__device__ __forceinline__ float settle(float x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // LDS written by a wave is read by other lanes of it after this.
 __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
