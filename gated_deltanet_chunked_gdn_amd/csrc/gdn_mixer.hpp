@@ -101,11 +101,15 @@ constexpr int vec_of() {
 __device__ __forceinline__ float sigmoidf(float z) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
-// log(1 + exp(z)) = max(z, 0) + log1p(exp(-|z|)), finite for every finite z
-// and to fp32's relative accuracy where it is small (there log1p matters: the
-// step sizes of a state-space layer begin at 0.001)
+// log(1 + exp(z)) = max(z, 0) + log1p(t), t = exp(-|z|): finite for every finite
+// z and right to fp32's relative accuracy where it is small (the step sizes of
+// a state-space layer begin at 0.001).  log1p(t) = t log(u) / (u - 1) with u =
+// 1 + t as rounded: the rounding of u cancels in the quotient (Kahan's form of
+// log1p), where log(u) alone would lose t's last digits.
 __device__ __forceinline__ float softplusf(float z) {
-  return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
+  const float t = __expf(-fabsf(z)), u = 1.f + t;
+  const float l = u == 1.f ? t : t * (__logf(u) * __builtin_amdgcn_rcpf(u - 1.f));
+  return fmaxf(z, 0.f) + l;
 }
 
 // a weight held in the problem's type or in fp32

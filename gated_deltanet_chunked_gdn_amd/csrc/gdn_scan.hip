@@ -431,22 +431,25 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 }  // namespace
 }  // namespace scan
 
-// Forward segments: as long as the whole sequence unless that leaves compute
-// units without work, then a multiple of 64 tokens that gives about two waves
-// a SIMD over all heads.  fp32 backward: 64 tokens, because the chain of dg
-// gathers the rounding of every a_t and r_t since the segment's end: over 256
-// tokens the sums over a head (ddt_bias) were off by 4e-5 of their value.
+// Segments: as long as the whole sequence unless that leaves compute units
+// without work, then as many as give each a workgroup of the matrix kernels
+// (bf16, whole chunks of 64) or eight waves of the sweeps (fp32, which walk
+// token by token: down to 16 tokens).  fp32 backward: 64 tokens at the most,
+// because the chain of dg gathers the rounding of every a_t and r_t since the
+// segment's end: over 256 tokens the sums over a head (ddt_bias) were off by
+// 4e-5 of their value.
 ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   ScanArgs a = a0;
-  // workgroups a segment: of the matrix kernels (bf16) one holds a compute
-  // unit, of the sweeps' single waves eight do
+  // workgroups a segment
   const int slices = a.Hv / a.Hq * (a.V / 32);
   const int64_t per = a.dtype == 1 ? (int64_t)a.Hq * (slices / scan::slices_per_block(slices)) : (int64_t)a.Hv * ((a.V + 63) / 64);
   int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
-  seg = bwd && a.dtype != 1 ? 64 : (seg + 63) / 64 * 64;
-  if (seg < 64) seg = 64;
+  const int64_t unit = a.dtype == 1 ? 64 : scan::TB;
+  seg = (seg + unit - 1) / unit * unit;
+  if (seg < unit) seg = unit;
+  if (bwd && a.dtype != 1 && seg > 64) seg = 64;
   ScanPlan p;
   p.seg = (int)seg;
   a.slots = p.slots = scan::slots_of(a.s, p.seg);
