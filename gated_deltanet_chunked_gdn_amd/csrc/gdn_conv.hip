@@ -41,14 +41,7 @@ __device__ __forceinline__ void load_row(Vec<E, VEC> &r, const ConvArgs &a, cons
 template <typename E, int VEC, int W>
 struct Taps {
   float w[W][VEC], b[VEC];
-  __device__ __forceinline__ Taps(const ConvArgs &a, int c0) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[j][i] = load_w(a.w, (int64_t)(c0 + i) * W + j, a.wdtype);
-      b[i] = a.bias ? load_w(a.bias, c0 + i, a.wdtype) : 0.f;
-    }
-  }
+  __device__ __forceinline__ Taps(const ConvArgs &a, int c0) { load_taps(w, b, a.w, a.bias, c0, a.wdtype); }
 };
 
 // A workgroup is `subs` token tiles of `tt` tokens times 256 / subs groups of
@@ -341,14 +334,16 @@ __global__ void conv_step_kernel(ConvStepArgs a, int cblocks) {
   }
   E *st = static_cast<E *>(a.state) + slot * (W - 1) * a.D + c0;
   Vec<E, VEC> win[W], out;
+  float w[W][VEC], b[VEC];
+  load_taps(w, b, a.w, a.bias, c0, a.wdtype);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) win[j].load(st + (int64_t)j * a.D);
   win[W - 1].load(static_cast<const E *>(a.x) + row * a.xs + c0);
 #pragma unroll
   for (int k = 0; k < VEC; ++k) {
-    float p = a.bias ? load_w(a.bias, c0 + k, a.wdtype) : 0.f;
+    float p = b[k];
 #pragma unroll
-    for (int j = 0; j < W; ++j) p += load_w(a.w, (int64_t)(c0 + k) * W + j, a.wdtype) * win[j].v[k];
+    for (int j = 0; j < W; ++j) p += w[j][k] * win[j].v[k];
     out.v[k] = a.silu ? silu(p) : p;
   }
   out.store(y);
@@ -459,7 +454,7 @@ static bool wide4(const ConvArgs &a, std::initializer_list<const void *> rows) {
   const uintptr_t mask = a.dtype == 1 ? 7 : 15;
   for (const void *p : rows)
     if ((uintptr_t)p & mask) return false;
-  return a.D % 4 == 0 && a.xs % 4 == 0;
+  return a.D % 4 == 0 && a.xs % 4 == 0 && rows16(a.w) && rows16(a.bias);
 }
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t st) {
   return dispatch<GoFwd, 4>(a.dtype, wide4(a, {a.x, a.y, a.h0, a.ht}), a.W, a, st);
@@ -469,7 +464,8 @@ hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t st) {
 }
 hipError_t launch_conv_step(const ConvStepArgs &a, hipStream_t st) {
   const int vec = a.dtype == 1 ? 8 : 4;
-  const bool wide = a.D % vec == 0 && a.xs % vec == 0 && rows16(a.x) && rows16(a.y) && rows16(a.state);
+  const bool wide = a.D % vec == 0 && a.xs % vec == 0 && rows16(a.x) && rows16(a.y) && rows16(a.state) &&
+                    rows16(a.w) && rows16(a.bias);
   return dispatch<GoStep, 8>(a.dtype, wide, a.W, a, st);
 }
 

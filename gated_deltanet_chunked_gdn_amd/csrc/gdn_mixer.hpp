@@ -148,6 +148,25 @@ __device__ __forceinline__ void load_ws(float (&r)[VEC], const void *p, int64_t 
   }
 }
 
+// The W taps and the bias of VEC channels from c0 on ([D, W] and [D]), by
+// channel.
+template <int VEC, int W>
+__device__ __forceinline__ void load_taps(float (&w)[W][VEC], float (&b)[VEC], const void *wp, const void *bp, int c0,
+                                          int wdtype) {
+  load_ws<VEC>(b, bp, c0, wdtype, 0.f);
+  if constexpr (VEC == 1) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][0] = load_w(wp, (int64_t)c0 * W + j, wdtype);
+  } else {
+    float t[VEC * W];
+    load_ws<VEC * W>(t, wp, (int64_t)c0 * W, wdtype, 0.f);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = t[i * W + j];
+  }
+}
+
 // Sums of `n` columns over `parts` rows, in an order that does not depend on
 // the launch: a workgroup of 512 has 32 columns, 16 rows at a time (a single
 // thread a column takes a load's latency for every row: 234 us for 1024 rows

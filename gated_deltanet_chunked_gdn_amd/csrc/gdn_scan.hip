@@ -432,8 +432,8 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 }  // namespace scan
 
 // Segments: as long as the whole sequence unless that leaves compute units
-// without work, then as many as give each a workgroup of the matrix kernels
-// (bf16, whole chunks of 64) or eight waves of the sweeps (fp32, which walk
+// without work, then as many as give each two workgroups of the matrix
+// kernels (bf16, whole chunks of 64) or eight waves of the sweeps (fp32, which walk
 // token by token: down to 16 tokens).  fp32 backward: 64 tokens at the most,
 // because the chain of dg gathers the rounding of every a_t and r_t since the
 // segment's end: over 256 tokens the sums over a head (ddt_bias) were off by
@@ -443,7 +443,7 @@ ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   // workgroups a segment
   const int slices = a.Hv / a.Hq * (a.V / 32);
   const int64_t per = a.dtype == 1 ? (int64_t)a.Hq * (slices / scan::slices_per_block(slices)) : (int64_t)a.Hv * ((a.V + 63) / 64);
-  int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 8) + per - 1) / per;  // segments over the whole batch
+  int64_t want = (compute_units() * (a.dtype == 1 ? 2 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
   const int64_t unit = a.dtype == 1 ? 64 : scan::TB;

@@ -101,12 +101,11 @@ __device__ __forceinline__ void put_rows(const f32x16 &acc, float skip, const bf
 __device__ __forceinline__ int next_bit(uint32_t m) { return m ? __builtin_ctz(m) : 32; }
 
 template <int K, int V, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+__global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, int blocks_per_group) {
   using D = Dims<K, V>;
   constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
   __shared__ __align__(16) bf16 Ql[64 * KP], Kl[64 * KP], Xl[NW][64 * VP], Dl[NW][64 * VP];
-  __shared__ __align__(16) Gates G[NW];
-  __shared__ float Sa[NW][64], Sr[NW][64], Sm[NW][64];
+  __shared__ __align__(16) GatesCore G[NW];
   const int tid0 = threadIdx.x, wave = wave_of(tid0);
   const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
   const int blk = (int)(item % blocks_per_group), hq = (int)(item / blocks_per_group % a.Hq);
@@ -176,9 +175,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     const int64_t t0 = loc.t0 + 64 * (int64_t)c;
-    Gates &g = G[wave];
+    GatesCore &g = G[wave];
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
+    const int64_t sums = ((int64_t)vs * a.Hv + h) * a.s.tokens + t0;  // of a_part, r_part, m_part
     const float eL = gt.all();
     // Y^T = Z^T B^T (rows v, lane token), <S, Z>, and Z out
     f32x16 Y[2] = {zero16(), zero16()};
@@ -281,36 +281,26 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void grad_kernel(ScanArgs
       }
       rs += __shfl_xor(rs, 32);
       ms += __shfl_xor(ms, 32);
-      if (h2 == 0) {
-        Sr[wave][tj] = rs + ri[jt];
-        Sm[wave][tj] = ms;
+      if (h2 == 0 && tj < rows) {
+        w.r_part(a)[sums + tj] = rs + ri[jt];
+        w.m_part(a)[sums + tj] = ms;
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) T[i] *= dj;
       put_rows(T, skip, dy + tj * VP, out, tj < rows ? (uint32_t)(tj * ys * 2) : kOutside, h2);
       __builtin_amdgcn_sched_barrier(0);
     }
-    wave_lds_fence();
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
       const float v = fold16(ar[it], lane);
       const int i = 32 * it + 8 * ((lane & 15) >> 2) + 4 * h2 + (lane & 3);
-      if (!(lane & 16)) Sa[wave][i] = v;
+      if (!(lane & 16) && i < rows) w.a_part(a)[sums + i] = v;
     }
-    wave_lds_fence();
     dD = wave_sum(dD);
-    {
-      const int64_t hs = (int64_t)vs * a.Hv + h;
-      if (lane < rows) {
-        w.a_part(a)[hs * a.s.tokens + t0 + lane] = Sa[wave][lane];
-        w.r_part(a)[hs * a.s.tokens + t0 + lane] = Sr[wave][lane];
-        w.m_part(a)[hs * a.s.tokens + t0 + lane] = Sm[wave][lane];
-      }
-      if (lane == 0) {
-        const int64_t i = ((int64_t)vs * w.chunks + first_chunk + c) * a.Hv + h;
-        w.x_part(a)[i] = xo;
-        w.dd_part(a)[i] = dD;
-      }
+    if (lane == 0) {
+      const int64_t i = ((int64_t)vs * w.chunks + first_chunk + c) * a.Hv + h;
+      w.x_part(a)[i] = xo;
+      w.dd_part(a)[i] = dD;
     }
     In in;
     fetch(in, c > 0 ? c - 1 : 0, tid);
@@ -642,9 +632,7 @@ hipError_t go(const ScanArgs &a, const Layout &w, hipStream_t st) {
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   {
     KernelTimer kt("scan_grad", st);
-    if (nw == 8)
-      grad_kernel<K, V, 8><<<blocks, 512, 0, st>>>(a, w, per / 8);
-    else if (nw == 4)
+    if (nw == 4)
       grad_kernel<K, V, 4><<<blocks, 256, 0, st>>>(a, w, per / 4);
     else if (nw == 2)
       grad_kernel<K, V, 2><<<blocks, 128, 0, st>>>(a, w, per / 2);

@@ -6,13 +6,12 @@
 //   S'  = 2^{gamma_L} S + sum_j b_j (2^{gamma_L - gamma_j} delta_j x_j)^T
 //
 // A wave owns 32 columns of one head's state and a segment's chunks in order;
-// the waves of a workgroup (8 where the group has as many) are column slices
-// of a head group, which share c and b: the workgroup stages those for the
-// next chunk while it works on this one, and no wave waits for another but at
-// the one barrier a chunk.  (64 columns a wave form B C^T half as often, but
-// then the state needs the accumulation registers, which vector instructions
-// reach only by moves, and one wave a SIMD leaves its latencies open: 171 us
-// against the 8-wave form's time at 8192 tokens x 64 heads.)
+// the waves of a workgroup are column slices of a head group, which share c
+// and b in LDS, the next chunk's rows on their way while one is worked on.
+// Two workgroups of four waves a compute unit fill each other's gaps.  (At
+// 8192 tokens x 64 heads, K 128, V 64: one wave a SIMD with 64 columns 171 us,
+// the state in accumulation registers that vector instructions reach only by
+// moves; eight waves in one workgroup 66 us.)
 //
 // Everything is arranged so that accumulators are operands without moving
 // (gdn_slice.hpp): S tiles (rows k, lane v) give S^T for c; C B^T is formed
@@ -40,11 +39,11 @@ namespace {
 enum { kLocal, kOut, kStates, kRLocal };
 
 template <int K, int V, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+__global__ __launch_bounds__(64 * NW, 2) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
   constexpr bool OUT = MODE == kOut, REV = MODE == kRLocal, QROWS = OUT || MODE == kStates;
   using D = Dims<K, V>;
   constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
-  __shared__ __align__(16) bf16 Kl[2][64 * KP], Ql[QROWS ? 2 : 1][QROWS ? 64 * KP : 8], Vl[NW][64 * VP];
+  __shared__ __align__(16) bf16 Kl[64 * KP], Ql[QROWS ? 64 * KP : 8], Vl[NW][64 * VP];
   __shared__ __align__(16) Gates G[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), h2 = lane >> 5, r32 = lane & 31;
   const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
@@ -90,17 +89,17 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     r.v.load(xp + t * a.xs, a.xs, rows, lane);
     r.dt = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
   };
-  auto commit = [&](const In &r, int buf, int tid) {
+  auto commit = [&](const In &r, int tid) {
     const int lane = tid & 63;
-    r.k.store_pi(Kl[buf], KP, tid);
-    if (QROWS) r.q.store_pi(Ql[buf], KP, tid);
+    r.k.store_pi(Kl, KP, tid);
+    if (QROWS) r.q.store_pi(Ql, KP, tid);
     r.v.store_pi(Vl[wave], VP, lane);
     z = settle((float)r.dt);
   };
   if (nc > 0) {
     In r;
     fetch(r, 0, tid);
-    commit(r, 0, tid);
+    commit(r, tid);
   }
   __syncthreads();
   float total = 0.f;
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
     In in;
     fetch(in, step + 1 < nc ? step + 1 : step, tid);
-    const bf16 *k = Kl[step & 1], *q = Ql[QROWS ? step & 1 : 0], *v = Vl[wave];
+    const bf16 *k = Kl, *q = Ql, *v = Vl[wave];
     if (MODE == kStates) {
       const int64_t at = ((w.chunk(a, loc, c) * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32) + lane * 8;
       bf16x4 dyv[2][4];  // dy of this lane's tokens, columns 8 b + 4 h ..
@@ -233,7 +232,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void mma_kernel(ScanArgs 
         S[kt] = mma32(kf, x.lo, S[kt]);
       }
     }
-    if (step + 1 < nc) commit(in, (step + 1) & 1, tid);
+    __syncthreads();  // every wave is done with b and c
+    commit(in, tid);
     __syncthreads();
   }
   if (MODE == kLocal || REV) {
@@ -252,9 +252,7 @@ hipError_t go(const char *name, const ScanArgs &a, const Layout &w, hipStream_t 
   const int nw = slices_per_block(per);
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   KernelTimer kt(name, st);
-  if (nw == 8)
-    mma_kernel<K, V, 8, MODE><<<blocks, 512, 0, st>>>(a, w, per / 8);
-  else if (nw == 4)
+  if (nw == 4)
     mma_kernel<K, V, 4, MODE><<<blocks, 256, 0, st>>>(a, w, per / 4);
   else if (nw == 2)
     mma_kernel<K, V, 2, MODE><<<blocks, 128, 0, st>>>(a, w, per / 2);

@@ -99,8 +99,11 @@ __device__ __forceinline__ bf16 load_dt(const bf16 *dt, int64_t stride, int rows
 // exact 0 and stays out of the sums, where it would cost the differences
 // between later tokens their digits; m0, m1 mark such tokens of the halves.
 constexpr float kForget = -27.f;
-struct Gates {
-  float gam[64], del[64], w[64], w1[64], p[64], u[32], u1[32], e[32];
+struct GatesCore {
+  float gam[64], del[64], w1[64], p[64], u1[32], e[32];
+};
+struct Gates : GatesCore {
+  float w[64], u[32];
 };
 struct GateTotals {
   float t0, t1;     // the halves' sums of log2 decays
@@ -112,7 +115,8 @@ __device__ __forceinline__ uint32_t upto(uint32_t m, int i) { return m & (0xFFFF
 __device__ __forceinline__ uint32_t above(uint32_t m, int i) { return m & ~(0xFFFFFFFFu >> (31 - i)); }
 __device__ __forceinline__ int last_bit(uint32_t m) { return m ? 31 - __builtin_clz(m) : 0; }
 
-__device__ __forceinline__ GateTotals gates(Gates &s, float z, float A2, bool softplus, bool live, int lane) {
+template <typename G>
+__device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softplus, bool live, int lane) {
   const float d = live ? (softplus ? softplusf(z) : z) : 0.f;
   const float g = d * A2;
   const bool cut = g < kForget;
@@ -127,11 +131,11 @@ __device__ __forceinline__ GateTotals gates(Gates &s, float z, float A2, bool so
   s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam : t.t0 + gam);
   const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? (t.t0 - gam) + t.t1 : t.t1 - gam);
   s.w1[lane] = w1;
-  s.w[lane] = w1 * d;
+  if constexpr (sizeof(G) == sizeof(Gates)) s.w[lane] = w1 * d;
   if (lane < 32) {
     const float u1 = later ? 0.f : exp2_hw(t.t0 - gam);
     s.u1[lane] = u1;
-    s.u[lane] = u1 * d;
+    if constexpr (sizeof(G) == sizeof(Gates)) s.u[lane] = u1 * d;
   } else {
     s.e[lane - 32] = upto(t.m1, i) ? 0.f : exp2_hw(gam);
   }
@@ -180,7 +184,8 @@ __device__ __forceinline__ float acc_dot(const f32x16 &acc, const bf16x4 (&x)[4]
 template <int K, int V>
 struct Dims {
   static constexpr int VW = 32, KT = K / 32;
-  static constexpr int KP = K + 16, VP = VW + 16;  // LDS row pitches
+  // LDS row pitches: 16-byte reads of 16 consecutive rows meet every bank once
+  static constexpr int KP = K + 8, VP = VW + 8;
   typedef f32x16 State[KT];                        // rows k, lane v
 };
 

@@ -18,7 +18,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWavesPerGroup = 4;
+constexpr int kMostWaves = 4;  // of a workgroup
 
 // Sum over the 8 row lanes (lane bits 3, 4, 5).
 __device__ __forceinline__ float rows_sum(float v) {
@@ -43,11 +43,11 @@ __device__ __forceinline__ void load_n(float (&r)[N], const E *p) {
 }
 
 template <typename E, int K, bool DELTA>
-__global__ __launch_bounds__(64 * kWavesPerGroup) void step_kernel(StepArgs a) {
+__global__ __launch_bounds__(64 * kMostWaves) void step_kernel(StepArgs a) {
   constexpr int R = K / 8;  // rows a lane
   const int lane = threadIdx.x & 63, cl = lane & 7, rl = lane >> 3;
   const int slices = a.V >> 5;
-  const int64_t unit = (int64_t)blockIdx.x * kWavesPerGroup + wave_of(threadIdx.x);
+  const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 6) + wave_of(threadIdx.x);
   const int sl = (int)(unit % slices), h = (int)(unit / slices % a.Hv);
   const int64_t row = unit / slices / a.Hv;
   if (row >= a.B) return;
@@ -142,13 +142,15 @@ __global__ __launch_bounds__(64 * kWavesPerGroup) void step_kernel(StepArgs a) {
 template <typename E, int K>
 hipError_t go(const StepArgs &a, hipStream_t st) {
   const int64_t units = (int64_t)a.B * a.Hv * (a.V / 32);
-  const unsigned blocks = (unsigned)((units + kWavesPerGroup - 1) / kWavesPerGroup);
+  // a compute unit each while there are no more waves than those
+  const int waves = units > compute_units() ? kMostWaves : 1;
+  const unsigned blocks = (unsigned)((units + waves - 1) / waves);
   if (a.delta) {
     KernelTimer kt("delta_step", st);
-    step_kernel<E, K, true><<<blocks, 64 * kWavesPerGroup, 0, st>>>(a);
+    step_kernel<E, K, true><<<blocks, 64 * waves, 0, st>>>(a);
   } else {
     KernelTimer kt("scan_step", st);
-    step_kernel<E, K, false><<<blocks, 64 * kWavesPerGroup, 0, st>>>(a);
+    step_kernel<E, K, false><<<blocks, 64 * waves, 0, st>>>(a);
   }
   return hipGetLastError();
 }

@@ -14,13 +14,12 @@ for the device and can be captured into a graph.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 
-from . import GDN_BF16, GDN_F32, GdnError, GdnProblem, _check, _check_device, _check_state, _contig, _ptr, last_error
+from . import GDN_BF16, GDN_F32, GdnError, GdnProblem, _check, _check_device, _check_state, _contig, last_error
 from . import lib as _base_lib
 
 _I32, _I64, _P, _S = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
@@ -134,15 +133,20 @@ def _rows(t, lead: int):
     return t.contiguous(), inner
 
 
-def _on(device):
-    """The device whose stream takes the launch, made current if it is not."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _call(f, device, *args):
+    """f(*args, stream) on the current stream of `device`, which is made current if it is not."""
+    i = device.index
+    if i == torch._C._cuda_getDevice():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc:
+        _check(rc)
 
 
 def _workspace(n, device):
@@ -207,9 +211,7 @@ def causal_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, a
     p.cu_seqlens, p.cu_seqlens_host = sq.ptrs()
     y = torch.empty(B, T, D, device=dev, dtype=x.dtype)
     ht = torch.empty(sq.N, p.W - 1, D, device=dev, dtype=x.dtype) if output_final_state else None
-    with _on(dev):
-        _check(lib().gdn_causal_conv_fwd(ctypes.byref(p), _ptr(xr), _ptr(weight), _ptr(bias), _ptr(h0), _ptr(y),
-                                         _ptr(ht), _stream(dev)))
+    _call(lib().gdn_causal_conv_fwd, dev, ctypes.byref(p), _p(xr), _p(weight), _p(bias), _p(h0), _p(y), _p(ht))
     return y, ht
 
 
@@ -238,9 +240,8 @@ def causal_conv_bwd(x, weight, bias, dy, initial_state=None, dfinal_state=None, 
     L = lib()
     n = L.gdn_causal_conv_bwd_workspace_size(ctypes.byref(p))
     ws = _workspace(n, dev)
-    with _on(dev):
-        _check(L.gdn_causal_conv_bwd(ctypes.byref(p), _ptr(xr), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(h0), _ptr(dht),
-                                     _ptr(dx), _ptr(dw), _ptr(db), _ptr(dh0), _ptr(ws), n, _stream(dev)))
+    _call(L.gdn_causal_conv_bwd, dev, ctypes.byref(p), _p(xr), _p(weight), _p(bias), _p(dy), _p(h0), _p(dht),
+          _p(dx), _p(dw), _p(db), _p(dh0), _p(ws), n)
     return dx, dw, db, dh0
 
 
@@ -259,9 +260,8 @@ def causal_conv_step(x, state, weight, bias=None, activation: Optional[str] = "s
     _check_device(x, state, weight, bias, idx)
     dev = x.device
     y = torch.empty(B, D, device=dev, dtype=x.dtype)
-    with _on(dev):
-        _check(lib().gdn_causal_conv_step(ctypes.byref(p), _ptr(xr), _ptr(state), _ptr(weight), _ptr(bias), _ptr(idx),
-                                          state.shape[0], _ptr(y), _stream(dev)))
+    _call(lib().gdn_causal_conv_step, dev, ctypes.byref(p), _p(xr), _p(state), _p(weight), _p(bias), _p(idx),
+          state.shape[0], _p(y))
     return y
 
 
@@ -313,9 +313,8 @@ def selective_scan_fwd(c, b, x, dt, A, D=None, dt_bias=None, dt_softplus: bool =
     L = lib()
     n = L.gdn_selective_scan_fwd_workspace_size(ctypes.byref(p))
     ws = _workspace(n, dev)
-    with _on(dev):
-        _check(L.gdn_selective_scan_fwd(ctypes.byref(p), _ptr(c), _ptr(b), _ptr(x), _ptr(dt), _ptr(A), _ptr(D),
-                                        _ptr(dt_bias), _ptr(h0), _ptr(y), _ptr(ht), _ptr(ws), n, _stream(dev)))
+    _call(L.gdn_selective_scan_fwd, dev, ctypes.byref(p), _p(c), _p(b), _p(x), _p(dt), _p(A), _p(D),
+          _p(dt_bias), _p(h0), _p(y), _p(ht), _p(ws), n)
     return y, ht
 
 
@@ -343,11 +342,9 @@ def selective_scan_bwd(c, b, x, dt, A, dy, dht=None, D=None, dt_bias=None, dt_so
     L = lib()
     n = L.gdn_selective_scan_bwd_workspace_size(ctypes.byref(p))
     ws = _workspace(n, dev)
-    with _on(dev):
-        _check(L.gdn_selective_scan_bwd(
-            ctypes.byref(p), _ptr(c), _ptr(b), _ptr(x), _ptr(dt), _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(h0), _ptr(dy),
-            _ptr(dht), _ptr(dc), _ptr(db), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dD), _ptr(dbias), _ptr(dh0), _ptr(ws), n,
-            _stream(dev)))
+    _call(L.gdn_selective_scan_bwd, dev, ctypes.byref(p), _p(c), _p(b), _p(x), _p(dt), _p(A), _p(D),
+          _p(dt_bias), _p(h0), _p(dy), _p(dht), _p(dc), _p(db), _p(dx), _p(ddt), _p(dA), _p(dD), _p(dbias),
+          _p(dh0), _p(ws), n)
     return dc, db, dx, ddt, dA, dD, dbias, dh0
 
 
@@ -366,10 +363,8 @@ def selective_scan_step(c, b, x, dt, A, state, D=None, dt_bias=None, dt_softplus
     _check_device(x, c, b, dt, A, D, dt_bias, state, idx)
     dev = x.device
     y = torch.empty(x.shape, device=dev, dtype=x.dtype)
-    with _on(dev):
-        _check(lib().gdn_selective_scan_step(
-            ctypes.byref(p), _ptr(c), _ptr(b), _ptr(x), _ptr(dt), _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(state), _ptr(idx),
-            state.shape[0], _ptr(y), _stream(dev)))
+    _call(lib().gdn_selective_scan_step, dev, ctypes.byref(p), _p(c), _p(b), _p(x), _p(dt), _p(A), _p(D),
+          _p(dt_bias), _p(state), _p(idx), state.shape[0], _p(y))
     return y
 
 
@@ -400,9 +395,8 @@ def gated_delta_rule_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_
     o = torch.empty(B, Hv, V, device=dev, dtype=v.dtype)
     p = GdnProblem(B, 1, Hq, Hv, K, V, B, dt, float(K ** -0.5 if scale is None else scale), None, None, -1,
                    int(bool(use_qk_l2norm_in_kernel)))
-    with _on(dev):
-        _check(lib().gdn_delta_rule_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), qs, ks, vs,
-                                         _ptr(state), _ptr(idx), state.shape[0], _ptr(o), _stream(dev)))
+    _call(lib().gdn_delta_rule_step, dev, ctypes.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta), qs, ks, vs,
+          _p(state), _p(idx), state.shape[0], _p(o))
     return o
 
 
@@ -435,9 +429,8 @@ def layer_norm_fwd(x, weight=None, bias=None, gate=None, eps: float = 1e-5, rms:
     y = torch.empty_like(x)
     mean = None if rms else torch.empty(x.shape[:-1], device=dev, dtype=torch.float32)
     rstd = torch.empty(x.shape[:-1], device=dev, dtype=torch.float32)
-    with _on(dev):
-        _check(lib().gdn_layer_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y),
-                                        _ptr(mean), _ptr(rstd), _stream(dev)))
+    _call(lib().gdn_layer_norm_fwd, dev, ctypes.byref(p), _p(x), _p(weight), _p(bias), _p(gate), _p(y),
+          _p(mean), _p(rstd))
     return y, mean, rstd
 
 
@@ -460,7 +453,6 @@ def layer_norm_bwd(dy, x, weight, bias, mean, rstd, gate=None, rms: bool = False
     L = lib()
     n = L.gdn_layer_norm_bwd_workspace_size(ctypes.byref(p))
     ws = _workspace(n, dev)
-    with _on(dev):
-        _check(L.gdn_layer_norm_bwd(ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(mean),
-                                    _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), _ptr(dgate), _ptr(ws), n, _stream(dev)))
+    _call(L.gdn_layer_norm_bwd, dev, ctypes.byref(p), _p(dy), _p(x), _p(weight), _p(bias), _p(gate), _p(mean),
+          _p(rstd), _p(dx), _p(dw), _p(db), _p(dgate), _p(ws), n)
     return dx, dw, db, dgate
