@@ -31,7 +31,8 @@ namespace gdn {
 namespace scan {
 namespace {
 
-constexpr int TB = 16;  // tokens staged at a time
+constexpr int TB = 16;      // tokens staged at a time
+constexpr int kAhead = 8;  // segments whose states a carry has in flight
 
 // What a sweep does.  Lane operand L (one value a lane and token), uniform
 // operands U (the update's other factor) and P (the output's factor):
@@ -176,9 +177,8 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
 // The segments' local ends -> every segment's start state (in place), and in
 // the backward the sequence's last state.  One thread has 4 elements of one
 // head's state.
-__global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float *hend) {
+__device__ __forceinline__ void carry(const ScanArgs &a, const Layout &w, float *hend, int64_t i) {
   const int64_t kv4 = (int64_t)a.K * a.V / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
   if (n >= a.s.N) return;
   const Span sp = seq_span(a.s, (int)n);
@@ -186,27 +186,35 @@ __global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float 
   f32x4 cur = zero4();
   const int64_t own = (n * a.Hv + h) * kv4 + e;
   if (a.h0) cur = reinterpret_cast<const f32x4 *>(a.h0)[own];
-  f32x4 *H = reinterpret_cast<f32x4 *>(w.start(a)) + h * kv4 + e;
-  for (int64_t s = 0; s < ns; ++s) {
-    f32x4 *p = H + (slot + s) * a.Hv * kv4;
-    f32x4 x = zero4();
-    float d = 0.f;
-    if (s < ns - 1 || w.need_last) {
-      x = *p;
-      d = expf(w.decay(a)[(slot + s) * a.Hv + h]);
-    }
-    *p = cur;
+  f32x4 *H = reinterpret_cast<f32x4 *>(w.start(a)) + (slot * a.Hv + h) * kv4 + e;
+  const float *g = w.decay(a) + slot * a.Hv + h;
+  const int64_t step = a.Hv * kv4, read = w.need_last ? ns : ns - 1;  // segments whose own state is there
+  for (int64_t s = 0; s < ns; s += kAhead) {
+    f32x4 x[kAhead];
+    float d[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cur[j] = d * cur[j] + x[j];
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t t = s + j < read ? s + j : 0;
+      x[j] = H[t * step];
+      d[j] = g[t * a.Hv];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (s + j >= ns) break;
+      H[(s + j) * step] = cur;
+      if (s + j >= read) break;
+      const float f = expf(d[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cur[k] = f * cur[k] + x[j][k];
+    }
   }
   if (hend) reinterpret_cast<f32x4 *>(hend)[own] = cur;
 }
 
 // In reverse: every segment's local gradient of its start state -> the
 // gradient of its last state from what follows it (in place), and dh0.
-__global__ __launch_bounds__(256) void rcarry_kernel(ScanArgs a, Layout w) {
+__device__ __forceinline__ void rcarry(const ScanArgs &a, const Layout &w, int64_t i) {
   const int64_t kv4 = (int64_t)a.K * a.V / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
   if (n >= a.s.N) return;
   const Span sp = seq_span(a.s, (int)n);
@@ -214,16 +222,37 @@ __global__ __launch_bounds__(256) void rcarry_kernel(ScanArgs a, Layout w) {
   f32x4 cur = zero4();
   const int64_t own = (n * a.Hv + h) * kv4 + e;
   if (a.dht) cur = reinterpret_cast<const f32x4 *>(a.dht)[own];
-  f32x4 *Z = reinterpret_cast<f32x4 *>(w.zend(a)) + h * kv4 + e;
-  for (int64_t s = ns - 1; s >= 0; --s) {
-    f32x4 *p = Z + (slot + s) * a.Hv * kv4;
-    const float d = expf(w.decay(a)[(slot + s) * a.Hv + h]);
-    const f32x4 x = *p;
-    *p = cur;
+  f32x4 *Z = reinterpret_cast<f32x4 *>(w.zend(a)) + (slot * a.Hv + h) * kv4 + e;
+  const float *g = w.decay(a) + slot * a.Hv + h;
+  const int64_t step = a.Hv * kv4;
+  for (int64_t s = ns - 1; s >= 0; s -= kAhead) {
+    f32x4 x[kAhead];
+    float d[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cur[j] = d * cur[j] + x[j];
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t t = s - j > 0 ? s - j : 0;
+      x[j] = Z[t * step];
+      d[j] = g[t * a.Hv];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (s - j < 0) break;
+      Z[(s - j) * step] = cur;
+      const float f = expf(d[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cur[k] = f * cur[k] + x[j][k];
+    }
   }
   if (a.dh0) reinterpret_cast<f32x4 *>(a.dh0)[own] = cur;
+}
+
+// Both in one launch where there are both (`blocks` workgroups each).
+__global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float *hend, int64_t blocks) {
+  const int64_t b = blockIdx.x;
+  if (b < blocks)
+    carry(a, w, hend, b * 256 + threadIdx.x);
+  else
+    rcarry(a, w, (b - blocks) * 256 + threadIdx.x);
 }
 
 // dg from a_t, r_t and m_t, then ddt and the segment's part of dA, ddt_bias and
@@ -358,7 +387,7 @@ hipError_t fwd(const ScanArgs &a, hipStream_t st) {
     e = sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return sweep<E, kOut>("scan_out", a, w, out, a.K, st);
@@ -370,7 +399,7 @@ hipError_t fwd_mma(const ScanArgs &a, hipStream_t st) {
     hipError_t e = launch_mma_local(a, w, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return launch_mma_out(a, w, st);
@@ -379,11 +408,10 @@ hipError_t fwd_mma(const ScanArgs &a, hipStream_t st) {
 hipError_t bwd_mma(const ScanArgs &a, hipStream_t st) {
   const Layout w = layout(a, true);
   hipError_t e;
-  if ((e = launch_mma_local(a, w, st)) != hipSuccess || (e = launch_mma_rlocal(a, w, st)) != hipSuccess) return e;
+  if ((e = launch_mma_locals(a, w, st)) != hipSuccess) return e;
   {
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr);
-    rcarry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w);
+    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if ((e = launch_mma_states(a, w, st)) != hipSuccess) return e;
@@ -405,8 +433,7 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
   GDN_DO((sweep<E, kRLocal>("scan_rlocal", a, w, dx, a.K, st)));
   {
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, w.hend(a));
-    rcarry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w);
+    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, w.hend(a), carry_blocks(a));
     GDN_DO(hipGetLastError());
   }
   GDN_DO((sweep<E, kDc>("scan_dc", a, w, dc, a.V, st)));

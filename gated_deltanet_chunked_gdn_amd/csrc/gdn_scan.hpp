@@ -128,7 +128,7 @@ inline int slices_per_block(int per) { return per % 4 == 0 ? 4 : per % 2 == 0 ? 
 hipError_t launch_mma_local(const ScanArgs &a, const Layout &w, hipStream_t st);
 hipError_t launch_mma_out(const ScanArgs &a, const Layout &w, hipStream_t st);
 hipError_t launch_mma_states(const ScanArgs &a, const Layout &w, hipStream_t st);
-hipError_t launch_mma_rlocal(const ScanArgs &a, const Layout &w, hipStream_t st);
+hipError_t launch_mma_locals(const ScanArgs &a, const Layout &w, hipStream_t st);
 // bf16, gdn_scan_bwd.hip
 hipError_t launch_mma_grad(const ScanArgs &a, const Layout &w, hipStream_t st);
 

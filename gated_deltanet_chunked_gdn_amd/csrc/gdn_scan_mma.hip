@@ -38,15 +38,20 @@ namespace {
 //            outputs; a.b, a.x hold c and dy: Z = 2^{gamma_L} Z + C^T (2^{gamma} dY)
 enum { kLocal, kOut, kStates, kRLocal };
 
-template <int K, int V, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW, 2) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+template <int K, int NW, bool QROWS>
+struct Lds {
+  bf16 k[64 * (K + 8)], q[QROWS ? 64 * (K + 8) : 8], v[NW][64 * 40];
+  Gates g[NW];
+};
+
+template <int K, int V, int NW, int MODE, typename L>
+__device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int blocks_per_group, int64_t item, L &lds) {
   constexpr bool OUT = MODE == kOut, REV = MODE == kRLocal, QROWS = OUT || MODE == kStates;
   using D = Dims<K, V>;
   constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
-  __shared__ __align__(16) bf16 Kl[64 * KP], Ql[QROWS ? 64 * KP : 8], Vl[NW][64 * VP];
-  __shared__ __align__(16) Gates G[NW];
+  static_assert(KP == K + 8 && VP == 40, "row pitches of Lds");
+  bf16 *const Kl = lds.k, *const Ql = lds.q;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), h2 = lane >> 5, r32 = lane & 31;
-  const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
   const int blk = (int)(item % blocks_per_group), hq = (int)(item / blocks_per_group % a.Hq);
   const int64_t slot = item / blocks_per_group / a.Hq;
   const SlotLoc loc = locate(a, slot);
@@ -93,7 +98,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mma_kernel(ScanArgs a, Layout w, i
     const int lane = tid & 63;
     r.k.store_pi(Kl, KP, tid);
     if (QROWS) r.q.store_pi(Ql, KP, tid);
-    r.v.store_pi(Vl[wave], VP, lane);
+    r.v.store_pi(lds.v[wave], VP, lane);
     z = settle((float)r.dt);
   };
   if (nc > 0) {
@@ -107,12 +112,12 @@ __global__ __launch_bounds__(64 * NW, 2) void mma_kernel(ScanArgs a, Layout w, i
     const int c = REV ? nc - 1 - step : step;
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
-    Gates &g = G[wave];
+    Gates &g = lds.g[wave];
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
     In in;
     fetch(in, step + 1 < nc ? step + 1 : step, tid);
-    const bf16 *k = Kl, *q = Ql, *v = Vl[wave];
+    const bf16 *k = Kl, *q = Ql, *v = lds.v[wave];
     if (MODE == kStates) {
       const int64_t at = ((w.chunk(a, loc, c) * a.Hv + h) * (V / 32) + v0 / 32) * (K * 32) + lane * 8;
       bf16x4 dyv[2][4];  // dy of this lane's tokens, columns 8 b + 4 h ..
@@ -240,9 +245,43 @@ __global__ __launch_bounds__(64 * NW, 2) void mma_kernel(ScanArgs a, Layout w, i
     if (REV && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
     float *dst = (REV ? w.zend(a) : w.start(a)) + (slot * a.Hv + h) * kv + v0;
     state_io<K, V>(S, dst, true, lane);
-    if (MODE == kLocal && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
+    // (in the backward the reverse pass has the decays: one writer)
+    if (MODE == kLocal && w.chunks == 0 && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
   } else if (OUT && a.ht && loc.last) {
     state_io<K, V>(S, a.ht + (loc.n * (int64_t)a.Hv + h) * kv + v0, true, lane);
+  }
+}
+
+template <int K, int V, int NW, int MODE>
+__global__ __launch_bounds__(64 * NW, 2) void mma_kernel(ScanArgs a, Layout w, int blocks_per_group) {
+  __shared__ __align__(16) Lds<K, NW, MODE == kOut || MODE == kStates> lds;
+  chunks<K, V, NW, MODE>(a, w, blocks_per_group, xcd_remap(blockIdx.x, gridDim.x), lds);
+}
+
+// The backward's two passes from zero, which need nothing of each other, in
+// one launch: the first half of the workgroups has kLocal, the other kRLocal
+// (`r`: the arguments with c and dy in b's and x's place).
+template <int K, int V, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void mma_locals_kernel(ScanArgs a, ScanArgs r, Layout w, int blocks_per_group) {
+  __shared__ __align__(16) Lds<K, NW, false> lds;
+  const int64_t half = gridDim.x / 2, b = blockIdx.x;
+  if (b < half)
+    chunks<K, V, NW, kLocal>(a, w, blocks_per_group, xcd_remap(b, half), lds);
+  else
+    chunks<K, V, NW, kRLocal>(r, w, blocks_per_group, xcd_remap(b - half, half), lds);
+}
+
+template <int K, int V, int MODE, int NW>
+void launch(const ScanArgs &a, const Layout &w, unsigned blocks, int per, hipStream_t st) {
+  if constexpr (MODE == kRLocal) {  // both passes from zero
+    ScanArgs r = a;
+    r.b = a.c;
+    r.bs = a.cs;
+    r.x = a.dy;
+    r.xs = (int64_t)a.Hv * a.V;
+    mma_locals_kernel<K, V, NW><<<2 * blocks, 64 * NW, 0, st>>>(a, r, w, per / NW);
+  } else {
+    mma_kernel<K, V, NW, MODE><<<blocks, 64 * NW, 0, st>>>(a, w, per / NW);
   }
 }
 
@@ -253,11 +292,11 @@ hipError_t go(const char *name, const ScanArgs &a, const Layout &w, hipStream_t 
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   KernelTimer kt(name, st);
   if (nw == 4)
-    mma_kernel<K, V, 4, MODE><<<blocks, 256, 0, st>>>(a, w, per / 4);
+    launch<K, V, MODE, 4>(a, w, blocks, per, st);
   else if (nw == 2)
-    mma_kernel<K, V, 2, MODE><<<blocks, 128, 0, st>>>(a, w, per / 2);
+    launch<K, V, MODE, 2>(a, w, blocks, per, st);
   else
-    mma_kernel<K, V, 1, MODE><<<blocks, 64, 0, st>>>(a, w, per);
+    launch<K, V, MODE, 1>(a, w, blocks, per, st);
   return hipGetLastError();
 }
 template <int MODE>
@@ -286,13 +325,8 @@ hipError_t launch_mma_out(const ScanArgs &a, const Layout &w, hipStream_t st) {
 hipError_t launch_mma_states(const ScanArgs &a, const Layout &w, hipStream_t st) {
   return pick<kStates>("scan_states", a, w, st);
 }
-hipError_t launch_mma_rlocal(const ScanArgs &a0, const Layout &w, hipStream_t st) {
-  ScanArgs a = a0;
-  a.b = a0.c;
-  a.bs = a0.cs;
-  a.x = a0.dy;
-  a.xs = (int64_t)a.Hv * a.V;
-  return pick<kRLocal>("scan_rlocal", a, w, st);
+hipError_t launch_mma_locals(const ScanArgs &a, const Layout &w, hipStream_t st) {
+  return pick<kRLocal>("scan_locals", a, w, st);
 }
 
 }  // namespace scan
