@@ -470,7 +470,7 @@ ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   // workgroups a segment
   const int slices = a.Hv / a.Hq * (a.V / 32);
   const int64_t per = a.dtype == 1 ? (int64_t)a.Hq * (slices / scan::slices_per_block(slices)) : (int64_t)a.Hv * ((a.V + 63) / 64);
-  int64_t want = (compute_units() * (a.dtype == 1 ? 2 : 8) + per - 1) / per;  // segments over the whole batch
+  int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
   const int64_t unit = a.dtype == 1 ? 64 : scan::TB;

@@ -628,7 +628,8 @@ __global__ __launch_bounds__(256) void chunk_heads_kernel(ScanArgs a, Layout w) 
 template <int K, int V>
 hipError_t go(const ScanArgs &a, const Layout &w, hipStream_t st) {
   const int per = a.Hv / a.Hq * (V / 32);  // column slices of a group
-  const int nw = slices_per_block(per);
+  // (four waves: with eight 173 us against 167 at 2 x 4096 tokens x 64 heads)
+  const int nw = slices_per_block(per) < 4 ? slices_per_block(per) : 4;
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   {
     KernelTimer kt("scan_grad", st);

@@ -6,12 +6,12 @@
 //   S'  = 2^{gamma_L} S + sum_j b_j (2^{gamma_L - gamma_j} delta_j x_j)^T
 //
 // A wave owns 32 columns of one head's state and a segment's chunks in order;
-// the waves of a workgroup are column slices of a head group, which share c
-// and b in LDS, the next chunk's rows on their way while one is worked on.
-// Two workgroups of four waves a compute unit fill each other's gaps.  (At
-// 8192 tokens x 64 heads, K 128, V 64: one wave a SIMD with 64 columns 171 us,
-// the state in accumulation registers that vector instructions reach only by
-// moves; eight waves in one workgroup 66 us.)
+// the waves of a workgroup (eight where the group has as many) are column
+// slices of a head group, which share c and b in LDS, the next chunk's rows on
+// their way while one is worked on.  (One wave a SIMD with 64 columns: 171 us
+// for the out pass at 8192 tokens x 64 heads, K 128, V 64, the state in
+// accumulation registers that vector instructions reach only by moves; this
+// form 68 us.)
 //
 // Everything is arranged so that accumulators are operands without moving
 // (gdn_slice.hpp): S tiles (rows k, lane v) give S^T for c; C B^T is formed
@@ -150,10 +150,15 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         if (h2 == 0 && 32 * i + r32 < rows) ai[32 * i + r32] = v;
       }
     }
-    bf16x8 vf[4];
+    // Mild decays (nearly every head): 2^{gamma_i - gamma_j} as the product
+    // 2^{gamma_i} 2^{-gamma_j}, both far inside fp32.  Then x takes 2^{-gamma_j}
+    // delta_j and y and S their factor at the end, and c_i . b_j needs a mask
+    // only: no exponential an element.
+    const bool mild = OUT && gt.mild();
+    Split xs[4];
     const TrA tv(v, VP, lane);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) vf[s] = tv.at(s, 0, VP);
+    for (int s = 0; s < 4; ++s) xs[s] = split_scaled(tv.at(s, 0, VP), (REV ? g.p : mild ? g.v : g.w) + 16 * s + 4 * h2);
     if (OUT) {
       bf16 *yp = static_cast<bf16 *>(a.y) + ((loc.t0 + 64 * (int64_t)c) * a.Hv + h) * V + v0;
       const int64_t ys = (int64_t)a.Hv * V;
@@ -176,8 +181,18 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         const uint32_t f = upto(it ? gt.m1 : gt.m0, r32);
         const float ei = f ? 0.f : exp2_hw(gi), e0 = it == 0 ? ei : gt.m0 | f ? 0.f : exp2_hw(gt.t0 + gi);
         const int first = last_bit(f);  // the first token of the half that token i sees
+        if (mild) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) Pd[i] = 8 * (i >> 2) + 4 * h2 + (i & 3) <= r32 ? Pd[i] : 0.f;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (it) Y = mma32(xs[s].hi, slots(Po, s), Y);
+            Y = mma32(xs[2 * it + s].hi, slots(Pd, s), Y);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) Y[i] *= e0;
+        if (!mild) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int j0 = 8 * b + 4 * h2;
@@ -193,8 +208,9 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (it) Y = mma32(vf[s], slots(Po, s), Y);
-          Y = mma32(vf[2 * it + s], slots(Pd, s), Y);
+          if (it) Y = mma32(tv.at(s, 0, VP), slots(Po, s), Y);
+          Y = mma32(tv.at(2 * it + s, 0, VP), slots(Pd, s), Y);
+        }
         }
         const int row = 32 * it + r32;
         const bf16 *xrow = v + row * VP;
@@ -220,23 +236,26 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    // S = 2^{gamma_L} S + B^T (w X)
+    // S = 2^{gamma_L} S + B^T (w X), with mild decays 2^{gamma_L} (S + B^T (v X))
     const float eL = gt.all();
+    auto scale = [&] {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) S[kt][i] *= eL;
+        for (int i = 0; i < 16; ++i) S[kt][i] *= eL;
+    };
+    if (!mild) scale();
     const TrA tk(k, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const Split x = split_scaled(vf[s], (REV ? g.p : g.w) + 16 * s + 4 * h2);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 kf = tk.at(s, kt, KP);
-        S[kt] = mma32(kf, x.hi, S[kt]);
-        S[kt] = mma32(kf, x.lo, S[kt]);
+        S[kt] = mma32(kf, xs[s].hi, S[kt]);
+        S[kt] = mma32(kf, xs[s].lo, S[kt]);
       }
     }
+    if (mild) scale();
     __syncthreads();  // every wave is done with b and c
     commit(in, tid);
     __syncthreads();
@@ -291,7 +310,9 @@ hipError_t go(const char *name, const ScanArgs &a, const Layout &w, hipStream_t 
   const int nw = slices_per_block(per);
   const unsigned blocks = (unsigned)(a.slots * a.Hq * (per / nw));
   KernelTimer kt(name, st);
-  if (nw == 4)
+  if (nw == 8)
+    launch<K, V, MODE, 8>(a, w, blocks, per, st);
+  else if (nw == 4)
     launch<K, V, MODE, 4>(a, w, blocks, per, st);
   else if (nw == 2)
     launch<K, V, MODE, 2>(a, w, blocks, per, st);

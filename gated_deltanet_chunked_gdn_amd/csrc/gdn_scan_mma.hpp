@@ -103,12 +103,14 @@ struct GatesCore {
   float gam[64], del[64], w1[64], p[64], u1[32], e[32];
 };
 struct Gates : GatesCore {
-  float w[64], u[32];
+  float w[64], u[32], v[64];  // v: delta 2^{-gamma}, gamma from the chunk's first token (mild decays)
 };
 struct GateTotals {
   float t0, t1;     // the halves' sums of log2 decays
   uint32_t m0, m1;  // tokens that forget
   __device__ __forceinline__ float all() const { return m0 | m1 ? 0.f : exp2_hw(t0 + t1); }
+  // no factor between two tokens of the chunk, nor its inverse, past 2^80
+  __device__ __forceinline__ bool mild() const { return !(m0 | m1) && fabsf(t0) < 40.f && fabsf(t1) < 40.f && fabsf(t0 + t1) < 80.f; }
 };
 // bits 0 .. i, and the bits above i
 __device__ __forceinline__ uint32_t upto(uint32_t m, int i) { return m & (0xFFFFFFFFu >> (31 - i)); }
@@ -131,7 +133,10 @@ __device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softpl
   s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam : t.t0 + gam);
   const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? (t.t0 - gam) + t.t1 : t.t1 - gam);
   s.w1[lane] = w1;
-  if constexpr (sizeof(G) == sizeof(Gates)) s.w[lane] = w1 * d;
+  if constexpr (sizeof(G) == sizeof(Gates)) {
+    s.w[lane] = w1 * d;
+    s.v[lane] = exp2_hw(lane < 32 ? -gam : -(t.t0 + gam)) * d;
+  }
   if (lane < 32) {
     const float u1 = later ? 0.f : exp2_hw(t.t0 - gam);
     s.u1[lane] = u1;
