@@ -123,7 +123,7 @@ int check_scan(const gdn_scan_t *p, bool step, gdn::ScanArgs *a) {
     return set_error(GDN_ERR_LAYOUT, "c, b and x strides must be multiples of 16 bytes");
   const int64_t tokens = (int64_t)p->B * p->T;
   if (tokens * (p->Hv > p->Hq ? p->Hv : p->Hq) * 128 > ((int64_t)1 << 40) ||
-      (tokens / 64 + p->N) * p->Hv * 4 >= kGrid || (int64_t)p->B * p->Hv >= kGrid)
+      (tokens / 16 + p->N) * p->Hv * 4 >= kGrid || (int64_t)p->B * p->Hv >= kGrid)
     return set_error(GDN_ERR_UNSUPPORTED, "problem too large");
   *a = gdn::ScanArgs{};
   a->s = gdn::Seqs{p->cu_seqlens, p->cu_seqlens ? p->N : p->B, p->T, tokens};

@@ -25,8 +25,9 @@
 // heads in turn, so that their sums stay in registers.
 //
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
-// enters them is held to fp32: S and Z as operands in two bf16 parts, G and M
-// from the inputs as they are, <S', Z> afresh in every chunk.  (One part
+// enters them is held to fp32: the recurrences of S and Z, S and Z as
+// operands in two bf16 parts, G and M from the inputs as they are, <S', Z>
+// afresh in every chunk.  (One part
 // would leave ddt_bias 5e-4 off; <S', Z> carried along over two chunks, 3e-5.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 #include "gdn_internal.h"
@@ -117,8 +118,8 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
   const int64_t kv = (int64_t)K * V, ys = (int64_t)a.Hv * V;
   const float A2 = a.A[h] * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.D ? a.D[h] : 0.f;
   const bf16 *cp = static_cast<const bf16 *>(a.c) + hq * K, *bp = static_cast<const bf16 *>(a.b) + hq * K;
-  const bf16 *xp = static_cast<const bf16 *>(a.x) + (int64_t)h * V + v0;
-  const bf16 *dp = static_cast<const bf16 *>(a.dy) + (int64_t)h * V + v0;
+  const int64_t col0 = (int64_t)hq * (a.Hv / a.Hq) * V + blk * NW * VW;  // the workgroup's first column
+  const bf16 *xp = static_cast<const bf16 *>(a.x) + col0, *dp = static_cast<const bf16 *>(a.dy) + col0;
   const bf16 *dtp = static_cast<const bf16 *>(a.dt) + h;
   const int nt = (int)(loc.t1 - loc.t0), nc = (nt + 63) >> 6;
   if (nc == 0) return;
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
   // outside it, loaded under a condition, would hold its registers throughout.)
   struct In {
     Rows<K, THREADS> k, q;
-    Rows<VW, 64> x, dy;
+    Rows<NW * VW, THREADS> x, dy;  // of all the slices, which lie side by side: whole lines of memory
     bf16 dt;  // of this lane's token
   };
   float z = 0.f;
@@ -144,8 +145,8 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     r.k.load(bp + t * a.bs, a.bs, rows, tid);
     r.q.load(cp + t * a.cs, a.cs, rows, tid);
-    r.x.load(xp + t * a.xs, a.xs, rows, lane);
-    r.dy.load(dp + t * ys, ys, rows, lane);
+    r.x.load(xp + t * a.xs, a.xs, rows, tid);
+    r.dy.load(dp + t * ys, ys, rows, tid);
     r.dt = load_dt(dtp + t * a.Hv, a.Hv, rows, lane);
   };
   auto fetch_state = [&](int c, int lane) {
@@ -160,8 +161,8 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
     const int lane = tid & 63;
     r.k.store_pi(Kl, KP, tid);
     r.q.store_pi(Ql, KP, tid);
-    r.x.store_pi(Xl[wave], VP, lane);
-    r.dy.store_pi(Dl[wave], VP, lane);
+    r.x.store_slices_pi(Xl[0], VP, tid);
+    r.dy.store_slices_pi(Dl[0], VP, tid);
     z = settle((float)r.dt);
   };
   {
@@ -313,12 +314,13 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
     const TrA tq(q, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const Split y = split_scaled(df[s], &g.p[16 * s + 4 * h2]);
+      const Split3 y = split_scaled(df[s], &g.p[16 * s + 4 * h2]);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 qf = tq.at(s, kt, KP);
-        Z[kt] = mma32(qf, y.hi, Z[kt]);
         Z[kt] = mma32(qf, y.lo, Z[kt]);
+        Z[kt] = mma32(qf, y.mid, Z[kt]);
+        Z[kt] = mma32(qf, y.hi, Z[kt]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }

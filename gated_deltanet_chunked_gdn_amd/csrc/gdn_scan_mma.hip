@@ -20,8 +20,9 @@
 // 16-byte stores after one exchange between the wave's halves.
 //
 // Roundings to bf16: P and the state as operands of y (y itself is bf16).
-// The state is held to fp32: its update takes b as it is and the weighted x
-// as the sum of two bf16 parts (2^-18 of it is lost).
+// The state is held to fp32: its update takes b as it is and the weighted x,
+// an fp32 number, as the sum of three bf16 parts, which lose nothing.  (Two
+// parts lose 2^-18 of it: 2e-6 of a final state, 2e-6 of dA and ddt_bias.)
 #include "gdn_internal.h"
 #include "gdn_scan_mma.hpp"
 
@@ -150,15 +151,10 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         if (h2 == 0 && 32 * i + r32 < rows) ai[32 * i + r32] = v;
       }
     }
-    // Mild decays (nearly every head): 2^{gamma_i - gamma_j} as the product
-    // 2^{gamma_i} 2^{-gamma_j}, both far inside fp32.  Then x takes 2^{-gamma_j}
-    // delta_j and y and S their factor at the end, and c_i . b_j needs a mask
-    // only: no exponential an element.
-    const bool mild = OUT && gt.mild();
-    Split xs[4];
+    bf16x8 vf[4];
     const TrA tv(v, VP, lane);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) xs[s] = split_scaled(tv.at(s, 0, VP), (REV ? g.p : mild ? g.v : g.w) + 16 * s + 4 * h2);
+    for (int s = 0; s < 4; ++s) vf[s] = tv.at(s, 0, VP);
     if (OUT) {
       bf16 *yp = static_cast<bf16 *>(a.y) + ((loc.t0 + 64 * (int64_t)c) * a.Hv + h) * V + v0;
       const int64_t ys = (int64_t)a.Hv * V;
@@ -181,18 +177,8 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         const uint32_t f = upto(it ? gt.m1 : gt.m0, r32);
         const float ei = f ? 0.f : exp2_hw(gi), e0 = it == 0 ? ei : gt.m0 | f ? 0.f : exp2_hw(gt.t0 + gi);
         const int first = last_bit(f);  // the first token of the half that token i sees
-        if (mild) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) Pd[i] = 8 * (i >> 2) + 4 * h2 + (i & 3) <= r32 ? Pd[i] : 0.f;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (it) Y = mma32(xs[s].hi, slots(Po, s), Y);
-            Y = mma32(xs[2 * it + s].hi, slots(Pd, s), Y);
-          }
-        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) Y[i] *= e0;
-        if (!mild) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int j0 = 8 * b + 4 * h2;
@@ -208,9 +194,8 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (it) Y = mma32(tv.at(s, 0, VP), slots(Po, s), Y);
-          Y = mma32(tv.at(2 * it + s, 0, VP), slots(Pd, s), Y);
-        }
+          if (it) Y = mma32(vf[s], slots(Po, s), Y);
+          Y = mma32(vf[2 * it + s], slots(Pd, s), Y);
         }
         const int row = 32 * it + r32;
         const bf16 *xrow = v + row * VP;
@@ -236,26 +221,24 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    // S = 2^{gamma_L} S + B^T (w X), with mild decays 2^{gamma_L} (S + B^T (v X))
+    // S = 2^{gamma_L} S + B^T (w X)
     const float eL = gt.all();
-    auto scale = [&] {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[kt][i] *= eL;
-    };
-    if (!mild) scale();
+      for (int i = 0; i < 16; ++i) S[kt][i] *= eL;
     const TrA tk(k, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
+      const Split3 x = split_scaled(vf[s], (REV ? g.p : g.w) + 16 * s + 4 * h2);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 kf = tk.at(s, kt, KP);
-        S[kt] = mma32(kf, xs[s].hi, S[kt]);
-        S[kt] = mma32(kf, xs[s].lo, S[kt]);
+        S[kt] = mma32(kf, x.lo, S[kt]);
+        S[kt] = mma32(kf, x.mid, S[kt]);
+        S[kt] = mma32(kf, x.hi, S[kt]);
       }
     }
-    if (mild) scale();
     __syncthreads();  // every wave is done with b and c
     commit(in, tid);
     __syncthreads();

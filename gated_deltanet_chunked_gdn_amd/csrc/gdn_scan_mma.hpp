@@ -55,6 +55,14 @@ struct Rows {
       r[i] = buf_load16(rsrc, row < rows ? (uint32_t)(row * stride * 2 + col * 16) : kOutside);
     }
   }
+  // rows of COLS / 32 slices of 32 columns, each slice's to its own 64 rows
+  __device__ __forceinline__ void store_slices_pi(bf16 *lds, int pitch, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = tid + i * THREADS, row = pc / (COLS / 8), col = pc % (COLS / 8);
+      put_pi(lds + ((col >> 2) * 64 + row) * pitch, col & 3, r[i]);
+    }
+  }
   __device__ __forceinline__ void store_pi(bf16 *lds, int pitch, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -103,14 +111,12 @@ struct GatesCore {
   float gam[64], del[64], w1[64], p[64], u1[32], e[32];
 };
 struct Gates : GatesCore {
-  float w[64], u[32], v[64];  // v: delta 2^{-gamma}, gamma from the chunk's first token (mild decays)
+  float w[64], u[32];
 };
 struct GateTotals {
   float t0, t1;     // the halves' sums of log2 decays
   uint32_t m0, m1;  // tokens that forget
   __device__ __forceinline__ float all() const { return m0 | m1 ? 0.f : exp2_hw(t0 + t1); }
-  // no factor between two tokens of the chunk, nor its inverse, past 2^80
-  __device__ __forceinline__ bool mild() const { return !(m0 | m1) && fabsf(t0) < 40.f && fabsf(t1) < 40.f && fabsf(t0 + t1) < 80.f; }
 };
 // bits 0 .. i, and the bits above i
 __device__ __forceinline__ uint32_t upto(uint32_t m, int i) { return m & (0xFFFFFFFFu >> (31 - i)); }
@@ -133,10 +139,7 @@ __device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softpl
   s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam : t.t0 + gam);
   const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? (t.t0 - gam) + t.t1 : t.t1 - gam);
   s.w1[lane] = w1;
-  if constexpr (sizeof(G) == sizeof(Gates)) {
-    s.w[lane] = w1 * d;
-    s.v[lane] = exp2_hw(lane < 32 ? -gam : -(t.t0 + gam)) * d;
-  }
+  if constexpr (sizeof(G) == sizeof(Gates)) s.w[lane] = w1 * d;
   if (lane < 32) {
     const float u1 = later ? 0.f : exp2_hw(t.t0 - gam);
     s.u1[lane] = u1;
@@ -148,22 +151,39 @@ __device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softpl
   return t;
 }
 
-// bf16 parts hi + lo of x[e] * w[e]
-struct Split {
-  bf16x8 hi, lo;
+// x[e] * w[e], rounded to fp32, as the sum of three bf16 numbers: its upper 8
+// bits, the next 8 and the last (each cut off by a mask, so exactly).
+struct Split3 {
+  bf16x8 hi, mid, lo;
 };
-__device__ __forceinline__ Split split_scaled(const bf16x8 &x, const float *w) {
+__device__ __forceinline__ Split3 split_scaled(const bf16x8 &x, const float *w) {
   const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w), w1 = *reinterpret_cast<const f32x4 *>(w + 8);
-  Split r;
+  typedef uint32_t u32x4_ __attribute__((ext_vector_type(4)));
+  u32x4_ hi, mid;
+  Split3 r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float f = (float)x[e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
-    r.hi[e] = (bf16)f;
-    r.lo[e] = (bf16)(f - (float)r.hi[e]);
+  for (int e = 0; e < 8; e += 2) {
+    uint32_t u[2], m[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float f = (float)x[e + k] * (e < 4 ? w0[(e + k) & 3] : w1[(e + k) & 3]);
+      u[k] = __builtin_bit_cast(uint32_t, f);
+      const float r1 = f - __builtin_bit_cast(float, u[k] & 0xFFFF0000u);
+      m[k] = __builtin_bit_cast(uint32_t, r1);
+      r.lo[e + k] = (bf16)(r1 - __builtin_bit_cast(float, m[k] & 0xFFFF0000u));
+    }
+    hi[e / 2] = __builtin_amdgcn_perm(u[1], u[0], 0x07060302);
+    mid[e / 2] = __builtin_amdgcn_perm(m[1], m[0], 0x07060302);
   }
+  r.hi = __builtin_bit_cast(bf16x8, hi);
+  r.mid = __builtin_bit_cast(bf16x8, mid);
   return r;
 }
 
+// bf16 parts hi + lo, to 2^-18
+struct Split {
+  bf16x8 hi, lo;
+};
 // bf16 parts of operand slots 8 s .. 8 s + 7 of an accumulator tile
 __device__ __forceinline__ Split split(const f32x16 &x, int s) {
   Split r;
