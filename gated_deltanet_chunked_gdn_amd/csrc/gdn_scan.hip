@@ -272,18 +272,20 @@ __global__ __launch_bounds__(64) void gates_kernel(ScanArgs a, Layout w, int ksl
   const f32x4 *se = reinterpret_cast<const f32x4 *>(
       loc.last ? w.hend(a) + (loc.n * (int64_t)a.Hv + h) * kv4 * 4 : w.start(a) + ((slot + 1) * a.Hv + h) * kv4 * 4);
   const f32x4 *ze = reinterpret_cast<const f32x4 *>(w.zend(a) + (slot * a.Hv + h) * kv4 * 4);
-  float x = 0.f;
+  double x = 0.;
   for (int64_t i = lane; i < kv4; i += 64) {
     const f32x4 p = se[i], q = ze[i];
-    x += p[0] * q[0] + p[1] * q[1] + p[2] * q[2] + p[3] * q[3];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x += (double)p[k] * q[k];
   }
-  float dg_next = wave_sum(x);
+  double dg_next = wave_sum64(x);
   const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-  float dA = 0.f, dbias = 0.f;
+  double dA = 0., dbias = 0.;
   for (int64_t e = loc.t1; e > loc.t0; e -= 64) {
     const int64_t t = e - 1 - lane;  // lane 0 has the last token
     const bool on = t >= loc.t0;
-    float av = 0.f, rv = 0.f, mv = 0.f, z = 0.f;
+    double av = 0., rv = 0., mv = 0.;
+    float z = 0.f;
     if (on) {
       for (int s = 0; s < kslices; ++s) av += w.a_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
       for (int s = 0; s < vslices; ++s) {
@@ -293,37 +295,23 @@ __global__ __launch_bounds__(64) void gates_kernel(ScanArgs a, Layout w, int ksl
       z = to_f32(static_cast<const E *>(a.dt)[t * a.Hv + h]) + bias;
     }
     const float delta = on ? (a.softplus ? softplusf(z) : z) : 0.f;
-    // dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 to fp32 where the token forgets all
-    // (e^-20 is far below half a step of its parts), and the chain begins
-    // again there: delta_t r_t, large where delta_t is, leaves no rounding.
-    int cut = on && delta * A < -20.f;
-    float dg = cut ? 0.f : on ? av - delta * rv : 0.f;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const float below = __shfl_up(dg, d);
-      const int cut_below = __shfl_up(cut, d);
-      if (lane >= d && !cut) {
-        dg += below;
-        cut = cut_below;
-      }
-    }
-    if (!cut) dg += dg_next;
-    dg_next = lane63(dg);
-    float dd = rv + mv + A * dg;
+    const double dg = dg_chain(on ? av - delta * rv : 0., on && delta * A < -20.f, dg_next, lane);
+    dg_next = __shfl(dg, 63);
+    double dd = rv + mv + A * dg;
     if (a.softplus) dd *= 1.f / (1.f + expf(-z));
     if (on) {
-      static_cast<E *>(a.ddt)[t * a.Hv + h] = from_f32<E>(dd);
+      static_cast<E *>(a.ddt)[t * a.Hv + h] = from_f32<E>((float)dd);
       dA += delta * dg;
       dbias += dd;
     }
   }
-  dA = wave_sum(dA);
-  dbias = wave_sum(dbias);
+  dA = wave_sum64(dA);
+  dbias = wave_sum64(dbias);
   if (lane == 0) {
     float dD = 0.f;
     for (int s = 0; s < vslices; ++s) dD += w.dd_part(a)[((int64_t)s * a.slots + slot) * a.Hv + h];
-    part[0] = dA;
-    part[1] = dbias;
+    part[0] = (float)dA;
+    part[1] = (float)dbias;
     part[2] = dD;
   }
 }
@@ -332,13 +320,13 @@ __global__ __launch_bounds__(64) void gates_kernel(ScanArgs a, Layout w, int ksl
 // in a fixed order.
 __global__ __launch_bounds__(64) void heads_kernel(ScanArgs a, Layout w) {
   const int h = blockIdx.x;
-  float v[3] = {0.f, 0.f, 0.f};
+  double v[3] = {0., 0., 0.};
   for (int64_t s = threadIdx.x; s < a.slots; s += 64)
     for (int k = 0; k < 3; ++k) v[k] += w.head_part(a)[(s * a.Hv + h) * 3 + k];
   float *out[3] = {a.dA, a.ddt_bias, a.dD};
   for (int k = 0; k < 3; ++k) {
-    const float t = wave_sum(v[k]);
-    if (threadIdx.x == 0 && out[k]) out[k][h] = t;
+    const double t = wave_sum64(v[k]);
+    if (threadIdx.x == 0 && out[k]) out[k][h] = (float)t;
   }
 }
 

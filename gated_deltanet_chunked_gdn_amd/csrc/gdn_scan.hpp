@@ -132,6 +132,32 @@ hipError_t launch_mma_locals(const ScanArgs &a, const Layout &w, hipStream_t st)
 // bf16, gdn_scan_bwd.hip
 hipError_t launch_mma_grad(const ScanArgs &a, const Layout &w, hipStream_t st);
 
+// The chain of dg over 64 tokens, lane 0 the last: sums from lane 0 on of
+// `val` (a - delta r) onto `next` (<S, Z> of the state behind them).
+//
+// dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 to fp32 where the token forgets all
+// (`cut`), and the chain begins again there: delta_t r_t, large where delta_t
+// is, leaves no rounding behind.  The terms cancel among each other, and again
+// against r and m in the sums over all tokens: the chain is held in 64 bits.
+__device__ __forceinline__ double dg_chain(double val, int cut, double next, int lane) {
+  double dg = cut ? 0.0 : val;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double below = __shfl_up(dg, d);
+    const int cut_below = __shfl_up(cut, d);
+    if (lane >= d && !cut) {
+      dg += below;
+      cut = cut_below;
+    }
+  }
+  return cut ? dg : dg + next;
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
 __device__ __forceinline__ SlotLoc locate(const ScanArgs &a, int64_t slot) {
   int lo = 0, hi = a.s.N - 1;
   if (!a.s.cu) {

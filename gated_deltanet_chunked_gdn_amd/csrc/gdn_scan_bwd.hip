@@ -569,10 +569,10 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const int slices = a.V / 32;
   const bool on = lane < rows;
   const int64_t t = loc.t1 - 1 - (on ? lane : 0);
-  float av = 0.f, rv = 0.f, mv = 0.f, x = 0.f, dD = 0.f;
+  double av = 0., rv = 0., mv = 0., x = 0., dD = 0.;
   for (int s = 0; s < slices; ++s) {
     const int64_t i = ((int64_t)s * a.Hv + h) * a.s.tokens + t;
-    av += w.a_part(a)[i] + w.ai_part(a)[i];
+    av += (double)w.a_part(a)[i] + (double)w.ai_part(a)[i];
     rv += w.r_part(a)[i];
     mv += w.m_part(a)[i];
     const int64_t j = ((int64_t)s * w.chunks + slot) * a.Hv + h;
@@ -582,48 +582,34 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const float A = a.A[h];
   const float z = (float)static_cast<const bf16 *>(a.dt)[t * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
   const float delta = a.softplus ? softplusf(z) : z;
-  // dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 to fp32 where the token forgets all,
-  // and the chain begins again there: delta_t r_t, large where delta_t is,
-  // leaves no rounding behind.
-  int cut = on && delta * A * kLog2e < kForget;
-  float dg = cut || !on ? 0.f : av - delta * rv;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const float below = __shfl_up(dg, d);
-    const int cut_below = __shfl_up(cut, d);
-    if (lane >= d && !cut) {
-      dg += below;
-      cut = cut_below;
-    }
-  }
-  if (!cut) dg += x;
-  float dd = rv + mv + A * dg;
+  const double dg = dg_chain(on ? av - delta * rv : 0., on && delta * A * kLog2e < kForget, x, lane);
+  double dd = rv + mv + A * dg;
   if (a.softplus) dd *= 1.f / (1.f + expf(-z));
-  if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)dd;
-  const float dA = wave_sum(on ? delta * dg : 0.f), dbias = wave_sum(on ? dd : 0.f);
+  if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)(float)dd;
+  const float dA = (float)wave_sum64(on ? delta * dg : 0.), dbias = (float)wave_sum64(on ? dd : 0.);
   if (lane == 0) {
     part[0] = dA;
     part[1] = dbias;
-    part[2] = dD;
+    part[2] = (float)dD;
   }
 }
 
 // dA, ddt_bias, dD of a head: the chunks' parts in a fixed order.
 __global__ __launch_bounds__(256) void chunk_heads_kernel(ScanArgs a, Layout w) {
-  __shared__ float red[3][4];
+  __shared__ double red[3][4];
   const int h = blockIdx.x, lane = threadIdx.x & 63;
-  float v[3] = {0.f, 0.f, 0.f};
+  double v[3] = {0., 0., 0.};
   for (int64_t s = threadIdx.x; s < w.chunks; s += 256)
     for (int k = 0; k < 3; ++k) v[k] += w.head_part(a)[(s * a.Hv + h) * 3 + k];
   for (int k = 0; k < 3; ++k) {
-    const float t = wave_sum(v[k]);
+    const double t = wave_sum64(v[k]);
     if (lane == 0) red[k][threadIdx.x >> 6] = t;
   }
   __syncthreads();
   float *out[3] = {a.dA, a.ddt_bias, a.dD};
   if (threadIdx.x < 3 && out[threadIdx.x]) {
-    const float *r = red[threadIdx.x];
-    out[threadIdx.x][h] = (r[0] + r[1]) + (r[2] + r[3]);
+    const double *r = red[threadIdx.x];
+    out[threadIdx.x][h] = (float)((r[0] + r[1]) + (r[2] + r[3]));
   }
 }
 
