@@ -396,8 +396,8 @@ hipError_t fwd_mma(const ScanArgs &a, hipStream_t st) {
 hipError_t bwd_mma(const ScanArgs &a, hipStream_t st) {
   const Layout w = layout(a, true);
   hipError_t e;
-  if ((e = launch_mma_locals(a, w, st)) != hipSuccess) return e;
-  {
+  if (!a.one_seg) {
+    if ((e = launch_mma_locals(a, w, st)) != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
     carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -468,7 +468,7 @@ ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   ScanPlan p;
   p.seg = (int)seg;
   a.slots = p.slots = scan::slots_of(a.s, p.seg);
-  a.one_seg = p.one_seg = !bwd && a.s.T <= seg;
+  a.one_seg = p.one_seg = (!bwd || a.dtype == 1) && a.s.T <= seg;
   p.ws = scan::layout(a, bwd).total;
   return p;
 }

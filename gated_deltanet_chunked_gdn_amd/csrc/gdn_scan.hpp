@@ -30,7 +30,7 @@ struct SlotLoc {
 
 // Byte offsets of the workspace's pieces (each at a 256-byte boundary).
 struct Layout {
-  size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
+  size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_ri = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
          o_dc = 0, o_db = 0, o_ai = 0, o_shi = 0, o_slo = 0, o_z = 0, total = 0;
   int64_t chunks = 0;      // slots of 64-token chunks (bf16 backward)
   bool need_last = false;  // the local pass runs a sequence's last segment too
@@ -49,11 +49,14 @@ struct Layout {
   __host__ __device__ float *a_part(const ScanArgs &a) const { return at(a, o_a); }
   __host__ __device__ float *r_part(const ScanArgs &a) const { return at(a, o_r); }
   __host__ __device__ float *m_part(const ScanArgs &a) const { return at(a, o_m); }
-  // bf16: what of a_t comes from the state entering the chunk
+  // bf16, the same: what of a_t comes from the state entering the chunk, and
+  // of r_t from the gradient of the state leaving it (a_part, r_part: the rest)
   __host__ __device__ float *ai_part(const ScanArgs &a) const { return at(a, o_ai); }
+  __host__ __device__ float *ri_part(const ScanArgs &a) const { return at(a, o_ri); }
   // parts of dD: [slices][slots, bf16: chunks][Hv]
   __host__ __device__ float *dd_part(const ScanArgs &a) const { return at(a, o_dd); }
-  // [slices][chunks][Hv]: parts of <S, Z> of every chunk's last state (bf16)
+  // [slices][chunks][Hv]: parts of 2^{gamma_L} <S, Z>, S entering the chunk, Z
+  // of the state leaving it (bf16)
   __host__ __device__ float *x_part(const ScanArgs &a) const { return at(a, o_x); }
   // [slots or chunks][Hv][3]: parts of dA, ddt_bias, dD
   __host__ __device__ float *head_part(const ScanArgs &a) const { return at(a, o_head); }
@@ -87,7 +90,7 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_start = piece(heads * kv * 4);
     w.o_decay = piece(heads * 4);
   }
-  if (bwd) w.o_zend = piece(heads * kv * 4);
+  if (bwd && !a.one_seg) w.o_zend = piece(heads * kv * 4);
   if (bwd && a.dtype != 1) {
     w.o_hend = piece((size_t)a.s.N * a.Hv * kv * 4);
     w.o_a = piece(tok * ((a.K + 63) / 64) * 4);
@@ -106,6 +109,7 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_r = piece(tok * slices * 4);
     w.o_m = piece(tok * slices * 4);
     w.o_ai = piece(tok * slices * 4);
+    w.o_ri = piece(tok * slices * 4);
     w.o_dd = piece(ch * slices * 4);
     w.o_x = piece(ch * slices * 4);
     w.o_head = piece(ch * 3 * 4);

@@ -13,22 +13,22 @@
 // and for the gates, with W_ij = E_ij G_ij M_ij,
 //
 //   a_i = sum_{j < i} W_ij delta_j + p_i c_i . S dy_i
-//   r_j = sum_{i > j} W_ij + w_j b_j . Z x_j,   m_j = W_jj
-//   dg_t = <S', Z> + sum_{s >= t} (a_s - delta_s r_s),  S' the state leaving
-//   d delta_t = r_t + m_t + A dg_t
+//   r_j = sum_{i > j} W_ij,   z_j = w_j b_j . Z x_j,   m_j = W_jj
+//   dg_t = 2^{gamma_L} <S, Z> + sum_{s >= t} (a_s - delta_s r_s) + sum_{s < t} delta_s z_s
+//   d delta_t = r_t + z_t + m_t + A dg_t
 //
 // The pass that forms the states (kStates, gdn_scan_mma.hip) also has the
-// state's part of a_i.  Two kernels share the rest.  grad_kernel walks a segment's chunks from its end
-// with Z in accumulators (32 columns of a head a wave, as the forward): dx,
-// the gates' sums, and Z of every chunk, rounded to bf16, for the other.
-// pair_kernel has dc and db: one chunk of one head group a workgroup, the
-// heads in turn, so that their sums stay in registers.
+// state's part of a_i.  Two kernels share the rest.  grad_kernel walks a
+// segment's chunks from its end with Z in accumulators (32 columns of a head a
+// wave, as the forward): dx, the gates' sums, and Z of every chunk, rounded to
+// bf16, for the other.  pair_kernel has dc and db: one chunk of one head group
+// a workgroup, the heads in turn, so that their sums stay in registers.
 //
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
 // enters them is held to fp32: the recurrences of S and Z, S and Z as
-// operands in two bf16 parts, G and M from the inputs as they are, <S', Z>
-// afresh in every chunk.  (One part
-// would leave ddt_bias 5e-4 off; <S', Z> carried along over two chunks, 3e-5.)
+// operands in two bf16 parts, G and M from the inputs as they are, <S, Z>
+// afresh in every chunk.  (One part would leave ddt_bias 5e-4 off; <S, Z>
+// carried along over two chunks, 3e-5.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 #include "gdn_internal.h"
 #include "gdn_scan_mma.hpp"
@@ -122,10 +122,19 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
   const bf16 *xp = static_cast<const bf16 *>(a.x) + col0, *dp = static_cast<const bf16 *>(a.dy) + col0;
   const bf16 *dtp = static_cast<const bf16 *>(a.dt) + h;
   const int nt = (int)(loc.t1 - loc.t0), nc = (nt + 63) >> 6;
-  if (nc == 0) return;
 
   typename D::State Z;
-  state_io<K, V>(Z, w.zend(a) + (slot * a.Hv + h) * kv + v0, false, tid0 & 63);
+  const int64_t seq = (loc.n * (int64_t)a.Hv + h) * kv + v0;
+  const float *src = a.one_seg ? (a.dht ? a.dht + seq : nullptr) : w.zend(a) + (slot * a.Hv + h) * kv + v0;
+  float *const dh0 = a.one_seg && a.dh0 ? a.dh0 + seq : nullptr;  // (else the carries have it)
+  if (nc == 0) {
+    if (dh0)
+      for (int i = tid0 & 63; i < K * VW; i += 64) {
+        const int64_t at = (int64_t)(i / VW) * V + i % VW;
+        dh0[at] = src ? src[at] : 0.f;
+      }
+    return;
+  }
   bf16x8 sh[K / 16], sl[K / 16];
   // one chunk's rows on their way to LDS.  (An object of the loop's body: one
   // outside it, loaded under a condition, would hold its registers throughout.)
@@ -168,8 +177,14 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
   {
     In r;
     fetch(r, nc - 1, tid0);
-    fetch_state(nc - 1, tid0 & 63);
     commit(r, tid0);
+  }
+  fetch_state(nc - 1, tid0 & 63);
+  if (src) {
+    state_io<K, V>(Z, const_cast<float *>(src), false, tid0 & 63);
+  } else {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) Z[kt] = zero16();
   }
   __syncthreads();
   for (int c = nc - 1; c >= 0; --c) {
@@ -203,18 +218,12 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
         if (s & 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    float xo = wave_sum(xd) * eL;
-    float ri[2];
-    {
-      float sum = 0.f;
+    const float xo = wave_sum(xd) * eL;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int tok = 32 * i + r32;
-        ri[i] = row_dot(Y[i], x + tok * VP, h2) * g.w1[tok];
-        sum += ri[i] * g.del[tok];
-      }
-      // (both halves hold the same 32 + 32 values)
-      xo += 0.5f * wave_sum(sum);
+    for (int i = 0; i < 2; ++i) {
+      const int tok = 32 * i + r32;
+      const float v = row_dot(Y[i], x + tok * VP, h2) * g.w1[tok];
+      if (h2 == 0 && tok < rows) w.ri_part(a)[sums + tok] = v;
     }
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 df[4];  // dy^T: lane v, tokens
@@ -231,7 +240,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
 #pragma unroll
     for (int jt = 0; jt < 2; ++jt) {
       const int tj = 32 * jt + r32;  // token j of this lane
-      const float gj = g.gam[tj], dj = g.del[tj];
+      const float gj = g.gam[tj], lj = g.rest[tj], dj = g.del[tj];
       const int lim = next_bit(above(jt ? gt.m1 : gt.m0, r32));  // the first token of the half that no longer sees j
       f32x16 T = Y[jt];
       const float wj = g.w1[tj];
@@ -256,12 +265,13 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
           const int i0 = 8 * b + 4 * h2;
           // rows i: log2 decays (diagonal tile) or decays from the second half's start
           const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &g.gam[32 * it + i0] : &g.e[i0]);
+          const f32x4 li = *reinterpret_cast<const f32x4 *>(&g.rest[32 * it + i0]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = i0 + e;
             float E;
             if (it == jt)
-              E = exp2_if(i >= r32 && i < lim, gi[e] - gj);
+              E = exp2_if(i >= r32 && i < lim, (gi[e] - gj) + (li[e] - lj));
             else
               E = gi[e] * uj;
             const float p = P[4 * b + e] * E, wm = p * M[4 * b + e];
@@ -283,7 +293,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       rs += __shfl_xor(rs, 32);
       ms += __shfl_xor(ms, 32);
       if (h2 == 0 && tj < rows) {
-        w.r_part(a)[sums + tj] = rs + ri[jt];
+        w.r_part(a)[sums + tj] = rs;
         w.m_part(a)[sums + tj] = ms;
       }
 #pragma unroll
@@ -332,6 +342,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       __syncthreads();
     }
   }
+  if (dh0) state_io<K, V>(Z, dh0, true, opaque_tid() & 63);
 }
 
 // dc and db of one chunk and head group.  Waves are (k tile, dc or db), units
@@ -467,18 +478,19 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
       const bf16 *yi = Dl + (32 * it + r32) * UP + 8 * h2, *xj = Xl + (32 * jt + r32) * UP + 8 * h2;
 #pragma unroll
       for (int s = 0; s < UC / 16; ++s) M = mma32(lds16(yi + 16 * s), lds16(xj + 16 * s), M);
-      const float gj = g.gam[32 * jt + r32], dj = g.del[32 * jt + r32], uj = g.u[r32];
+      const float gj = g.gam[32 * jt + r32], lj = g.rest[32 * jt + r32], dj = g.del[32 * jt + r32], uj = g.u[r32];
       const int lim = next_bit(above(Gm[u & 1][jt], r32));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int i0 = 8 * b + 4 * h2;
         const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &g.gam[32 * it + i0] : &g.e[i0]);
+        const f32x4 li = *reinterpret_cast<const f32x4 *>(&g.rest[32 * it + i0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = i0 + e;
           float E;
           if (it == jt)
-            E = exp2_if(i >= r32 && i < lim, gi[e] - gj) * dj;
+            E = exp2_if(i >= r32 && i < lim, (gi[e] - gj) + (li[e] - lj)) * dj;
           else
             E = gi[e] * uj;
           Nacc[4 * b + e] += E * M[4 * b + e];
@@ -550,7 +562,7 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   }
 }
 
-// The gates of one chunk and head: dg from the chunk's <S', Z> and its a, r,
+// The gates of one chunk and head: dg from the chunk's <S, Z> and its a, r, z,
 // then ddt and the chunk's parts of dA, ddt_bias, dD.  Lanes are tokens, lane
 // 0 the last.
 __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) {
@@ -569,11 +581,12 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const int slices = a.V / 32;
   const bool on = lane < rows;
   const int64_t t = loc.t1 - 1 - (on ? lane : 0);
-  double av = 0., rv = 0., mv = 0., x = 0., dD = 0.;
+  double av = 0., rv = 0., ri = 0., mv = 0., x = 0., dD = 0.;
   for (int s = 0; s < slices; ++s) {
     const int64_t i = ((int64_t)s * a.Hv + h) * a.s.tokens + t;
     av += (double)w.a_part(a)[i] + (double)w.ai_part(a)[i];
     rv += w.r_part(a)[i];
+    ri += w.ri_part(a)[i];
     mv += w.m_part(a)[i];
     const int64_t j = ((int64_t)s * w.chunks + slot) * a.Hv + h;
     x += w.x_part(a)[j];
@@ -582,8 +595,18 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const float A = a.A[h];
   const float z = (float)static_cast<const bf16 *>(a.dt)[t * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
   const float delta = a.softplus ? softplusf(z) : z;
-  const double dg = dg_chain(on ? av - delta * rv : 0., on && delta * A * kLog2e < kForget, x, lane);
-  double dd = rv + mv + A * dg;
+  // the sum of delta_j z_j over the tokens before t (nothing is left of them
+  // where t or a later one forgets all: w_j is 0)
+  double before = on ? delta * ri : 0.;
+  before = __shfl_down(before, 1);
+  if (lane == 63) before = 0.;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double more = __shfl_down(before, d);
+    if (lane + d < 64) before += more;
+  }
+  const double dg = dg_chain(on ? av - delta * rv : 0., on && delta * A * kLog2e < kForget, x, lane) + before;
+  double dd = rv + ri + mv + A * dg;
   if (a.softplus) dd *= 1.f / (1.f + expf(-z));
   if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)(float)dd;
   const float dA = (float)wave_sum64(on ? delta * dg : 0.), dbias = (float)wave_sum64(on ? dd : 0.);

@@ -67,9 +67,8 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
 
   typename D::State S;
   const float *src = nullptr;
-  if (OUT)
+  if (OUT || MODE == kStates)
     src = a.one_seg ? (a.h0 ? a.h0 + (loc.n * (int64_t)a.Hv + h) * kv : nullptr) : w.start(a) + (slot * a.Hv + h) * kv;
-  if (MODE == kStates) src = w.start(a) + (slot * a.Hv + h) * kv;
   if (src) {
     state_io<K, V>(S, const_cast<float *>(src) + v0, false, lane);
   } else {
@@ -173,9 +172,9 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
           if (it) Po = mma32(lds16(ko + 16 * s), qf, Po);
           if ((s & 3) == 3) __builtin_amdgcn_sched_barrier(0);
         }
-        const float gi = g.gam[32 * it + r32];  // of token i, from its half's start
+        const float gi = g.gam[32 * it + r32], li = g.rest[32 * it + r32];  // of token i, from its half's start
         const uint32_t f = upto(it ? gt.m1 : gt.m0, r32);
-        const float ei = f ? 0.f : exp2_hw(gi), e0 = it == 0 ? ei : gt.m0 | f ? 0.f : exp2_hw(gt.t0 + gi);
+        const float ei = it ? g.e[r32] : 0.f, e0 = g.p[32 * it + r32];
         const int first = last_bit(f);  // the first token of the half that token i sees
 #pragma unroll
         for (int i = 0; i < 16; ++i) Y[i] *= e0;
@@ -183,12 +182,13 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         for (int b = 0; b < 4; ++b) {
           const int j0 = 8 * b + 4 * h2;
           const f32x4 gj = *reinterpret_cast<const f32x4 *>(&g.gam[32 * it + j0]);
+          const f32x4 lj = *reinterpret_cast<const f32x4 *>(&g.rest[32 * it + j0]);
           const f32x4 dj = *reinterpret_cast<const f32x4 *>(&g.del[32 * it + j0]);
           const f32x4 uj = *reinterpret_cast<const f32x4 *>(&g.u[j0]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + i;
-            Pd[4 * b + i] *= exp2_if(j <= r32 && j >= first, gi - gj[i]) * dj[i];
+            Pd[4 * b + i] *= exp2_if(j <= r32 && j >= first, (gi - gj[i]) + (li - lj[i])) * dj[i];
             if (it) Po[4 * b + i] *= ei * uj[i];
           }
         }

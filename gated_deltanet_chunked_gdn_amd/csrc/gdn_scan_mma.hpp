@@ -102,13 +102,15 @@ __device__ __forceinline__ bf16 load_dt(const bf16 *dt, int64_t stride, int rows
 // the half's last (u1) and times delta (u), from the second half's first token
 // to its tokens (e), and from the chunk's first token to the token (p).
 //
-// A token whose own decay is below 2^kForget ends all that is before it to
-// fp32 (2^-27 of a term is an eighth of its half step).  It counts as an
-// exact 0 and stays out of the sums, where it would cost the differences
-// between later tokens their digits; m0, m1 mark such tokens of the halves.
-constexpr float kForget = -27.f;
+// The last digits of gamma are the relative error of 2^{gamma_i - gamma_j}, and
+// a chunk's log decays can add up to thousands: each is taken as a multiple of
+// 2^-12 (gam, whose sums and differences are exact up to 2^12) and the rest
+// (rest, below 2^-13 each).  A token whose own decay is below 2^kForget ends
+// all that is before it; it counts as an exact 0 and stays out of the sums, so
+// that a half's stays below 2^12.  m0, m1 mark such tokens of the halves.
+constexpr float kForget = -126.f;
 struct GatesCore {
-  float gam[64], del[64], w1[64], p[64], u1[32], e[32];
+  float gam[64], rest[64], del[64], w1[64], p[64], u1[32], e[32];
 };
 struct Gates : GatesCore {
   float w[64], u[32];
@@ -129,23 +131,26 @@ __device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softpl
   const float g = d * A2;
   const bool cut = g < kForget;
   const unsigned long long m = __ballot(cut);
-  const float gam = half_incl_scan(cut ? 0.f : g);
-  GateTotals t{lane_f(gam, 31), lane_f(gam, 63), (uint32_t)m, (uint32_t)(m >> 32)};
+  const float gh = cut ? 0.f : __builtin_rintf(g * 4096.f) * (1.f / 4096.f), gl = cut ? 0.f : g - gh;
+  const float gam = half_incl_scan(gh), rest = half_incl_scan(gl);
+  const float h0 = lane_f(gam, 31), h1 = lane_f(gam, 63), r0 = lane_f(rest, 31), r1 = lane_f(rest, 63);
+  GateTotals t{h0 + r0, h1 + r1, (uint32_t)m, (uint32_t)(m >> 32)};
   const int i = lane & 31;
   const uint32_t later = lane < 32 ? above(t.m0, i) : above(t.m1, i);
   s.gam[lane] = gam;
+  s.rest[lane] = rest;
   s.del[lane] = d;
   const uint32_t before = upto(lane < 32 ? t.m0 : t.m1, i) | (lane < 32 ? 0u : t.m0);
-  s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam : t.t0 + gam);
-  const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? (t.t0 - gam) + t.t1 : t.t1 - gam);
+  s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam + rest : (h0 + gam) + (r0 + rest));
+  const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? ((h0 - gam) + h1) + ((r0 - rest) + r1) : (h1 - gam) + (r1 - rest));
   s.w1[lane] = w1;
   if constexpr (sizeof(G) == sizeof(Gates)) s.w[lane] = w1 * d;
   if (lane < 32) {
-    const float u1 = later ? 0.f : exp2_hw(t.t0 - gam);
+    const float u1 = later ? 0.f : exp2_hw((h0 - gam) + (r0 - rest));
     s.u1[lane] = u1;
     if constexpr (sizeof(G) == sizeof(Gates)) s.u[lane] = u1 * d;
   } else {
-    s.e[lane - 32] = upto(t.m1, i) ? 0.f : exp2_hw(gam);
+    s.e[lane - 32] = upto(t.m1, i) ? 0.f : exp2_hw(gam + rest);
   }
   wave_lds_fence();
   return t;

@@ -264,6 +264,66 @@ def test_scan_extreme_steps(gdn):
     check_scan_grads(got, (c, b, x, dt, A, D, bias, h0), dy, dht, cu, sp, "bf16")
 
 
+@pytest.mark.parametrize("step", [1e-4, 0.3, 2.0, 9.0, 18.0, 40.0, "mixed"])
+def test_scan_decay_regimes(gdn, step):
+    """Log decays a token from nothing to all (18 is just short of what counts
+    as all), and each kind beside the others in one chunk."""
+    announce(f"scan decays {step}")
+    g = gen(17)
+    c, b, x, _, _, D, _, h0, dy, dht, _, _ = scan_inputs(("bf16", 1, 150, 1, 2, 64, 64, None, True, True, True, True))
+    if step == "mixed":
+        d = torch.tensor([1e-4, 0.3, 2.0, 9.0, 18.0, 40.0, 200.0])[torch.randint(0, 7, (1, 150, 2), generator=g)]
+    else:
+        d = step * (0.8 + 0.4 * torch.rand(1, 150, 2, generator=g))
+    A = torch.tensor([-1.0, -0.5]).cuda()
+    dt = (d / torch.tensor([1.0, 0.5])).bfloat16().cuda()
+    y, ht = gdn.selective_scan_fwd(c, b, x, dt, A, D=D, dt_softplus=False, initial_state=h0)
+    ry, rht = ref.scan(*[dbl(t) for t in (c, b, x, dt, A, D)], None, dbl(h0), None, False)
+    near("y", y, ry, SCAN["bf16"])
+    near("ht", ht, rht, F32)
+    got = gdn.selective_scan_bwd(c, b, x, dt, A, dy, dht=dht, D=D, dt_softplus=False, initial_state=h0)
+    check_scan_grads(got, (c, b, x, dt, A, D, None, h0), dy, dht, None, False, "bf16")
+
+
+def test_scan_many_short_sequences(gdn):
+    """More sequences than segments would need, single tokens and empty ones."""
+    lens = [int(v) for v in torch.randint(0, 5, (300,), generator=gen(23))] + [200]
+    case = ("bf16", 1, 0, 2, 4, 32, 32, lens, True, True, True, True)
+    c, b, x, dt, A, D, bias, h0, dy, dht, cu, sp = scan_inputs(case)
+    y, ht = gdn.selective_scan_fwd(c, b, x, dt, A, D=D, dt_bias=bias, initial_state=h0, cu_seqlens=cu)
+    ry, rht = ref.scan(*[dbl(t) for t in (c, b, x, dt, A, D, bias, h0)], cu, sp)
+    near("y", y, ry, SCAN["bf16"])
+    near("ht", ht, rht, F32)
+    got = gdn.selective_scan_bwd(c, b, x, dt, A, dy, dht=dht, D=D, dt_bias=bias, initial_state=h0, cu_seqlens=cu)
+    check_scan_grads(got, (c, b, x, dt, A, D, bias, h0), dy, dht, cu, sp, "bf16")
+
+
+def test_scan_batch_by_batch_is_the_batch(gdn):
+    """Rows of a batch do not meet: each alone gives the batch's values, cut into
+    other segments."""
+    case = ("bf16", 2, 130, 1, 8, 64, 64, None, True, True, True, True)
+    c, b, x, dt, A, D, bias, h0, *_ = scan_inputs(case)
+    y, ht = gdn.selective_scan_fwd(c, b, x, dt, A, D=D, dt_bias=bias, initial_state=h0)
+    for i in range(2):
+        r = slice(i, i + 1)
+        y1, ht1 = gdn.selective_scan_fwd(c[r], b[r], x[r], dt[r], A, D=D, dt_bias=bias, initial_state=h0[r])
+        near("y", y1, dbl(y[r]), SCAN["bf16"])
+        near("ht", ht1, dbl(ht[r]), F32)
+
+
+def test_scan_a_nan_stays_in_its_sequence(gdn):
+    lens = [70, 30, 64]
+    c, b, x, dt, A, D, bias, h0, dy, dht, cu, sp = scan_inputs(("bf16", 1, 0, 1, 2, 64, 64, lens, True, True, True, True))
+    clean = gdn.selective_scan_fwd(c, b, x, dt, A, D=D, dt_bias=bias, initial_state=h0, cu_seqlens=cu)
+    x2 = x.clone()
+    x2[0, 75] = float("nan")
+    y, ht = gdn.selective_scan_fwd(c, b, x2, dt, A, D=D, dt_bias=bias, initial_state=h0, cu_seqlens=cu)
+    keep = torch.ones(164, dtype=torch.bool)
+    keep[70:100] = False
+    assert torch.equal(y[0, keep], clean[0][0, keep]) and torch.equal(ht[[0, 2]], clean[1][[0, 2]])
+    assert bool(torch.isnan(y[0, 75:100]).all())
+
+
 # ---------------------------------------------------------------- steps
 
 
@@ -324,6 +384,8 @@ NORMS = [
     ("bf16", 5, 16384, True, True, True, False, True),
     ("bf16", 5, 16385, True, True, True, False, True),
     ("f32", 34, 20001, True, False, False, True, True),
+    ("bf16", 40000, 72, True, True, True, False, True),
+    ("f32", 3000, 1500, True, True, False, False, True),
 ]
 
 
