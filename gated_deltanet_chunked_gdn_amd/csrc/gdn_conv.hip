@@ -6,7 +6,10 @@
 // that goes in and comes out; its backward, and its form for single tokens.
 // All of it moves data far longer than it computes: x and y once (the
 // backward: x, dy and dx), so each kernel is one pass with the window in
-// registers.
+// registers.  16384 tokens x 8192 channels in bf16 forward: 108 us, 5.0 TB/s
+// (a large copy here: 5.4); 2 x 4096 x 8192 backward with the sums: 105 us,
+// 3.8 TB/s (three streams, half the waves by registers).  A token's step is a
+// launch: 9 us a call at 32 x 8192.
 #include <initializer_list>
 
 #include "gdn_internal.h"

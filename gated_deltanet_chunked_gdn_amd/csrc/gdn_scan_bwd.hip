@@ -14,7 +14,8 @@
 //
 //   a_i = sum_{j < i} W_ij delta_j + p_i c_i . S dy_i
 //   r_j = sum_{i > j} W_ij,   z_j = w_j b_j . Z x_j,   m_j = W_jj
-//   dg_t = 2^{gamma_L} <S, Z> + sum_{s >= t} (a_s - delta_s r_s) + sum_{s < t} delta_s z_s
+//   dg_t = 2^{gamma_L} <S, Z> + sum_{s >= t} p_s c_s . S dy_s + sum_{s < t} delta_s z_s
+//          + sum_{j < t <= i} W_ij delta_j
 //   d delta_t = r_t + z_t + m_t + A dg_t
 //
 // The pass that forms the states (kStates, gdn_scan_mma.hip) also has the
@@ -27,8 +28,11 @@
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
 // enters them is held to fp32: the recurrences of S and Z, S and Z as
 // operands in two bf16 parts, G and M from the inputs as they are, <S, Z>
-// afresh in every chunk.  (One part would leave ddt_bias 5e-4 off; <S, Z>
-// carried along over two chunks, 3e-5.)
+// afresh in every chunk, and the pairs' sum of dg_t by halves of the chunk:
+// pairs from both halves by i (t in the second) or by j (t in the first),
+// terms that do not cancel; pairs inside a half as the sum over s >= t of
+// a_s - delta_s r_s.  (One part would leave ddt_bias 5e-4 off; <S, Z> carried
+// along over two chunks, 3e-5.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 #include "gdn_internal.h"
 #include "gdn_scan_mma.hpp"
@@ -232,9 +236,6 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
 #pragma unroll
       for (int s = 0; s < 4; ++s) df[s] = td.at(s, 0, VP);
     }
-    float ar[2][16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ar[0][i] = ar[1][i] = 0.f;
     float dD = 0.f;
     const auto out = raw_buffer(static_cast<bf16 *>(a.dx) + (t0 * a.Hv + h) * V + v0, (uint32_t)(((rows - 1) * ys + VW) * 2));
 #pragma unroll
@@ -246,9 +247,10 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       const float wj = g.w1[tj];
 #pragma unroll
       for (int i = 0; i < 16; ++i) T[i] *= wj;
-      float rs = 0.f, ms = 0.f;
+      float ms = 0.f;
 #pragma unroll
       for (int it = jt; it < 2; ++it) {
+        float rs = 0.f, ar[16];
         f32x16 P = zero16(), M = zero16();
         const bf16 *qi = q + (32 * it + r32) * KP + 8 * h2, *kj = k + tj * KP + 8 * h2;
 #pragma unroll
@@ -283,29 +285,24 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
             }
             const float wx = diag ? 0.f : wm;
             rs += wx;
-            ar[it][4 * b + e] += wx * dj;
+            ar[4 * b + e] = wx * dj;
           }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) T = mma32(df[2 * it + s], slots(P, s), T);
+        rs += __shfl_xor(rs, 32);
+        if (h2 == 0 && tj < rows) (it == jt ? w.r_part(a) : w.cross_part(a))[sums + tj] = rs;
+        const float v = fold16(ar, lane);
+        const int i = 32 * it + 8 * ((lane & 15) >> 2) + 4 * h2 + (lane & 3);
+        if (!(lane & 16) && i < rows) (it == jt ? w.a_part(a) : w.cross_part(a))[sums + i] = v;
         __builtin_amdgcn_sched_barrier(0);
       }
-      rs += __shfl_xor(rs, 32);
       ms += __shfl_xor(ms, 32);
-      if (h2 == 0 && tj < rows) {
-        w.r_part(a)[sums + tj] = rs;
-        w.m_part(a)[sums + tj] = ms;
-      }
+      if (h2 == 0 && tj < rows) w.m_part(a)[sums + tj] = ms;
 #pragma unroll
       for (int i = 0; i < 16; ++i) T[i] *= dj;
       put_rows(T, skip, dy + tj * VP, out, tj < rows ? (uint32_t)(tj * ys * 2) : kOutside, h2);
       __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      const float v = fold16(ar[it], lane);
-      const int i = 32 * it + 8 * ((lane & 15) >> 2) + 4 * h2 + (lane & 3);
-      if (!(lane & 16) && i < rows) w.a_part(a)[sums + i] = v;
     }
     dD = wave_sum(dD);
     if (lane == 0) {
@@ -562,6 +559,34 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   }
 }
 
+// Of the chunk's pairs j < t <= i, those inside one half of it: the chain of
+// dg_chain over the tokens of the half (tok = rows - 1 - lane).
+__device__ __forceinline__ double half_chain(double val, int cut, int tok, int lane) {
+  double dg = cut ? 0. : val;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const double later = __shfl_up(dg, d);
+    const int cut_later = __shfl_up(cut, d);
+    if (lane >= d && ((tok + d) ^ tok) < 32 && !cut) {
+      dg += later;
+      cut = cut_later;
+    }
+  }
+  return dg;
+}
+// The sum of `v` over the tokens before a lane's.  (No cut: the weights of the
+// terms are 0 where a token between them forgets all.)
+__device__ __forceinline__ double sum_before(double v, int lane) {
+  v = __shfl_down(v, 1);
+  if (lane == 63) v = 0.;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double more = __shfl_down(v, d);
+    if (lane + d < 64) v += more;
+  }
+  return v;
+}
+
 // The gates of one chunk and head: dg from the chunk's <S, Z> and its a, r, z,
 // then ddt and the chunk's parts of dA, ddt_bias, dD.  Lanes are tokens, lane
 // 0 the last.
@@ -581,10 +606,12 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const int slices = a.V / 32;
   const bool on = lane < rows;
   const int64_t t = loc.t1 - 1 - (on ? lane : 0);
-  double av = 0., rv = 0., ri = 0., mv = 0., x = 0., dD = 0.;
+  double av = 0., ai = 0., rv = 0., ri = 0., cross = 0., mv = 0., x = 0., dD = 0.;
   for (int s = 0; s < slices; ++s) {
     const int64_t i = ((int64_t)s * a.Hv + h) * a.s.tokens + t;
-    av += (double)w.a_part(a)[i] + (double)w.ai_part(a)[i];
+    av += w.a_part(a)[i];
+    ai += w.ai_part(a)[i];
+    cross += w.cross_part(a)[i];
     rv += w.r_part(a)[i];
     ri += w.ri_part(a)[i];
     mv += w.m_part(a)[i];
@@ -595,18 +622,12 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const float A = a.A[h];
   const float z = (float)static_cast<const bf16 *>(a.dt)[t * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
   const float delta = a.softplus ? softplusf(z) : z;
-  // the sum of delta_j z_j over the tokens before t (nothing is left of them
-  // where t or a later one forgets all: w_j is 0)
-  double before = on ? delta * ri : 0.;
-  before = __shfl_down(before, 1);
-  if (lane == 63) before = 0.;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double more = __shfl_down(before, d);
-    if (lane + d < 64) before += more;
-  }
-  const double dg = dg_chain(on ? av - delta * rv : 0., on && delta * A * kLog2e < kForget, x, lane) + before;
-  double dd = rv + ri + mv + A * dg;
+  const int tok = rows - 1 - lane;
+  const bool second = tok >= 32, cut = on && delta * A * kLog2e < kForget;
+  const double dg = dg_chain(on ? ai : 0., cut, x, lane) +
+                    half_chain(on ? av - delta * rv + (second ? cross : 0.) : 0., cut, tok, lane) +
+                    sum_before(on ? delta * ri : 0., lane) + (second ? 0. : 1.) * sum_before(on && !second ? delta * cross : 0., lane);
+  double dd = rv + (second ? 0. : cross) + ri + mv + A * dg;
   if (a.softplus) dd *= 1.f / (1.f + expf(-z));
   if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)(float)dd;
   const float dA = (float)wave_sum64(on ? delta * dg : 0.), dbias = (float)wave_sum64(on ? dd : 0.);

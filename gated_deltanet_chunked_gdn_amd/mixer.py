@@ -76,6 +76,12 @@ def _dtype(t, name):
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
+def _sizes(*sizes):
+    """The descriptors and slot counts are 32-bit; ctypes would cut a larger one."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"a size is beyond 32 bits: {sizes}")
+
+
 def _weight_dtype(x, *weights):
     """GDN dtype of the weights that are given (one type, x's or float32)."""
     given = [w for w in weights if w is not None]
@@ -165,6 +171,7 @@ def _like(t, shape, dtype, name):
 
 
 def _indices(idx, B, state, name="state_indices"):
+    _sizes(state.shape[0])
     if idx is None:
         if state.shape[0] < B:
             raise ValueError(f"state has {state.shape[0]} slots for {B} batch rows")
@@ -185,6 +192,7 @@ def _conv_problem(x, weight, bias, activation, lead):
     if activation not in (None, "silu"):
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
     D, W = weight.shape
+    _sizes(*x.shape, W)
     dt, wd = _dtype(x, "x"), _weight_dtype(x, weight, bias)
     xr, xs = _rows(x, lead)
     return ConvProblem(x.shape[0], x.shape[1] if lead == 2 else 1, D, W, x.shape[0], dt, wd,
@@ -276,6 +284,7 @@ def _scan_problem(c, b, x, dt, A, D, dt_bias, dt_softplus, lead):
         raise ValueError(f"dt must be {list(x.shape[:lead + 1])}, got {list(dt.shape)}")
     if not (c.dtype == b.dtype == x.dtype == dt.dtype):
         raise TypeError("c, b, x and dt must share one dtype")
+    _sizes(*x.shape, *c.shape)
     Hv = x.shape[lead]
     for t, name in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")):
         if t is None and name != "A":
@@ -298,7 +307,9 @@ def selective_scan_fwd(c, b, x, dt, A, D=None, dt_bias=None, dt_softplus: bool =
     h // (Hv // Hq)), x [B, T, Hv, V], dt [B, T, Hv] in one dtype; A, D,
     dt_bias float32 [Hv]; states float32 [N, Hv, K, V].  The token rows of c,
     b and x may be slices of a wider tensor.  A state that grows (A > 0) is
-    computed as it is, up to what float32 holds."""
+    computed as it is, up to what float32 holds.  A NaN or an infinity in a
+    token reaches the tokens of its 64-token chunk, earlier ones too, and all
+    later ones of its sequence; no other sequence."""
     p, c, b, x, dt, A, D, dt_bias = _scan_problem(c, b, x, dt, A, D, dt_bias, dt_softplus, 2)
     dev = x.device
     sq = _Seqs(cu_seqlens, p.B, p.T, dev, check_cu_seqlens)
@@ -379,6 +390,7 @@ def gated_delta_rule_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_
         raise ValueError("q, k must be [B,Hq,K] and v [B,Hv,V]")
     B, Hq, K = q.shape
     Hv, V = v.shape[1:]
+    _sizes(*q.shape, Hv, V)
     if tuple(g.shape) != (B, Hv) or tuple(beta.shape) != (B, Hv):
         raise ValueError("g and beta must be [B,Hv]")
     if k.dtype != q.dtype or v.dtype != q.dtype or beta.dtype != q.dtype:
@@ -407,6 +419,7 @@ def _norm_problem(x, weight, bias, gate, eps, rms):
     D = x.shape[-1] if x.dim() else 0
     if D == 0:
         raise ValueError(f"x must be [..., D] with D > 0, got {list(x.shape)}")
+    _sizes(D)
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None and tuple(t.shape) != (D,):
             raise ValueError(f"{name} must be [{D}], got {list(t.shape)}")

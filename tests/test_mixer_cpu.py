@@ -216,3 +216,17 @@ def test_strided_rows_are_taken_as_they_are():
     assert s == 16 and t.is_contiguous()
     t, s = mixer._rows(z(2, 5, 4, 64)[..., :32], 2)
     assert s == 128 and t.is_contiguous()
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """They would be cut in the descriptors (2^32 + 1 tokens to one)."""
+    n = (1 << 32) + 1
+    wide = lambda *shape, dt=BF: torch.empty(1, dtype=dt).expand(*shape)  # noqa: E731
+    for call in (
+            lambda: gdn.causal_conv_fwd(wide(1, n, 1), z(1, 2)),
+            lambda: gdn.causal_conv_step(wide(n, 1), z(3, 1, 1), z(1, 2)),
+            lambda: gdn.selective_scan_fwd(wide(1, n, 1, 32), wide(1, n, 1, 32), wide(1, n, 1, 32), wide(1, n, 1),
+                                           z(1, dt=torch.float32)),
+            lambda: gdn.layer_norm_fwd(wide(1, n))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
