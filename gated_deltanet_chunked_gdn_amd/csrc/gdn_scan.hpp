@@ -129,8 +129,8 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
 
 // Column slices of a head group that a workgroup of the matrix kernels has.
 // Eight hold a compute unit; with four, two workgroups of them, c and b come
-// in twice (8192 tokens x 64 heads: out pass 71 us against 68, the backward's
-// passes from zero 78 against 70).
+// in twice (8192 tokens x 64 heads, with the updates in two parts: out pass 71
+// us against 68, the backward's passes from zero 78 against 70).
 inline int slices_per_block(int per) { return per % 8 == 0 ? 8 : per % 4 == 0 ? 4 : per % 2 == 0 ? 2 : 1; }
 // bf16, gdn_scan_mma.hip
 hipError_t launch_mma_local(const ScanArgs &a, const Layout &w, hipStream_t st);

@@ -34,6 +34,11 @@
 // a_s - delta_s r_s.  (One part would leave ddt_bias 5e-4 off; <S, Z> carried
 // along over two chunks, 3e-5.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
+//
+// 2 x 4096 tokens x 64 heads, K 128, V 64: passes from zero 78 us, carries 17,
+// states 112, grad_kernel 172, pair_kernel 135, gates 25.  S and Z of every
+// chunk, 0.8 GB written and read again, are what the middle three move beside
+// the tensors, at 3.3 to 3.6 TB/s.
 #include "gdn_internal.h"
 #include "gdn_scan_mma.hpp"
 

@@ -11,7 +11,9 @@
 // their way while one is worked on.  (One wave a SIMD with 64 columns: 171 us
 // for the out pass at 8192 tokens x 64 heads, K 128, V 64, the state in
 // accumulation registers that vector instructions reach only by moves; this
-// form 68 us.)
+// form 68 us, and 74 with the exact state updates below.)  The pass from zero
+// takes 41 us there: both are bound by latency, one workgroup a compute unit
+// going in step from barrier to barrier.
 //
 // Everything is arranged so that accumulators are operands without moving
 // (gdn_slice.hpp): S tiles (rows k, lane v) give S^T for c; C B^T is formed

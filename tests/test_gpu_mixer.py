@@ -593,3 +593,54 @@ def test_fewer_tokens_than_the_batch(gdn):
                                              None, torch.cuda.current_stream().cuda_stream)
     assert rc == 0
     assert bool((y[:, 60:] == 7).all()) and not bool((y[:, :60] == 7).all())
+
+
+def test_offsets_past_32_bits(gdn):
+    """The last rows of tensors of more than 2^31 elements are what the same
+    rows give alone."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    rnd = lambda *shape, dt=torch.bfloat16: torch.randn(*shape, generator=g, device="cuda", dtype=dt)  # noqa: E731
+    T, D = 270_000, 8192
+    x, w = rnd(1, T, D), rnd(D, 4)
+    announce("offsets conv")
+    y, _ = gdn.causal_conv_fwd(x, w)
+    one, _ = gdn.causal_conv_fwd(x[:, -40:].clone(), w, initial_state=x[:, -43:-40].clone())
+    assert torch.equal(y[:, -40:], one)
+    dy = y
+    dx, _, _, _ = gdn.causal_conv_bwd(x, w, None, dy)
+    one, _, _, _ = gdn.causal_conv_bwd(x[:, -40:].clone(), w, None, dy[:, -40:].clone(),
+                                       initial_state=x[:, -43:-40].clone())
+    assert torch.equal(dx[:, -40:], one)
+    del y, dy, dx
+    announce("offsets norm")
+    rows = x.view(T * 2, D // 2)
+    y, mean, rstd = gdn.layer_norm_fwd(rows, gate=rows)
+    dx, _, _, dg = gdn.layer_norm_bwd(rows, rows, None, None, mean, rstd, gate=rows)
+    last = rows[-50:].clone()
+    yl, ml, rl = gdn.layer_norm_fwd(last, gate=last)
+    dxl, _, _, dgl = gdn.layer_norm_bwd(last, last, None, None, ml, rl, gate=last)
+    for u, v in ((y, yl), (mean, ml), (rstd, rl), (dx, dxl), (dg, dgl)):
+        assert torch.equal(u[-50:], v)
+    del y, dx, dg, rows
+    announce("offsets scan")
+    x = x.view(1, T, 128, 64)
+    c, b = rnd(1, T, 2, 32), rnd(1, T, 2, 32)
+    dt, A = rnd(1, T, 128), -torch.ones(128, device="cuda")
+    cut = T - 200
+    cu = torch.tensor([0, cut, T], dtype=torch.int32)
+    y, ht = gdn.selective_scan_fwd(c, b, x, dt, A, cu_seqlens=cu)
+    tail = [t[:, cut:].clone() for t in (c, b, x, dt)]
+    yl, hl = gdn.selective_scan_fwd(*tail, A)
+    near("y", y[:, cut:], dbl(yl), SCAN["bf16"])
+    near("ht", ht[1:], dbl(hl), F32)
+    del y, ht, x
+    announce("offsets step")
+    slots = 4200  # 4200 x 32 x 128 x 128: 2.2e9 elements
+    state = torch.zeros(slots, 32, 128, 128, device="cuda")
+    q, k, v = rnd(2, 16, 128), rnd(2, 16, 128), rnd(2, 32, 128)
+    gg, beta = -torch.rand(2, 32, generator=g, device="cuda"), rnd(2, 32)
+    o = gdn.gated_delta_rule_step(q, k, v, gg, beta, state, state_indices=torch.tensor([slots - 1, 0], dtype=torch.int32).cuda())
+    small = torch.zeros(2, 32, 128, 128, device="cuda")
+    assert torch.equal(o, gdn.gated_delta_rule_step(q, k, v, gg, beta, small))
+    assert torch.equal(state[-1], small[0]) and torch.equal(state[0], small[1])
+    assert not state[1:-1].any()
