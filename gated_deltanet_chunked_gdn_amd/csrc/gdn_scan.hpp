@@ -30,7 +30,7 @@ struct SlotLoc {
 
 // Byte offsets of the workspace's pieces (each at a 256-byte boundary).
 struct Layout {
-  size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_ri = 0, o_cross = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
+  size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_ri = 0, o_half = 0, o_quarter = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
          o_dc = 0, o_db = 0, o_ai = 0, o_shi = 0, o_slo = 0, o_z = 0, total = 0;
   int64_t chunks = 0;      // slots of 64-token chunks (bf16 backward)
   bool need_last = false;  // the local pass runs a sequence's last segment too
@@ -54,8 +54,9 @@ struct Layout {
   __host__ __device__ float *ai_part(const ScanArgs &a) const { return at(a, o_ai); }
   __host__ __device__ float *ri_part(const ScanArgs &a) const { return at(a, o_ri); }
   // and what pairs of tokens from both halves of a chunk add, to r in the
-  // first half, to a in the second
-  __host__ __device__ float *cross_part(const ScanArgs &a) const { return at(a, o_cross); }
+  // first half, to a in the second; pairs from both quarters of a half likewise
+  __host__ __device__ float *half_part(const ScanArgs &a) const { return at(a, o_half); }
+  __host__ __device__ float *quarter_part(const ScanArgs &a) const { return at(a, o_quarter); }
   // parts of dD: [slices][slots, bf16: chunks][Hv]
   __host__ __device__ float *dd_part(const ScanArgs &a) const { return at(a, o_dd); }
   // [slices][chunks][Hv]: parts of 2^{gamma_L} <S, Z>, S entering the chunk, Z
@@ -113,7 +114,8 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_m = piece(tok * slices * 4);
     w.o_ai = piece(tok * slices * 4);
     w.o_ri = piece(tok * slices * 4);
-    w.o_cross = piece(tok * slices * 4);
+    w.o_half = piece(tok * slices * 4);
+    w.o_quarter = piece(tok * slices * 4);
     w.o_dd = piece(ch * slices * 4);
     w.o_x = piece(ch * slices * 4);
     w.o_head = piece(ch * 3 * 4);

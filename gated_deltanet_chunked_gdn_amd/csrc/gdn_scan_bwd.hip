@@ -28,15 +28,17 @@
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
 // enters them is held to fp32: the recurrences of S and Z, S and Z as
 // operands in two bf16 parts, G and M from the inputs as they are, <S, Z>
-// afresh in every chunk, and the pairs' sum of dg_t by halves of the chunk:
-// pairs from both halves by i (t in the second) or by j (t in the first),
-// terms that do not cancel; pairs inside a half as the sum over s >= t of
-// a_s - delta_s r_s.  (One part would leave ddt_bias 5e-4 off; <S, Z> carried
-// along over two chunks, 3e-5.)
+// afresh in every chunk, and the pairs' sum of dg_t by halves and quarters of
+// the chunk: pairs from both halves by i (t in the second) or by j (t in the
+// first), terms that do not cancel; so the pairs from both quarters of a half;
+// pairs inside a quarter as the sum over s >= t of a_s - delta_s r_s, where
+// they cancel if both are behind t.  (S and Z in one part would leave ddt_bias
+// 5e-4 off; <S, Z> carried along over two chunks, 3e-5; the last sum over the
+// whole chunk 2.3e-6 against 1.1e-6 by halves.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 //
 // 2 x 4096 tokens x 64 heads, K 128, V 64: passes from zero 78 us, carries 17,
-// states 112, grad_kernel 172, pair_kernel 135, gates 25.  S and Z of every
+// states 114, grad_kernel 180, pair_kernel 138, gates 26.  S and Z of every
 // chunk, 0.8 GB written and read again, are what the middle three move beside
 // the tensors, at 3.3 to 3.6 TB/s.
 #include "gdn_internal.h"
@@ -46,8 +48,8 @@ namespace gdn {
 namespace scan {
 namespace {
 
-// Sum over the 32 lanes of a half of 16 registers each: lane l ends with the
-// sum of register l & 15.
+// Sums over the 16 lanes of a quarter of 16 registers each: lane l ends with
+// the sum of register l & 15.
 __device__ __forceinline__ float fold16(float (&r)[16], int lane) {
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
@@ -65,9 +67,7 @@ __device__ __forceinline__ float fold16(float (&r)[16], int lane) {
     r[n] = (b ? r[2 * n + 1] : r[2 * n]) + __shfl_xor(b ? r[2 * n] : r[2 * n + 1], 4);
   }
   const bool b = lane & 8;
-  float v = (b ? r[1] : r[0]) + __shfl_xor(b ? r[0] : r[1], 8);
-  v += __shfl_xor(v, 16);
-  return v;
+  return (b ? r[1] : r[0]) + __shfl_xor(b ? r[0] : r[1], 8);
 }
 
 // fp32 dot product of two bf16x8, added to c
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       float ms = 0.f;
 #pragma unroll
       for (int it = jt; it < 2; ++it) {
-        float rs = 0.f, ar[16];
+        float rs[2] = {0.f, 0.f}, ar[16];  // (rs: of i in the tile's first and second 16 rows)
         f32x16 P = zero16(), M = zero16();
         const bf16 *qi = q + (32 * it + r32) * KP + 8 * h2, *kj = k + tj * KP + 8 * h2;
 #pragma unroll
@@ -289,17 +289,26 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
               dD += diag ? M[4 * b + e] : 0.f;
             }
             const float wx = diag ? 0.f : wm;
-            rs += wx;
+            rs[b >> 1] += wx;
             ar[4 * b + e] = wx * dj;
           }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) T = mma32(df[2 * it + s], slots(P, s), T);
-        rs += __shfl_xor(rs, 32);
-        if (h2 == 0 && tj < rows) (it == jt ? w.r_part(a) : w.cross_part(a))[sums + tj] = rs;
-        const float v = fold16(ar, lane);
+        rs[0] += __shfl_xor(rs[0], 32);
+        rs[1] += __shfl_xor(rs[1], 32);
+        const float lo = fold16(ar, lane), hi = __shfl_xor(lo, 16);  // j in the tile's first, second 16 columns (lanes of the first)
         const int i = 32 * it + 8 * ((lane & 15) >> 2) + 4 * h2 + (lane & 3);
-        if (!(lane & 16) && i < rows) (it == jt ? w.a_part(a) : w.cross_part(a))[sums + i] = v;
+        const bool put_r = h2 == 0 && tj < rows, put_a = !(lane & 16) && i < rows;
+        if (it != jt) {
+          if (put_r) w.half_part(a)[sums + tj] = rs[0] + rs[1];
+          if (put_a) w.half_part(a)[sums + i] = lo + hi;
+        } else {
+          if (put_r) w.r_part(a)[sums + tj] = r32 & 16 ? rs[1] : rs[0];
+          if (put_r && !(r32 & 16)) w.quarter_part(a)[sums + tj] = rs[1];
+          if (put_a) w.a_part(a)[sums + i] = i & 16 ? hi : lo;
+          if (put_a && (i & 16)) w.quarter_part(a)[sums + i] = lo;
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       ms += __shfl_xor(ms, 32);
@@ -564,27 +573,38 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   }
 }
 
-// Of the chunk's pairs j < t <= i, those inside one half of it: the chain of
-// dg_chain over the tokens of the half (tok = rows - 1 - lane).
-__device__ __forceinline__ double half_chain(double val, int cut, int tok, int lane) {
+// Tokens of `width` in a row, tok = rows - 1 - lane: the chain of dg_chain over
+// the pairs inside them.
+__device__ __forceinline__ double inner_chain(double val, int cut, int tok, int lane, int width) {
   double dg = cut ? 0. : val;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
+  for (int d = 1; d < width; d <<= 1) {
     const double later = __shfl_up(dg, d);
     const int cut_later = __shfl_up(cut, d);
-    if (lane >= d && ((tok + d) ^ tok) < 32 && !cut) {
+    if (lane >= d && ((tok + d) ^ tok) < width && !cut) {
       dg += later;
       cut = cut_later;
     }
   }
   return dg;
 }
-// The sum of `v` over the tokens before a lane's.  (No cut: the weights of the
-// terms are 0 where a token between them forgets all.)
+// The pairs from two such neighbours: for t in the second, the sum of v over
+// its tokens from t on (a_i); in the first, over its tokens before t (delta_j
+// r_j).  (No cut: the terms are 0 where a token between i and j forgets all.)
+__device__ __forceinline__ double outer_sum(double v, int tok, int lane, int width) {
+  const bool second = tok & width;
+  const double prior = __shfl_down(v, 1);
+  if (!second) v = lane < 63 && (tok & (width - 1)) ? prior : 0.;
+  for (int d = 1; d < width; d <<= 1) {
+    const int from = second ? lane - d : lane + d, at = second ? tok + d : tok - d;
+    const double more = __shfl(v, from & 63);
+    if (from >= 0 && from < 64 && (at ^ tok) < width && at >= 0) v += more;
+  }
+  return v;
+}
+// The sum of v over the tokens before a lane's (no cut either).
 __device__ __forceinline__ double sum_before(double v, int lane) {
   v = __shfl_down(v, 1);
   if (lane == 63) v = 0.;
-#pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const double more = __shfl_down(v, d);
     if (lane + d < 64) v += more;
@@ -611,12 +631,13 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const int slices = a.V / 32;
   const bool on = lane < rows;
   const int64_t t = loc.t1 - 1 - (on ? lane : 0);
-  double av = 0., ai = 0., rv = 0., ri = 0., cross = 0., mv = 0., x = 0., dD = 0.;
+  double av = 0., ai = 0., rv = 0., ri = 0., half = 0., quarter = 0., mv = 0., x = 0., dD = 0.;
   for (int s = 0; s < slices; ++s) {
     const int64_t i = ((int64_t)s * a.Hv + h) * a.s.tokens + t;
     av += w.a_part(a)[i];
     ai += w.ai_part(a)[i];
-    cross += w.cross_part(a)[i];
+    half += w.half_part(a)[i];
+    quarter += w.quarter_part(a)[i];
     rv += w.r_part(a)[i];
     ri += w.ri_part(a)[i];
     mv += w.m_part(a)[i];
@@ -628,11 +649,12 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const float z = (float)static_cast<const bf16 *>(a.dt)[t * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
   const float delta = a.softplus ? softplusf(z) : z;
   const int tok = rows - 1 - lane;
-  const bool second = tok >= 32, cut = on && delta * A * kLog2e < kForget;
-  const double dg = dg_chain(on ? ai : 0., cut, x, lane) +
-                    half_chain(on ? av - delta * rv + (second ? cross : 0.) : 0., cut, tok, lane) +
-                    sum_before(on ? delta * ri : 0., lane) + (second ? 0. : 1.) * sum_before(on && !second ? delta * cross : 0., lane);
-  double dd = rv + (second ? 0. : cross) + ri + mv + A * dg;
+  const bool cut = on && delta * A * kLog2e < kForget, late32 = tok & 32, late16 = tok & 16;
+  const double dg = dg_chain(on ? ai : 0., cut, x, lane) + sum_before(on ? delta * ri : 0., lane) +
+                    outer_sum(on ? (late32 ? half : delta * half) : 0., tok, lane, 32) +
+                    outer_sum(on ? (late16 ? quarter : delta * quarter) : 0., tok, lane, 16) +
+                    inner_chain(on ? av - delta * rv : 0., cut, tok, lane, 16);
+  double dd = rv + (late16 ? 0. : quarter) + (late32 ? 0. : half) + ri + mv + A * dg;
   if (a.softplus) dd *= 1.f / (1.f + expf(-z));
   if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)(float)dd;
   const float dA = (float)wave_sum64(on ? delta * dg : 0.), dbias = (float)wave_sum64(on ? dd : 0.);
