@@ -38,7 +38,7 @@
 // dx, dc and db are bf16 themselves and take their operands rounded.
 //
 // 2 x 4096 tokens x 64 heads, K 128, V 64: passes from zero 78 us, carries 17,
-// states 114, grad_kernel 180, pair_kernel 138, gates 26.  S and Z of every
+// states 112, grad_kernel 176, pair_kernel 129, gates 26.  S and Z of every
 // chunk, 0.8 GB written and read again, are what the middle three move beside
 // the tensors, at 3.3 to 3.6 TB/s.
 #include "gdn_internal.h"
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
   using D = Dims<K, V>;
   constexpr int VW = D::VW, KT = D::KT, KP = D::KP, VP = D::VP, THREADS = 64 * NW;
   __shared__ __align__(16) bf16 Ql[64 * KP], Kl[64 * KP], Xl[NW][64 * VP], Dl[NW][64 * VP];
-  __shared__ __align__(16) GatesCore G[NW];
+  __shared__ __align__(16) FineGates G[NW];
   const int tid0 = threadIdx.x, wave = wave_of(tid0);
   const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
   const int blk = (int)(item % blocks_per_group), hq = (int)(item / blocks_per_group % a.Hq);
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     const int64_t t0 = loc.t0 + 64 * (int64_t)c;
-    GatesCore &g = G[wave];
+    FineGates &g = G[wave];
     const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
     const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
     const int64_t sums = ((int64_t)vs * a.Hv + h) * a.s.tokens + t0;  // of a_part, r_part, m_part
@@ -489,19 +489,18 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
       const bf16 *yi = Dl + (32 * it + r32) * UP + 8 * h2, *xj = Xl + (32 * jt + r32) * UP + 8 * h2;
 #pragma unroll
       for (int s = 0; s < UC / 16; ++s) M = mma32(lds16(yi + 16 * s), lds16(xj + 16 * s), M);
-      const float gj = g.gam[32 * jt + r32], lj = g.rest[32 * jt + r32], dj = g.del[32 * jt + r32], uj = g.u[r32];
+      const float gj = g.gam[32 * jt + r32], dj = g.del[32 * jt + r32], uj = g.u[r32];
       const int lim = next_bit(above(Gm[u & 1][jt], r32));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int i0 = 8 * b + 4 * h2;
         const f32x4 gi = *reinterpret_cast<const f32x4 *>(it == jt ? &g.gam[32 * it + i0] : &g.e[i0]);
-        const f32x4 li = *reinterpret_cast<const f32x4 *>(&g.rest[32 * it + i0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = i0 + e;
           float E;
           if (it == jt)
-            E = exp2_if(i >= r32 && i < lim, (gi[e] - gj) + (li[e] - lj)) * dj;
+            E = exp2_if(i >= r32 && i < lim, gi[e] - gj) * dj;
           else
             E = gi[e] * uj;
           Nacc[4 * b + e] += E * M[4 * b + e];

@@ -11,7 +11,7 @@
 // their way while one is worked on.  (One wave a SIMD with 64 columns: 171 us
 // for the out pass at 8192 tokens x 64 heads, K 128, V 64, the state in
 // accumulation registers that vector instructions reach only by moves; this
-// form 68 us, and 74 with the exact state updates below.)  The pass from zero
+// form 68 us, and 73 with the exact state updates below.)  The pass from zero
 // takes 41 us there: both are bound by latency, one workgroup a compute unit
 // going in step from barrier to barrier.
 //
@@ -174,7 +174,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
           if (it) Po = mma32(lds16(ko + 16 * s), qf, Po);
           if ((s & 3) == 3) __builtin_amdgcn_sched_barrier(0);
         }
-        const float gi = g.gam[32 * it + r32], li = g.rest[32 * it + r32];  // of token i, from its half's start
+        const float gi = g.gam[32 * it + r32];  // of token i, from its half's start
         const uint32_t f = upto(it ? gt.m1 : gt.m0, r32);
         const float ei = it ? g.e[r32] : 0.f, e0 = g.p[32 * it + r32];
         const int first = last_bit(f);  // the first token of the half that token i sees
@@ -184,13 +184,12 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         for (int b = 0; b < 4; ++b) {
           const int j0 = 8 * b + 4 * h2;
           const f32x4 gj = *reinterpret_cast<const f32x4 *>(&g.gam[32 * it + j0]);
-          const f32x4 lj = *reinterpret_cast<const f32x4 *>(&g.rest[32 * it + j0]);
           const f32x4 dj = *reinterpret_cast<const f32x4 *>(&g.del[32 * it + j0]);
           const f32x4 uj = *reinterpret_cast<const f32x4 *>(&g.u[j0]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + i;
-            Pd[4 * b + i] *= exp2_if(j <= r32 && j >= first, (gi - gj[i]) + (li - lj[i])) * dj[i];
+            Pd[4 * b + i] *= exp2_if(j <= r32 && j >= first, gi - gj[i]) * dj[i];
             if (it) Po[4 * b + i] *= ei * uj[i];
           }
         }

@@ -108,9 +108,17 @@ __device__ __forceinline__ bf16 load_dt(const bf16 *dt, int64_t stride, int rows
 // (rest, below 2^-13 each).  A token whose own decay is below 2^kForget ends
 // all that is before it; it counts as an exact 0 and stays out of the sums, so
 // that a half's stays below 2^12.  m0, m1 mark such tokens of the halves.
+//
+// The reverse pass, whose pairs' decays reach fp32 gradients, keeps gam and
+// rest apart (FineGates); where only bf16 outputs see them (Gates) gam is the
+// sum of both, off by 2^-25 of itself (8192 tokens x 64 heads, both apart: out
+// pass 76 us against 73).
 constexpr float kForget = -126.f;
 struct GatesCore {
-  float gam[64], rest[64], del[64], w1[64], p[64], u1[32], e[32];
+  float gam[64], del[64], w1[64], p[64], u1[32], e[32];
+};
+struct FineGates : GatesCore {
+  float rest[64];
 };
 struct Gates : GatesCore {
   float w[64], u[32];
@@ -137,18 +145,19 @@ __device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softpl
   GateTotals t{h0 + r0, h1 + r1, (uint32_t)m, (uint32_t)(m >> 32)};
   const int i = lane & 31;
   const uint32_t later = lane < 32 ? above(t.m0, i) : above(t.m1, i);
-  s.gam[lane] = gam;
-  s.rest[lane] = rest;
+  constexpr bool fine = __is_same(G, FineGates);
+  s.gam[lane] = fine ? gam : gam + rest;
+  if constexpr (fine) s.rest[lane] = rest;
   s.del[lane] = d;
   const uint32_t before = upto(lane < 32 ? t.m0 : t.m1, i) | (lane < 32 ? 0u : t.m0);
   s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam + rest : (h0 + gam) + (r0 + rest));
   const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? ((h0 - gam) + h1) + ((r0 - rest) + r1) : (h1 - gam) + (r1 - rest));
   s.w1[lane] = w1;
-  if constexpr (sizeof(G) == sizeof(Gates)) s.w[lane] = w1 * d;
+  if constexpr (!fine) s.w[lane] = w1 * d;
   if (lane < 32) {
     const float u1 = later ? 0.f : exp2_hw((h0 - gam) + (r0 - rest));
     s.u1[lane] = u1;
-    if constexpr (sizeof(G) == sizeof(Gates)) s.u[lane] = u1 * d;
+    if constexpr (!fine) s.u[lane] = u1 * d;
   } else {
     s.e[lane - 32] = upto(t.m1, i) ? 0.f : exp2_hw(gam + rest);
   }
