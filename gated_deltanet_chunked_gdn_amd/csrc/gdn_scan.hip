@@ -9,17 +9,14 @@
 //
 //   Z_t = c_t dy_t^T + Z'_t,  Z'_t = e^{g_{t+1}} Z_{t+1}
 //   dc_t = S_t dy_t,  db_t = delta_t Z_t x_t,  dx_t = delta_t Z_t^T b_t + D dy_t
-//   dg_t = <e^{g_t} S_{t-1}, Z_t> = dg_{t+1} + a_t - delta_t r_t,
-//     a_t = c_t . e^{g_t} S_{t-1} dy_t,  r_t = x_t . Z'_t^T b_t
-//     (a token's own product (c.b)(x.dy) is in both <S_t, c dy^T> and
-//     delta <b x^T, Z_t> and is left out of both, so that it cancels exactly)
-//   d delta_t = r_t + m_t + A dg_t,  m_t = (c_t . b_t)(x_t . dy_t)
+//   dg_t = <e^{g_t} S_{t-1}, Z_t>
+//   d delta_t = r_t + m_t + A dg_t,
+//     r_t = x_t . Z'_t^T b_t,  m_t = (c_t . b_t)(x_t . dy_t)
 //
 // Sequences are cut into segments that run side by side: a pass over every
 // segment from a zero state, a scan of the segments' ends, and the pass that
 // writes the results from the true start states (backward: the same in
-// reverse order for Z).  The chain of dg is begun again from <S, Z> at every
-// segment's end, which keeps the sums short.
+// reverse order for Z).
 //
 // The kernels of this file hold the state in fp32 registers, one column (or
 // row) of it a lane, and walk token by token: they are the form for fp32
@@ -61,7 +58,7 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
   const int sl = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv;
   const int64_t slot = blockIdx.x / slices / a.Hv;
   const SlotLoc loc = locate(a, slot);
-  if (!loc.used || (MODE == kLocal && loc.last && !w.need_last)) return;
+  if (!loc.used || (MODE == kLocal && loc.last)) return;
   const int hq = h / (a.Hv / a.Hq);
   const int l = sl * 64 + lane;
   const bool on = l < s.LD;
@@ -141,11 +138,6 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
       } else if (MODE == kDc || MODE == kDb) {
         float *part = MODE == kDc ? w.dc_part(a) : w.db_part(a);
         if (on) part[(t * a.Hv + h) * a.K + l] = MODE == kDc ? out + f * up : delta * out;
-        if (MODE == kDc) {
-          const float c = to_f32(static_cast<const E *>(a.c)[t * a.cs + (int64_t)hq * a.K + lc]);
-          const float v = wave_sum(on ? c * out : 0.f);
-          if (lane == 0) w.a_part(a)[((int64_t)sl * a.Hv + h) * a.s.tokens + t] = v;
-        }
       } else if (MODE == kDx) {
         const float x = to_f32(static_cast<const E *>(a.x)[t * a.xs + (int64_t)h * a.V + lc]);
         if (on) static_cast<E *>(a.dx)[(t * a.Hv + h) * a.V + l] = from_f32<E>(delta * (out + f * up) + skip * mine);
@@ -163,7 +155,8 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
     float *dst = (MODE == kLocal ? w.start(a) : w.zend(a)) + (slot * a.Hv + h) * kv;
     if (on)
       for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
-    if (MODE == kLocal && lane == 0 && sl == 0) w.decay(a)[slot * a.Hv + h] = total;
+    // (in the backward the reverse pass, which has every segment: one writer)
+    if ((MODE == kRLocal || !a.dy) && lane == 0 && sl == 0) w.decay(a)[slot * a.Hv + h] = total;
   }
   if (MODE == kOut && loc.last && a.ht && on) {
     float *dst = a.ht + (loc.n * (int64_t)a.Hv + h) * kv;
@@ -174,10 +167,9 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
   }
 }
 
-// The segments' local ends -> every segment's start state (in place), and in
-// the backward the sequence's last state.  One thread has 4 elements of one
-// head's state.
-__device__ __forceinline__ void carry(const ScanArgs &a, const Layout &w, float *hend, int64_t i) {
+// The segments' local ends -> every segment's start state (in place).  One
+// thread has 4 elements of one head's state.
+__device__ __forceinline__ void carry(const ScanArgs &a, const Layout &w, int64_t i) {
   const int64_t kv4 = (int64_t)a.K * a.V / 4;
   const int64_t e = i % kv4, h = i / kv4 % a.Hv, n = i / kv4 / a.Hv;
   if (n >= a.s.N) return;
@@ -188,7 +180,7 @@ __device__ __forceinline__ void carry(const ScanArgs &a, const Layout &w, float 
   if (a.h0) cur = reinterpret_cast<const f32x4 *>(a.h0)[own];
   f32x4 *H = reinterpret_cast<f32x4 *>(w.start(a)) + (slot * a.Hv + h) * kv4 + e;
   const float *g = w.decay(a) + slot * a.Hv + h;
-  const int64_t step = a.Hv * kv4, read = w.need_last ? ns : ns - 1;  // segments whose own state is there
+  const int64_t step = a.Hv * kv4, read = ns - 1;  // segments whose own state is there
   for (int64_t s = 0; s < ns; s += kAhead) {
     f32x4 x[kAhead];
     float d[kAhead];
@@ -208,7 +200,6 @@ __device__ __forceinline__ void carry(const ScanArgs &a, const Layout &w, float 
       for (int k = 0; k < 4; ++k) cur[k] = f * cur[k] + x[j][k];
     }
   }
-  if (hend) reinterpret_cast<f32x4 *>(hend)[own] = cur;
 }
 
 // In reverse: every segment's local gradient of its start state -> the
@@ -247,72 +238,179 @@ __device__ __forceinline__ void rcarry(const ScanArgs &a, const Layout &w, int64
 }
 
 // Both in one launch where there are both (`blocks` workgroups each).
-__global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, float *hend, int64_t blocks) {
+__global__ __launch_bounds__(256) void carry_kernel(ScanArgs a, Layout w, int64_t blocks) {
   const int64_t b = blockIdx.x;
   if (b < blocks)
-    carry(a, w, hend, b * 256 + threadIdx.x);
+    carry(a, w, b * 256 + threadIdx.x);
   else
     rcarry(a, w, (b - blocks) * 256 + threadIdx.x);
 }
 
-// dg from a_t, r_t and m_t, then ddt and the segment's part of dA, ddt_bias and
-// dD.  One wave has one segment of one head, 64 tokens at a time from its
-// end, begun from <S, Z> of its last state.
-template <typename E>
-__global__ __launch_bounds__(64) void gates_kernel(ScanArgs a, Layout w, int kslices, int vslices) {
-  const int lane = threadIdx.x, h = blockIdx.x % a.Hv;
-  const int64_t slot = blockIdx.x / a.Hv;
-  const SlotLoc loc = locate(a, slot);
-  float *part = w.head_part(a) + (slot * a.Hv + h) * 3;
-  if (!loc.used) {
-    if (lane < 3) part[lane] = 0.f;
-    return;
-  }
-  const int64_t kv4 = (int64_t)a.K * a.V / 4;
-  const f32x4 *se = reinterpret_cast<const f32x4 *>(
-      loc.last ? w.hend(a) + (loc.n * (int64_t)a.Hv + h) * kv4 * 4 : w.start(a) + ((slot + 1) * a.Hv + h) * kv4 * 4);
-  const f32x4 *ze = reinterpret_cast<const f32x4 *>(w.zend(a) + (slot * a.Hv + h) * kv4 * 4);
-  double x = 0.;
-  for (int64_t i = lane; i < kv4; i += 64) {
-    const f32x4 p = se[i], q = ze[i];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x += (double)p[k] * q[k];
-  }
-  double dg_next = wave_sum64(x);
-  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-  double dA = 0., dbias = 0.;
-  for (int64_t e = loc.t1; e > loc.t0; e -= 64) {
-    const int64_t t = e - 1 - lane;  // lane 0 has the last token
-    const bool on = t >= loc.t0;
-    double av = 0., rv = 0., mv = 0.;
-    float z = 0.f;
-    if (on) {
-      for (int s = 0; s < kslices; ++s) av += w.a_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
-      for (int s = 0; s < vslices; ++s) {
-        rv += w.r_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
-        mv += w.m_part(a)[((int64_t)s * a.Hv + h) * a.s.tokens + t];
-      }
-      z = to_f32(static_cast<const E *>(a.dt)[t * a.Hv + h]) + bias;
+// dg, then ddt and the segment's part of dA, ddt_bias and dD.
+//
+// dg_t = <e^{g_t} S_{t-1}, Z_t> of a segment whose first state is S0 and whose
+// last state has the gradient Z1, with E_ij the decay from token j to i, p_t
+// that from the segment's start to t and w_t that from t to its end:
+//
+//   dg_t = p_end <S0, Z1> + sum_{i >= t} p_i c_i . S0 dy_i + sum_{j < t} delta_j w_j b_j . Z1 x_j
+//          + sum_{j < t <= i} E_ij delta_j (c_i . b_j)(dy_i . x_j)
+//
+// which is the product taken apart: nothing cancels that does not cancel in it.
+// (As the chain dg_{t+1} + c_t . e^{g_t} S_{t-1} dy_t - delta_t r_t it was off by
+// 3e-3 of dA where tokens forget to e^-9 and dg is far below both terms.)
+//
+// A workgroup has one segment (64 tokens at the most) of one head, a wave 16 of
+// its tokens: their rows of C B^T and DY X^T, S0 dy and Z1 x, all by fp32
+// matrix instructions.  Log decays are summed in 64 bits, so that the decay
+// between two tokens is as good as its own logarithm.
+//
+// 2 x 4096 tokens x 16 heads, K = V = 64: 83 us (the chain: 19, of a backward of
+// 590), three workgroups a compute unit by registers and latency of the steps.
+template <int K, int V>
+__global__ __launch_bounds__(256, 3) void gates_kernel(ScanArgs a, Layout w) {
+  constexpr int KF = K / 16, VF = V / 16, P = V + 4, WP = 65;
+  __shared__ __align__(16) float mats[2 * K * P > 64 * WP ? 2 * K * P : 64 * WP];  // S0 and Z1, then the pairs
+  __shared__ double gam[64];
+  __shared__ float del[64], own[2][64], pairs[64];
+  float *const s0 = mats, *const z1 = mats + K * P;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), l16 = lane & 15, q = lane >> 4;
+  const int64_t units = a.slots * a.Hv;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int h = (int)(unit % a.Hv), hq = h / (a.Hv / a.Hq);
+    const SlotLoc loc = locate(a, unit / a.Hv);
+    float *part = w.head_part(a) + unit * 3;
+    const int nt = loc.used ? (int)(loc.t1 - loc.t0) : 0;
+    if (nt <= 0) {
+      if (tid < 3) part[tid] = 0.f;
+      continue;
     }
-    const float delta = on ? (a.softplus ? softplusf(z) : z) : 0.f;
-    const double dg = dg_chain(on ? av - delta * rv : 0., on && delta * A < -20.f, dg_next, lane);
-    dg_next = __shfl(dg, 63);
+    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    auto dt_at = [&](int tok) { return static_cast<const float *>(a.dt)[(loc.t0 + tok) * a.Hv + h] + bias; };
+    __syncthreads();  // the unit before is done with LDS
+    for (int i = tid; i < K * V / 4; i += 256) {
+      const int at = i / (V / 4) * P + i % (V / 4) * 4;
+      *reinterpret_cast<f32x4 *>(s0 + at) = reinterpret_cast<const f32x4 *>(w.start(a) + unit * K * V)[i];
+      *reinterpret_cast<f32x4 *>(z1 + at) = reinterpret_cast<const f32x4 *>(w.zend(a) + unit * K * V)[i];
+    }
+    if (wave == 0) {
+      const float z = dt_at(lane < nt ? lane : nt - 1);
+      const float delta = lane < nt ? (a.softplus ? softplusf(z) : z) : 0.f, g = delta * A;
+      gam[lane] = sum_upto(g < -1e4f ? -1e4f : g, lane);  // (e^-1e4 is 0; an infinity would leave no difference)
+      del[lane] = delta;
+    }
+    __syncthreads();
+    // rows of the tokens 16 blk + l16, elements 16 s + 4 q ..
+    auto rows = [&](f32x4 *r, const void *p, int64_t stride, int col, int blk, int frags) {
+      const int tok = 16 * blk + l16 < nt ? 16 * blk + l16 : nt - 1;
+      const float *e = static_cast<const float *>(p) + (loc.t0 + tok) * stride + col + 4 * q;
+      for (int s = 0; s < frags; ++s) r[s] = *reinterpret_cast<const f32x4 *>(e + 16 * s);
+    };
+    auto prod = [](const f32x4 &x, const f32x4 &y, f32x4 c) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c = Mma<float>::mma(x[k], y[k], c);
+      return c;
+    };
+    const int64_t ys = (int64_t)a.Hv * V;
+    const double end = gam[nt - 1];
+    f32x4 pt[4];  // this wave's tokens i (rows), all j before the block's end
+    if (16 * wave < nt) {
+      f32x4 cf[KF], bf[KF], df[VF], xf[VF];
+      rows(cf, a.c, a.cs, hq * K, wave, KF);
+      rows(df, a.dy, ys, h * V, wave, VF);
+#pragma unroll 1
+      for (int jb = 0; jb <= wave; ++jb) {
+        rows(bf, a.b, a.bs, hq * K, jb, KF);
+        rows(xf, a.x, a.xs, h * V, jb, VF);
+        f32x4 g = zero4(), m = zero4();
+#pragma unroll
+        for (int s = 0; s < KF; ++s) g = prod(cf[s], bf[s], g);
+#pragma unroll
+        for (int s = 0; s < VF; ++s) m = prod(df[s], xf[s], m);
+        const int j = 16 * jb + l16;
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * wave + 4 * q + e;
+          const bool in = j < i && i < nt;
+          const float decay = expf(in ? (float)(gam[i] - gam[j]) : 0.f);
+          v[e] = in ? decay * g[e] * (m[e] * del[j]) : 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) pt[b] = b == jb ? v : pt[b];
+      }
+      // (bf, xf: of the wave's own tokens)
+      float sa = 0.f, sb = 0.f;
+#pragma unroll
+      for (int k = 0; k < KF; ++k) {
+        f32x4 u = zero4(), v = zero4();  // rows 16 k + 4 q .. of S0 dy^T and Z1 x^T, columns the tokens
+        const int at = (16 * k + l16) * P + 4 * q;
+#pragma unroll
+        for (int s = 0; s < VF; ++s) {
+          u = prod(*reinterpret_cast<const f32x4 *>(s0 + at + 16 * s), df[s], u);
+          v = prod(*reinterpret_cast<const f32x4 *>(z1 + at + 16 * s), xf[s], v);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sa += cf[k][e] * u[e];
+          sb += bf[k][e] * v[e];
+        }
+      }
+      sa += __shfl_xor(sa, 16);
+      sb += __shfl_xor(sb, 16);
+      sa += __shfl_xor(sa, 32);
+      sb += __shfl_xor(sb, 32);
+      const int tok = 16 * wave + l16;
+      if (q == 0 && tok < nt) {
+        own[0][tok] = sa * expf((float)gam[tok]);
+        own[1][tok] = sb * (del[tok] * expf((float)(end - gam[tok])));
+      }
+    }
+    double sz = 0.;
+    if (wave == 0)
+      for (int i = lane; i < K * V; i += 64) {
+        const int at = i / V * P + i % V;
+        sz += (double)s0[at] * z1[at];
+      }
+    __syncthreads();
+    float *const tri = mats;  // [i][j], j < i
+    if (16 * wave < nt) {
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb)
+        if (jb <= wave)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tri[(16 * wave + 4 * q + e) * WP + 16 * jb + l16] = pt[jb][e];
+    }
+    __syncthreads();
+    // the pairs j < t <= i: a lane sums its row i up to t, the lanes from t on are added.
+    // (Rows i < t, and with them what no wave wrote, stay out.)
+    if (16 * wave < nt) {
+      float row = 0.f;
+      for (int j = 0; j < 16 * wave; ++j) row += tri[lane * WP + j];
+      for (int t = 16 * wave; t < 16 * wave + 16 && t < nt; ++t) {
+        const float v = wave_sum(lane >= t && lane < nt ? row : 0.f);
+        if (lane == 0) pairs[t] = v;
+        row += tri[lane * WP + t];
+      }
+    }
+    __syncthreads();
+    if (wave) continue;
+    // lane 0 the last token
+    const bool on = lane < nt;
+    const int tok = on ? nt - 1 - lane : 0;
+    const int64_t t = loc.t0 + tok, i = (int64_t)h * a.s.tokens + t;
+    const float z = dt_at(tok);
+    const double rv = on ? w.r_part(a)[i] : 0.f, mv = on ? w.m_part(a)[i] : 0.f;
+    const double dg = wave_sum64(sz) * expf((float)end) + sum_upto(on ? own[0][tok] : 0.f, lane) +
+                      sum_before(on ? own[1][tok] : 0.f, lane) + pairs[tok];
     double dd = rv + mv + A * dg;
     if (a.softplus) dd *= 1.f / (1.f + expf(-z));
-    if (on) {
-      static_cast<E *>(a.ddt)[t * a.Hv + h] = from_f32<E>((float)dd);
-      dA += delta * dg;
-      dbias += dd;
+    if (on) static_cast<float *>(a.ddt)[t * a.Hv + h] = (float)dd;
+    const double dA = wave_sum64(on ? del[tok] * dg : 0.), dbias = wave_sum64(on ? dd : 0.);
+    if (lane == 0) {
+      part[0] = (float)dA;
+      part[1] = (float)dbias;
+      part[2] = w.dd_part(a)[unit];
     }
-  }
-  dA = wave_sum64(dA);
-  dbias = wave_sum64(dbias);
-  if (lane == 0) {
-    float dD = 0.f;
-    for (int s = 0; s < vslices; ++s) dD += w.dd_part(a)[((int64_t)s * a.slots + slot) * a.Hv + h];
-    part[0] = (float)dA;
-    part[1] = (float)dbias;
-    part[2] = dD;
   }
 }
 
@@ -362,6 +460,17 @@ hipError_t sweep(const char *name, const ScanArgs &a, const Layout &w, const Swe
   return hipGetLastError();
 }
 
+void gates(const ScanArgs &a, const Layout &w, hipStream_t st) {
+  // (a launch has fewer than 2^32 threads; a workgroup takes more units beyond that)
+  const unsigned blocks = (unsigned)(a.slots * a.Hv < (1 << 22) ? a.slots * a.Hv : 1 << 22);
+  switch (a.K * 1000 + a.V) {
+    case 32032: gates_kernel<32, 32><<<blocks, 256, 0, st>>>(a, w); break;
+    case 32064: gates_kernel<32, 64><<<blocks, 256, 0, st>>>(a, w); break;
+    case 64032: gates_kernel<64, 32><<<blocks, 256, 0, st>>>(a, w); break;
+    default: gates_kernel<64, 64><<<blocks, 256, 0, st>>>(a, w);
+  }
+}
+
 unsigned carry_blocks(const ScanArgs &a) {
   return (unsigned)(((int64_t)a.s.N * a.Hv * a.K * a.V / 4 + 255) / 256);
 }
@@ -375,7 +484,7 @@ hipError_t fwd(const ScanArgs &a, hipStream_t st) {
     e = sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return sweep<E, kOut>("scan_out", a, w, out, a.K, st);
@@ -387,7 +496,7 @@ hipError_t fwd_mma(const ScanArgs &a, hipStream_t st) {
     hipError_t e = launch_mma_local(a, w, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return launch_mma_out(a, w, st);
@@ -399,7 +508,7 @@ hipError_t bwd_mma(const ScanArgs &a, hipStream_t st) {
   if (!a.one_seg) {
     if ((e = launch_mma_locals(a, w, st)) != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, nullptr, carry_blocks(a));
+    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if ((e = launch_mma_states(a, w, st)) != hipSuccess) return e;
@@ -421,7 +530,7 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
   GDN_DO((sweep<E, kRLocal>("scan_rlocal", a, w, dx, a.K, st)));
   {
     KernelTimer kt("scan_carry", st);
-    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, w.hend(a), carry_blocks(a));
+    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
     GDN_DO(hipGetLastError());
   }
   GDN_DO((sweep<E, kDc>("scan_dc", a, w, dc, a.V, st)));
@@ -429,7 +538,7 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
   GDN_DO((sweep<E, kDb>("scan_db", a, w, db, a.V, st)));
   {
     KernelTimer kt("scan_gates", st);
-    gates_kernel<E><<<(unsigned)(a.slots * a.Hv), 64, 0, st>>>(a, w, (a.K + 63) / 64, (a.V + 63) / 64);
+    gates(a, w, st);
     heads_kernel<<<a.Hv, 64, 0, st>>>(a, w);
     GDN_DO(hipGetLastError());
   }
@@ -450,9 +559,7 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 // without work, then as many as give each two workgroups of the matrix
 // kernels (bf16, whole chunks of 64) or eight waves of the sweeps (fp32, which walk
 // token by token: down to 16 tokens).  fp32 backward: 64 tokens at the most,
-// because the chain of dg gathers the rounding of every a_t and r_t since the
-// segment's end: over 256 tokens the sums over a head (ddt_bias) were off by
-// 4e-5 of their value.
+// what a workgroup of the gates' kernel has.
 ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   ScanArgs a = a0;
   // workgroups a segment

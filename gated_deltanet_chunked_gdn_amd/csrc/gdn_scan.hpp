@@ -30,10 +30,9 @@ struct SlotLoc {
 
 // Byte offsets of the workspace's pieces (each at a 256-byte boundary).
 struct Layout {
-  size_t o_start = 0, o_decay = 0, o_zend = 0, o_hend = 0, o_a = 0, o_r = 0, o_ri = 0, o_half = 0, o_quarter = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
+  size_t o_start = 0, o_decay = 0, o_zend = 0, o_a = 0, o_r = 0, o_ri = 0, o_half = 0, o_quarter = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
          o_dc = 0, o_db = 0, o_ai = 0, o_shi = 0, o_slo = 0, o_z = 0, total = 0;
   int64_t chunks = 0;      // slots of 64-token chunks (bf16 backward)
-  bool need_last = false;  // the local pass runs a sequence's last segment too
   __host__ __device__ float *at(const ScanArgs &a, size_t o) const { return reinterpret_cast<float *>(a.ws + o); }
   __host__ __device__ bf16 *bat(const ScanArgs &a, size_t o) const { return reinterpret_cast<bf16 *>(a.ws + o); }
   // fp32 [slots][Hv][K][V]: a segment's state from zero, then its start state
@@ -43,9 +42,7 @@ struct Layout {
   // [slots][Hv][K][V]: the gradient of a segment's first state from its own
   // tokens, then of its last state from what follows
   __host__ __device__ float *zend(const ScanArgs &a) const { return at(a, o_zend); }
-  // [N][Hv][K][V]: a sequence's last state (fp32 problems)
-  __host__ __device__ float *hend(const ScanArgs &a) const { return at(a, o_hend); }
-  // [slices][Hv][tokens] each: parts of a_t, r_t and m_t
+  // [slices][Hv][tokens] each: parts of a_t (bf16), r_t and m_t
   __host__ __device__ float *a_part(const ScanArgs &a) const { return at(a, o_a); }
   __host__ __device__ float *r_part(const ScanArgs &a) const { return at(a, o_r); }
   __host__ __device__ float *m_part(const ScanArgs &a) const { return at(a, o_m); }
@@ -96,8 +93,6 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
   }
   if (bwd && !a.one_seg) w.o_zend = piece(heads * kv * 4);
   if (bwd && a.dtype != 1) {
-    w.o_hend = piece((size_t)a.s.N * a.Hv * kv * 4);
-    w.o_a = piece(tok * ((a.K + 63) / 64) * 4);
     w.o_r = piece(tok * ((a.V + 63) / 64) * 4);
     w.o_m = piece(tok * ((a.V + 63) / 64) * 4);
     w.o_dd = piece(heads * ((a.V + 63) / 64) * 4);
@@ -123,8 +118,6 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_slo = piece(ch * kv * 2);
     w.o_z = piece(ch * kv * 2);
   }
-  // fp32: the chain of dg starts from the sequence's last state
-  w.need_last = bwd && a.dtype != 1;
   w.total = off ? off : 256;
   return w;
 }
@@ -142,13 +135,10 @@ hipError_t launch_mma_locals(const ScanArgs &a, const Layout &w, hipStream_t st)
 // bf16, gdn_scan_bwd.hip
 hipError_t launch_mma_grad(const ScanArgs &a, const Layout &w, hipStream_t st);
 
-// The chain of dg over 64 tokens, lane 0 the last: sums from lane 0 on of
-// `val` (a - delta r) onto `next` (<S, Z> of the state behind them).
-//
-// dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 to fp32 where the token forgets all
-// (`cut`), and the chain begins again there: delta_t r_t, large where delta_t
-// is, leaves no rounding behind.  The terms cancel among each other, and again
-// against r and m in the sums over all tokens: the chain is held in 64 bits.
+// The chain of dg over 64 tokens (bf16), lane 0 the last: sums from lane 0 on
+// of `val` onto `next` (<S, Z> of the state behind them), begun again where a
+// token forgets all (`cut`): dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 there.  In 64
+// bits, since dg cancels against r and m in the sums over all tokens.
 __device__ __forceinline__ double dg_chain(double val, int cut, double next, int lane) {
   double dg = cut ? 0.0 : val;
 #pragma unroll
@@ -161,6 +151,26 @@ __device__ __forceinline__ double dg_chain(double val, int cut, double next, int
     }
   }
   return cut ? dg : dg + next;
+}
+// Lane 0 the last token: the sum of v from a lane's token on, and over the
+// tokens before it.
+__device__ __forceinline__ double sum_upto(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ double sum_before(double v, int lane) {
+  v = __shfl_down(v, 1);
+  if (lane == 63) v = 0.;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_down(v, d);
+    if (lane + d < 64) v += o;
+  }
+  return v;
 }
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll

@@ -600,17 +600,6 @@ __device__ __forceinline__ double outer_sum(double v, int tok, int lane, int wid
   }
   return v;
 }
-// The sum of v over the tokens before a lane's (no cut either).
-__device__ __forceinline__ double sum_before(double v, int lane) {
-  v = __shfl_down(v, 1);
-  if (lane == 63) v = 0.;
-  for (int d = 1; d < 64; d <<= 1) {
-    const double more = __shfl_down(v, d);
-    if (lane + d < 64) v += more;
-  }
-  return v;
-}
-
 // The gates of one chunk and head: dg from the chunk's <S, Z> and its a, r, z,
 // then ddt and the chunk's parts of dA, ddt_bias, dD.  Lanes are tokens, lane
 // 0 the last.

@@ -58,7 +58,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
   const int blk = (int)(item % blocks_per_group), hq = (int)(item / blocks_per_group % a.Hq);
   const int64_t slot = item / blocks_per_group / a.Hq;
   const SlotLoc loc = locate(a, slot);
-  if (!loc.used || (MODE == kLocal && loc.last && !w.need_last)) return;
+  if (!loc.used || (MODE == kLocal && loc.last)) return;
   const int slice = blk * NW + wave;  // of the group's columns
   const int h = hq * (a.Hv / a.Hq) + slice * VW / V, v0 = slice * VW % V;
   const int64_t kv = (int64_t)K * V;

@@ -1,0 +1,144 @@
+"""GPU parity of the sequence-mixer operators on the paths that larger problems
+take, at sizes whose 64-bit value is still quick: segments of several chunks,
+sequences of one segment, every decay regime in both types, masked tokens,
+padded batches, rows at odd addresses and distances.
+
+The 64-bit form of the scan runs over all sequences at once on the GPU (one
+elementwise step a token).  Tolerances as in test_gpu_mixer.py."""
+import pytest
+import torch
+
+from tests.mixer_ref import DT, delta_of, near, near_sum
+from tests.gpu_util import announce
+from tests.test_gpu_mixer import F32, SCAN, SCAN_OUT, cu_of, gdn, gen, randn  # noqa: F401  (gdn: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(lens, B, T):
+    """Tokens of every sequence side by side: places [N, longest] in the batch's rows, and which of them are there."""
+    lens = torch.tensor(lens if lens is not None else [T] * B)
+    first = torch.cumsum(lens, 0) - lens
+    at = torch.arange(max(int(lens.max()), 1))
+    live = at < lens[:, None]
+    return torch.where(live, first[:, None] + at, 0).cuda(), live.cuda()
+
+
+def scan64(lens, c, b, x, dt, A, D, bias, h0, softplus):
+    """tests.mixer_ref.scan for all sequences at once; A, D, bias [B, T, Hv] or None.  (A token that is not there
+    leaves the state as it is.)"""
+    B, T, Hv, V = x.shape
+    K = c.shape[3]
+    at, live = rows_of(lens, B, T)
+    of = torch.arange(Hv, device="cuda") // (Hv // c.shape[2])
+    pick = lambda t: t.reshape(B * T, *t.shape[2:])[at]  # noqa: E731
+    delta = pick(delta_of(dt, bias, softplus)) * live[..., None]
+    g = delta * pick(A)
+    c, b, xs = pick(c)[:, :, of], pick(b)[:, :, of], pick(x)
+    S = torch.zeros(len(at), Hv, K, V, dtype=torch.float64, device="cuda") if h0 is None else h0
+    ys = []
+    for t in range(at.shape[1]):
+        S = torch.exp(g[:, t])[..., None, None] * S + (delta[:, t, :, None] * b[:, t])[..., None] * xs[:, t, :, None]
+        ys.append((S * c[:, t][..., None]).sum(2))
+    y = torch.stack(ys, 1)
+    y = y if D is None else y + pick(D)[..., None] * xs
+    return y[live].reshape(B, T, Hv, V), S
+
+
+def d64(t):
+    return None if t is None else t.detach().double()
+
+
+def near_dA(got, terms, decays):
+    """near_sum of dA's terms delta_t dg_t, dg_t = e^{g_t} <S_{t-1}, Z_t>.  A decay e^{g_t} below 2^-126 is below the
+    normal numbers of fp32, where an exponential may give 0: such a term may be missing, which is off by the term."""
+    lost = terms.abs() * (decays < 2.0 ** -126)
+    off, most = (d64(got) - terms.sum((0, 1))).abs(), F32 * terms.abs().sum((0, 1)) + lost.sum((0, 1))
+    assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
+
+
+def check_scan(gdn, dtype, lens, c, b, x, dt, A, D, bias, h0, dy, dht, softplus):  # noqa: F811
+    """Both directions against 64 bits."""
+    heads = x.shape[:3]
+    leaves = [d64(t) for t in (c, b, x, dt, A, D, bias, h0)]
+    leaves = [t.expand(heads).clone() if t is not None and i in (4, 5, 6) else t for i, t in enumerate(leaves)]
+    leaves = [None if t is None else t.requires_grad_() for t in leaves]
+    ry, rht = scan64(lens, *leaves, softplus)
+    kw = dict(D=D, dt_bias=bias, dt_softplus=softplus, initial_state=h0, cu_seqlens=cu_of(lens))
+    y, ht = gdn.selective_scan_fwd(c, b, x, dt, A, **kw)
+    near("y", y, ry, SCAN[dtype])
+    near("ht", ht, rht, F32)
+    value = (ry * d64(dy)).sum() if dht is None else (ry * d64(dy)).sum() + (rht * d64(dht)).sum()
+    want = iter(torch.autograd.grad(value, [t for t in leaves if t is not None]))
+    want = [None if t is None else next(want) for t in leaves]
+    got = gdn.selective_scan_bwd(c, b, x, dt, A, dy, dht=dht, **kw)
+    for n, a, r in zip(SCAN_OUT, got, want):
+        if n == "dA":
+            near_dA(a, r, torch.exp(delta_of(d64(dt), d64(bias), softplus) * d64(A)))
+        elif n in ("dD", "ddt_bias"):
+            near_sum(n, a, r if r is None else r.cpu(), F32)
+        else:
+            near(n, a, r, F32 if n == "dh0" else SCAN[dtype])
+
+
+def inputs(dtype, B, T, Hq, Hv, K, V, lens=None, state=True, seed=1):
+    g, dt = gen(seed), DT[dtype]
+    T = sum(lens) if lens is not None else T
+    N = len(lens) if lens is not None else B
+    c, b, x = randn(g, B, T, Hq, K, dt=dt), randn(g, B, T, Hq, K, dt=dt), randn(g, B, T, Hv, V, dt=dt)
+    A = -(0.5 + 8 * torch.rand(Hv, generator=g)).cuda()
+    D, bias = randn(g, Hv), randn(g, Hv, s=0.5) - 3
+    dtv = randn(g, B, T, Hv, s=0.7, dt=dt)
+    h0, dht = (randn(g, N, Hv, K, V, s=0.3), randn(g, N, Hv, K, V, s=0.3)) if state else (None, None)
+    return dict(c=c, b=b, x=x, dt=dtv, A=A, D=D, bias=bias, h0=h0, dy=randn(g, B, T, Hv, V, dt=dt), dht=dht, softplus=True)
+
+
+def segment(gdn, dtype, B, T, Hq, Hv, K, V, lens, bwd):  # noqa: F811
+    """Tokens of a segment by the planner's rule, held against the workspace that the forward asks for."""
+    T = sum(lens) if lens is not None else T
+    N = len(lens) if lens is not None else B
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    if dtype == "bf16":
+        slices = Hv // Hq * (V // 32)
+        each = next(n for n in (8, 4, 2, 1) if slices % n == 0)
+        want, unit = -(-cus // (Hq * (slices // each))), 64
+    else:
+        want, unit = -(-cus * 8 // (Hv * -(-V // 64))), 16
+    seg = max(unit, -(-(-(-B * T // max(want, N))) // unit) * unit)
+    slots = B * T // seg + N if lens is not None else N * -(-T // seg)
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    ws = 256 if T <= seg else up(slots * Hv * K * V * 4) + up(slots * Hv * 4)
+    cu = 16 if lens is not None else None
+    p = gdn.mixer.ScanProblem(B, T, Hq, Hv, K, V, N, int(dtype == "bf16"), 1, 0, 0, 0, cu, None)
+    import ctypes
+    assert gdn.mixer.lib().gdn_selective_scan_fwd_workspace_size(ctypes.byref(p)) == ws
+    return min(seg, 64) if bwd and dtype == "f32" else seg
+
+
+# The fp32 backward's segments are 64 tokens at the most.
+STEPS = [1e-4, 0.3, 2.0, 9.0, 18.0, 25.0, 40.0, 120.0, "mixed", "mostly mild"]
+
+
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("K,V", [(32, 32), (64, 64), (64, 32)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scan_decay_regimes_of_long_segments(gdn, dtype, K, V, state):  # noqa: F811
+    """Log decays a token from nothing to all, a regime a head, in segments of 64 tokens and a short one."""
+    Hv, B, T = 40, 52, 70
+    announce(f"scan regimes {dtype} {K} {V} state={state}")
+    assert dtype == "bf16" or segment(gdn, dtype, B, T, 1, Hv, K, V, None, True) == 64
+    i = inputs(dtype, B, T, 1, Hv, K, V, state=state, seed=17)
+    g = gen(18)
+    step = torch.empty(B, T, Hv)
+    for h in range(Hv):
+        s = STEPS[h % len(STEPS)]
+        if s == "mixed":
+            step[..., h] = torch.tensor([1e-4, 0.3, 2.0, 9.0, 18.0, 40.0, 200.0])[torch.randint(0, 7, (B, T), generator=g)]
+        elif s == "mostly mild":
+            step[..., h] = torch.tensor([0.001, 0.01, 0.3, 19.0])[torch.randint(0, 4, (B, T), generator=g)]
+        else:
+            step[..., h] = s * (0.8 + 0.4 * torch.rand(B, T, generator=g))
+    i["A"] = -torch.tensor([1.0, 0.5])[torch.arange(Hv) % 2].cuda()
+    i["dt"] = (step / torch.tensor([1.0, 0.5])[torch.arange(Hv) % 2]).to(DT[dtype]).cuda()
+    i["bias"], i["softplus"] = None, False
+    check_scan(gdn, dtype, None, **i)
