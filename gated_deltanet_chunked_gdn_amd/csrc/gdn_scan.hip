@@ -428,7 +428,8 @@ __global__ __launch_bounds__(64) void heads_kernel(ScanArgs a, Layout w) {
   }
 }
 
-// dc, db: the sum over the heads of a group, 4 elements a thread.
+// dc, db: the sum over the heads of a group, 4 elements a thread.  (Tokens that
+// no sequence has have no parts, and their rows are not the kernel's.)
 template <typename E>
 __global__ __launch_bounds__(256) void group_kernel(ScanArgs a, Layout w) {
   const int64_t k4 = a.K / 4, n = a.s.tokens * a.Hq * k4;
@@ -436,6 +437,11 @@ __global__ __launch_bounds__(256) void group_kernel(ScanArgs a, Layout w) {
   if (i >= n) return;
   const int R = a.Hv / a.Hq;
   const int64_t e = i % k4, th = i / k4;  // th = token * Hq + hq
+  if (a.s.cu) {
+    const int64_t t = th / a.Hq;
+    const Span sp = seq_span(a.s, seq_of(a.s, t));
+    if (t < sp.first || t >= sp.end) return;
+  }
   const f32x4 *pc = reinterpret_cast<const f32x4 *>(w.dc_part(a)) + th * R * k4 + e;
   const f32x4 *pb = reinterpret_cast<const f32x4 *>(w.db_part(a)) + th * R * k4 + e;
   f32x4 c = zero4(), b = zero4();

@@ -10,7 +10,9 @@ points: torch supplies outputs, workspace and the current stream of the
 inputs' device; nothing here computes.  Tensors are [B, T, ...]; a packed batch
 has B = 1 and cu_seqlens (int32 [N + 1]).  With check_cu_seqlens=False a device
 cu_seqlens is not copied to the host for checking, so the call does not wait
-for the device and can be captured into a graph.
+for the device and can be captured into a graph; its last entry may then be
+below T, and the rows of the outputs past it are not written (they hold what
+torch.empty left).
 """
 from __future__ import annotations
 

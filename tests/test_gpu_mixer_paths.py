@@ -142,3 +142,124 @@ def test_scan_decay_regimes_of_long_segments(gdn, dtype, K, V, state):  # noqa: 
     i["dt"] = (step / torch.tensor([1.0, 0.5])[torch.arange(Hv) % 2]).to(DT[dtype]).cuda()
     i["bias"], i["softplus"] = None, False
     check_scan(gdn, dtype, None, **i)
+
+
+# ---------------------------------------------------------------- buffers of the C entries
+
+
+class Buffers:
+    """Outputs and workspace of a C entry, each the middle of a wider buffer
+    whose ends hold a pattern, and the entry's inputs, which stay as they are.
+    Outputs start as 7, the workspace as NaN."""
+
+    BAND = 4096  # bytes
+
+    def __init__(self, inputs):  # noqa: F811
+        self.inputs = [(t, t.clone()) for t in inputs if t is not None]
+        self.bands = []
+
+    def bytes(self, n, fill):
+        whole = torch.full((n + 2 * self.BAND,), 0xA5, dtype=torch.uint8, device="cuda")
+        whole[self.BAND:self.BAND + n] = fill
+        self.bands.append((whole, n))
+        return whole[self.BAND:self.BAND + n]
+
+    def new(self, shape, dt):
+        n = torch.Size(shape).numel()
+        return self.bytes(n * dt.itemsize, 0).view(dt).view(shape).fill_(7)
+
+    def like(self, t):
+        return None if t is None else self.new(t.shape, t.dtype)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for whole, n in self.bands:
+            assert bool((whole[:self.BAND] == 0xA5).all()) and bool((whole[self.BAND + n:] == 0xA5).all())
+        for t, was in self.inputs:
+            assert torch.equal(t.reshape(-1).view(torch.uint8), was.reshape(-1).view(torch.uint8))
+
+
+def raw_call(f, *args):
+    import ctypes
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else ctypes.byref(a) if isinstance(a, ctypes.Structure) else a
+            for a in args]
+    assert f(*args, torch.cuda.current_stream().cuda_stream) == 0
+
+
+def raw_conv(gdn, x, w, b, h0, dy, dht, cu):  # noqa: F811
+    """(y, ht), (dx, dw, db, dh0) of the C entries, cu on the device, unchecked."""
+    import ctypes
+    m, N = gdn.mixer, cu.numel() - 1
+    p = m.ConvProblem(1, x.shape[1], x.shape[2], w.shape[1], N, int(x.dtype == torch.bfloat16), int(w.dtype == torch.bfloat16),
+                      1, 0, cu.data_ptr(), None)
+    o = Buffers((x, w, b, h0, dy, dht, cu))
+    y, ht = o.like(x), o.new((N, w.shape[1] - 1, x.shape[2]), x.dtype)
+    raw_call(m.lib().gdn_causal_conv_fwd, p, x, w, b, h0, y, ht)
+    grads = [o.like(t) for t in (x, w, b, h0)]
+    n = m.lib().gdn_causal_conv_bwd_workspace_size(ctypes.byref(p))
+    raw_call(m.lib().gdn_causal_conv_bwd, p, x, w, b, dy, h0, dht, *grads, o.bytes(n, 0xFF), n)
+    o.check()
+    return (y, ht), grads
+
+
+def raw_scan(gdn, i, cu):  # noqa: F811
+    """(y, ht), (dc, db, dx, ddt, dA, dD, ddt_bias, dh0) likewise."""
+    import ctypes
+    m, N, x, c = gdn.mixer, cu.numel() - 1, i["x"], i["c"]
+    p = m.ScanProblem(1, x.shape[1], c.shape[2], x.shape[2], c.shape[3], x.shape[3], N, int(x.dtype == torch.bfloat16),
+                      int(i["softplus"]), 0, 0, 0, cu.data_ptr(), None)
+    ins = [i[k] for k in ("c", "b", "x", "dt", "A", "D", "bias", "h0")]
+    o = Buffers(ins + [i["dy"], i["dht"], cu])
+    y, ht = o.like(x), o.new((N, x.shape[2], c.shape[3], x.shape[3]), torch.float32)
+    n = m.lib().gdn_selective_scan_fwd_workspace_size(ctypes.byref(p))
+    raw_call(m.lib().gdn_selective_scan_fwd, p, *ins, y, ht, o.bytes(n, 0xFF), n)
+    grads = [o.like(t) for t in ins]
+    n = m.lib().gdn_selective_scan_bwd_workspace_size(ctypes.byref(p))
+    raw_call(m.lib().gdn_selective_scan_bwd, p, *ins, i["dy"], i["dht"], *grads, o.bytes(n, 0xFF), n)
+    o.check()
+    return (y, ht), grads
+
+
+# tokens of the sequences, rows behind them
+PADDED = [([30, 0, 30], 40), ([70, 1, 64], 1), ([200], 100), ([5], 3), ([0, 0], 20)]
+
+
+@pytest.mark.parametrize("lens,pad", PADDED)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_behind_the_last_sequence_stay(gdn, dtype, lens, pad):  # noqa: F811
+    """They hold NaN, no result sees them, and nothing is written to theirs."""
+    announce(f"padded {dtype} {lens} {pad}")
+    T, cu = sum(lens), cu_of(lens).cuda()
+
+    def padded(t):
+        return torch.cat([t, torch.full((1, pad, *t.shape[2:]), float("nan"), dtype=t.dtype, device="cuda")], 1)
+
+    def rows(got, T):
+        assert bool((got[:, T:] == 7).all())
+        return got[:, :T]
+
+    g, dt = gen(41), DT[dtype]
+    x, w, b, dy = randn(g, 1, T, 40, dt=dt), randn(g, 40, 4, dt=dt), randn(g, 40, dt=dt), randn(g, 1, T, 40, dt=dt)
+    h0, dht = randn(g, len(lens), 3, 40, dt=dt), randn(g, len(lens), 3, 40, dt=dt)
+    (y, ht), (dx, dw, db, dh0) = raw_conv(gdn, padded(x), w, b, h0, padded(dy), dht, cu)
+    ry, rht = gdn.causal_conv_fwd(x, w, b, initial_state=h0, cu_seqlens=cu)
+    want = gdn.causal_conv_bwd(x, w, b, dy, initial_state=h0, dfinal_state=dht, cu_seqlens=cu)
+    assert torch.equal(rows(y, T), ry) and torch.equal(ht, rht) and torch.equal(rows(dx, T), want[0]) and torch.equal(dh0, want[3])
+    near("dw", dw, want[1], SCAN[dtype])
+    near("db", db, want[2], SCAN[dtype])
+
+    i = inputs(dtype, 1, 0, 2, 4, 64, 32, lens=lens, seed=42)
+    j = {k: padded(t) if k in ("c", "b", "x", "dt", "dy") else t for k, t in i.items()}
+    (y, ht), got = raw_scan(gdn, j, cu)
+    kw = dict(D=i["D"], dt_bias=i["bias"], initial_state=i["h0"], cu_seqlens=cu)
+    ins = [i[k] for k in ("c", "b", "x", "dt", "A")]
+    ry, rht = gdn.selective_scan_fwd(*ins, **kw)
+    near("y", rows(y, T), ry, SCAN[dtype])
+    near("ht", ht, rht, 2 * F32)  # (two results, each with its own segments)
+    want = gdn.selective_scan_bwd(*ins, i["dy"], dht=i["dht"], **kw)
+    for n, a, r in zip(SCAN_OUT, got, want):
+        a = rows(a, T) if a.dim() > 2 and n != "dh0" else a
+        if n in ("dA", "dD", "ddt_bias"):
+            assert bool(torch.isfinite(a).all())
+        else:
+            near(n, a, r, 2 * F32 if n == "dh0" else 2 * SCAN[dtype])
