@@ -70,7 +70,8 @@ int check_conv(const gdn_conv_t *p, gdn::ConvArgs *a) {
   const int rc = check_seqs(p->B, p->T, p->N, p->cu_seqlens, p->cu_seqlens_host);
   if (rc != GDN_OK) return rc;
   const int64_t tokens = (int64_t)p->B * p->T;
-  if (tokens >= kGrid || ((tokens + 7) / 8 + p->N) * (((int64_t)p->D + 31) / 32) >= kGrid)
+  // (channel indices are 32-bit, the last workgroup's among them: up to 1024 channels each)
+  if (p->D > INT32_MAX - 1023 || tokens >= kGrid || ((tokens + 7) / 8 + p->N) * (((int64_t)p->D + 31) / 32) >= kGrid)
     return set_error(GDN_ERR_UNSUPPORTED, "problem too large for the launch grid");
   *a = gdn::ConvArgs{};
   a->s = gdn::Seqs{p->cu_seqlens, p->cu_seqlens ? p->N : p->B, p->T, tokens};
@@ -83,6 +84,14 @@ int check_conv(const gdn_conv_t *p, gdn::ConvArgs *a) {
   return GDN_OK;
 }
 
+// The sums over the tokens' parts take 16 threads a column
+// (and a launch has fewer than 2^32 threads)
+int check_conv_bwd(const gdn_conv_t *p, gdn::ConvArgs *a) {
+  const int rc = check_conv(p, a);
+  if (rc == GDN_OK && (int64_t)(p->W + 1) * p->D >= ((int64_t)1 << 28))
+    return set_error(GDN_ERR_UNSUPPORTED, "problem too large for the launch grid");
+  return rc;
+}
 size_t conv_bwd_bytes(const gdn::ConvArgs &a) {
   const size_t n = (size_t)gdn::conv_bwd_tiles(a.s.tokens, a.D) * (a.W + 1) * a.D * 4;
   return n ? n : 256;
@@ -187,7 +196,7 @@ int gdn_causal_conv_fwd(const gdn_conv_t *p, const void *x, const void *weight, 
 size_t gdn_causal_conv_bwd_workspace_size(const gdn_conv_t *p) {
   gdn::clear_error();
   gdn::ConvArgs a;
-  return check_conv(p, &a) == GDN_OK ? conv_bwd_bytes(a) : 0;
+  return check_conv_bwd(p, &a) == GDN_OK ? conv_bwd_bytes(a) : 0;
 }
 
 int gdn_causal_conv_bwd(const gdn_conv_t *p, const void *x, const void *weight, const void *bias, const void *dy,
@@ -195,7 +204,7 @@ int gdn_causal_conv_bwd(const gdn_conv_t *p, const void *x, const void *weight, 
                         void *workspace, size_t ws_bytes, void *stream) {
   gdn::clear_error();
   gdn::ConvArgs a;
-  int rc = check_conv(p, &a);
+  int rc = check_conv_bwd(p, &a);
   if (rc != GDN_OK) return rc;
   if (!weight || !dweight || (a.s.tokens > 0 && (!x || !dy || !dx)))
     return set_error(GDN_ERR_INVALID_ARG, "x, weight, dy, dx and dweight are required");

@@ -230,3 +230,17 @@ def test_sizes_beyond_32_bits_are_refused():
             lambda: gdn.layer_norm_fwd(wide(1, n))):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_channels_whose_workgroups_end_past_32_bits_are_refused():
+    """A channel's index is 32-bit: the last workgroup's, up to 1023 past D, has to fit as well (it would come out
+    negative, in front of every buffer)."""
+    L = mixer.lib()
+    for D in (2 ** 31 - 1, 2 ** 31 - 1023):
+        p = ctypes.byref(conv(D=D, T=1))
+        assert L.gdn_causal_conv_bwd_workspace_size(p) == 0
+        assert L.gdn_causal_conv_fwd(p, P(16), P(16), P(16), None, P(16), None, None) == 2
+        assert L.gdn_causal_conv_bwd(p, *([P(16)] * 4), None, None, *([P(16)] * 3), None, P(256), 1 << 62, None) == 2
+        assert L.gdn_causal_conv_step(p, P(16), P(16), P(16), None, None, 1, P(16), None) == 2
+    assert L.gdn_causal_conv_bwd_workspace_size(ctypes.byref(conv(D=(2 ** 31 - 1) // 8, T=1))) == 0  # its sums' launch
+    assert L.gdn_causal_conv_bwd_workspace_size(ctypes.byref(conv(D=50_000_000, T=1))) > 0
