@@ -124,9 +124,9 @@ int check_scan(const gdn_scan_t *p, bool step, gdn::ScanArgs *a) {
     return set_error(GDN_ERR_INVALID_ARG, "a stride is below its row (c %lld b %lld x %lld)", (long long)cs,
                      (long long)bs, (long long)xs);
   const int64_t per = 16 / (int64_t)elem(p->dtype);
-  // (the kernels address 64 rows by 32-bit byte offsets)
+  // (the scan's kernels address 64 rows by 32-bit byte offsets, the step's one row by itself)
   constexpr int64_t kRow = (int64_t)1 << 24;
-  if (cs >= kRow || bs >= kRow || xs >= kRow)
+  if (!step && (cs >= kRow || bs >= kRow || xs >= kRow))
     return set_error(GDN_ERR_UNSUPPORTED, "c, b and x rows must lie less than 2^24 elements apart");
   if (cs % per || bs % per || xs % per)
     return set_error(GDN_ERR_LAYOUT, "c, b and x strides must be multiples of 16 bytes");

@@ -231,7 +231,7 @@ int gdn_causal_conv_step(const gdn_conv_t *p, const void *x, void *state, const 
  *   initial_state, final_state, dht, dh0 [N, Hv, K, V] fp32
  * K, V in {32, 64, 128} in bf16, {32, 64} in fp32.  c, b, x, y, dy, dx, dc,
  * db and the states are 16-byte aligned, c_stride, b_stride, x_stride
- * multiples of 16 bytes and below 2^24 elements.
+ * multiples of 16 bytes and (but for the step) below 2^24 elements.
  * Held in fp32: delta, the decays, the states, the gates' gradients and every
  * sum over tokens.  In bf16 problems the products inside a 64-token chunk and
  * the state as an operand of y, dc and db are rounded to bf16.  A NaN or an

@@ -263,3 +263,22 @@ def test_rows_behind_the_last_sequence_stay(gdn, dtype, lens, pad):  # noqa: F81
             assert bool(torch.isfinite(a).all())
         else:
             near(n, a, r, 2 * F32 if n == "dh0" else 2 * SCAN[dtype])
+
+
+# ---------------------------------------------------------------- rows as they lie
+
+
+def test_steps_on_a_token_of_a_long_sequence(gdn):  # noqa: F811
+    """q[:, t] of a [B, T, H, K]: rows 2^24 elements and more apart."""
+    g = gen(51)
+    B, T, Hq, Hv, K, V, t = 2, 16390, 8, 16, 128, 64, 16389
+    q, k, v = (torch.zeros(B, T, h, n, dtype=torch.bfloat16, device="cuda") for h, n in ((Hq, K), (Hq, K), (Hv, V)))
+    for x in (q, k, v):
+        x[:, t] = randn(g, B, *x.shape[2:], dt=torch.bfloat16)
+    beta, gate, A = torch.rand(B, Hv, generator=g).bfloat16().cuda(), -torch.rand(B, Hv, generator=g).cuda(), -torch.rand(Hv, generator=g).cuda()
+    st = randn(g, B, Hv, K, V)
+    for f in (lambda q, k, v, s: gdn.gated_delta_rule_step(q, k, v, gate, beta, s, use_qk_l2norm_in_kernel=True),
+              lambda q, k, v, s: gdn.selective_scan_step(q, k, v, beta, A, s)):
+        s1, s2 = st.clone(), st.clone()
+        assert torch.equal(f(q[:, t], k[:, t], v[:, t], s1), f(*(x[:, t].clone() for x in (q, k, v)), s2))
+        assert torch.equal(s1, s2)

@@ -244,3 +244,15 @@ def test_channels_whose_workgroups_end_past_32_bits_are_refused():
         assert L.gdn_causal_conv_step(p, P(16), P(16), P(16), None, None, 1, P(16), None) == 2
     assert L.gdn_causal_conv_bwd_workspace_size(ctypes.byref(conv(D=(2 ** 31 - 1) // 8, T=1))) == 0  # its sums' launch
     assert L.gdn_causal_conv_bwd_workspace_size(ctypes.byref(conv(D=50_000_000, T=1))) > 0
+
+
+def test_a_step_takes_rows_at_any_distance():
+    """x[:, t] of a long [B, T, ...]: the limit of 2^24 elements is the scan's, whose rows are 32-bit byte offsets
+    apart.  (Both calls stop at a missing pointer, past the sizes' checks.)"""
+    L = mixer.lib()
+    far = 1 << 24
+    s = scan(B=3, T=1, N=3, c_stride=far, b_stride=far, x_stride=far)
+    assert L.gdn_selective_scan_step(ctypes.byref(s), None, *([P(16)] * 4), None, None, P(16), None, 3, P(16), None) == 1
+    d = gdn.GdnProblem(3, 1, 2, 4, 32, 64, 3, gdn.GDN_BF16, 1.0, None, None, -1, 0)
+    assert L.gdn_delta_rule_step(ctypes.byref(d), None, *([P(16)] * 4), far, far, far, P(16), None, 3, P(16), None) == 1
+    assert L.gdn_selective_scan_fwd_workspace_size(ctypes.byref(s)) == 0
