@@ -118,15 +118,25 @@ class _Seqs:
         return (None if self.dev is None else self.dev.data_ptr(), None if self.host is None else self.host.data_ptr())
 
 
-def _rows(t, lead: int):
+def _aligned(t):
+    """t, contiguous and at a 16-byte boundary (a copy where it is not)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _rows(t, lead: int, aligned: bool = False, most: int = 1 << 62):
     """(tensor, elements from one row to the next) of t, whose first `lead`
-    dimensions count rows: t itself where its rows lie at one distance and each
-    is contiguous, in whole 16-byte pieces; a contiguous copy elsewhere."""
+    dimensions count rows: t itself where its rows lie at one distance (`most`
+    at the most) and each is contiguous, in whole 16-byte pieces; a contiguous
+    copy elsewhere.  A contiguous tensor is taken at any address unless
+    `aligned`."""
     inner = 1
     for n in t.shape[lead:]:
         inner *= n
     if t.is_contiguous():
-        return t, inner
+        return _aligned(t) if aligned else t, inner
     want, ok = 1, True
     for n, s in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
         ok = ok and (n == 1 or s == want)
@@ -136,7 +146,7 @@ def _rows(t, lead: int):
     if len(dims) == 2:
         ok = ok and dims[0][1] == dims[1][0] * dims[1][1]
     per = 16 // t.element_size()
-    if ok and step >= inner and step % per == 0 and t.data_ptr() % 16 == 0:
+    if ok and inner <= step <= most and step % per == 0 and t.data_ptr() % 16 == 0:
         return t, step
     return t.contiguous(), inner
 
@@ -293,7 +303,8 @@ def _scan_problem(c, b, x, dt, A, D, dt_bias, dt_softplus, lead):
             continue
         if t is None or t.dtype != torch.float32 or tuple(t.shape) != (Hv,):
             raise ValueError(f"{name} must be float32 [{Hv}]")
-    (cr, cs), (br, bs), (xr, xs) = _rows(c, lead), _rows(b, lead), _rows(x, lead)
+    most = (1 << 24) - 1 if lead == 2 else 1 << 62
+    (cr, cs), (br, bs), (xr, xs) = (_rows(t, lead, True, most) for t in (c, b, x))
     p = ScanProblem(x.shape[0], x.shape[1] if lead == 2 else 1, c.shape[lead], Hv, c.shape[lead + 1], x.shape[lead + 1],
                     x.shape[0], _dtype(x, "c, b, x and dt"), int(bool(dt_softplus)), cs, bs, xs, None, None)
     return p, cr, br, xr, dt.contiguous(), A.contiguous(), _contig(D), _contig(dt_bias)
@@ -316,7 +327,7 @@ def selective_scan_fwd(c, b, x, dt, A, D=None, dt_bias=None, dt_softplus: bool =
     dev = x.device
     sq = _Seqs(cu_seqlens, p.B, p.T, dev, check_cu_seqlens)
     shape = (sq.N, p.Hv, p.K, p.V)
-    h0 = _contig(initial_state)
+    h0 = _aligned(initial_state)
     _check_state(h0, "initial_state", shape)
     _check_device(x, c, b, dt, A, D, dt_bias, h0)
     p.N = sq.N
@@ -343,7 +354,7 @@ def selective_scan_bwd(c, b, x, dt, A, dy, dht=None, D=None, dt_bias=None, dt_so
     dev = x.device
     sq = _Seqs(cu_seqlens, p.B, p.T, dev, check_cu_seqlens)
     shape = (sq.N, p.Hv, p.K, p.V)
-    dy, dht, h0 = dy.contiguous(), _contig(dht), _contig(initial_state)
+    dy, dht, h0 = _aligned(dy), _aligned(dht), _aligned(initial_state)
     _check_state(dht, "dht", shape)
     _check_state(h0, "initial_state", shape)
     _check_device(x, c, b, dt, A, D, dt_bias, dy, dht, h0)
@@ -402,7 +413,7 @@ def gated_delta_rule_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_
     dt = _dtype(q, "q, k, v and beta")
     _step_state(state, Hv, K, V)
     idx = _indices(state_indices, B, state)
-    (q, qs), (k, ks), (v, vs) = _rows(q, 1), _rows(k, 1), _rows(v, 1)
+    (q, qs), (k, ks), (v, vs) = (_rows(t, 1, True) for t in (q, k, v))
     g, beta = g.contiguous(), beta.contiguous()
     _check_device(q, k, v, g, beta, state, idx)
     dev = q.device

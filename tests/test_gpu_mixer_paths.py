@@ -282,3 +282,34 @@ def test_steps_on_a_token_of_a_long_sequence(gdn):  # noqa: F811
         s1, s2 = st.clone(), st.clone()
         assert torch.equal(f(q[:, t], k[:, t], v[:, t], s1), f(*(x[:, t].clone() for x in (q, k, v)), s2))
         assert torch.equal(s1, s2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tensors_off_a_16_byte_boundary(gdn, dtype):  # noqa: F811
+    """Contiguous and one element off: the same bits as from a boundary, in every operator."""
+    def off(t):
+        if t is None:
+            return None
+        o = torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+        assert o.is_contiguous() and o.data_ptr() % 16
+        return o
+
+    def same(a, b):
+        for x, y in zip(a, b):
+            assert (x is None and y is None) or torch.equal(x, y)
+
+    i = inputs(dtype, 2, 70, 1, 2, 64, 32, seed=52)
+    o = {k: off(t) if isinstance(t, torch.Tensor) else t for k, t in i.items()}
+    fwd = lambda i: gdn.selective_scan_fwd(i["c"], i["b"], i["x"], i["dt"], i["A"], D=i["D"], dt_bias=i["bias"],  # noqa: E731
+                                           initial_state=i["h0"])
+    bwd = lambda i: gdn.selective_scan_bwd(i["c"], i["b"], i["x"], i["dt"], i["A"], i["dy"], dht=i["dht"], D=i["D"],  # noqa: E731
+                                           dt_bias=i["bias"], initial_state=i["h0"])
+    same(fwd(o), fwd(i))
+    same(bwd(o), bwd(i))
+    one = lambda i: [i[k][:, 0].contiguous() for k in ("c", "b", "x", "dt")]  # noqa: E731
+    s1, s2 = i["h0"].clone(), i["h0"].clone()
+    args = one(i)
+    gate = -args[3].float().abs()
+    same([gdn.selective_scan_step(*map(off, args), off(i["A"]), s1), s1], [gdn.selective_scan_step(*args, i["A"], s2), s2])
+    same([gdn.gated_delta_rule_step(*map(off, args[:3]), off(gate), off(args[3]), s1), s1],
+         [gdn.gated_delta_rule_step(*args[:3], gate, args[3], s2), s2])

@@ -256,3 +256,22 @@ def test_a_step_takes_rows_at_any_distance():
     d = gdn.GdnProblem(3, 1, 2, 4, 32, 64, 3, gdn.GDN_BF16, 1.0, None, None, -1, 0)
     assert L.gdn_delta_rule_step(ctypes.byref(d), None, *([P(16)] * 4), far, far, far, P(16), None, 3, P(16), None) == 1
     assert L.gdn_selective_scan_fwd_workspace_size(ctypes.byref(s)) == 0
+
+
+def test_rows_that_the_kernels_do_not_take_are_copied():
+    """A contiguous tensor off a 16-byte boundary like a strided one there, and tokens too far apart for the scan."""
+    off = torch.arange(2 * 5 * 16 + 1, dtype=torch.float32)[1:].view(2, 5, 16)
+    assert off.is_contiguous() and off.data_ptr() % 16
+    t, s = mixer._rows(off, 2, aligned=True)
+    assert s == 16 and t.data_ptr() % 16 == 0 and torch.equal(t, off)
+    t, s = mixer._rows(off, 2)  # the convolution takes any
+    assert s == 16 and t.data_ptr() == off.data_ptr()
+    far = torch.empty((1 << 24) + 32, dtype=BF)[:1].as_strided((1, 2, 1, 32), (1 << 25, 1 << 24, 32, 1))
+    far[:] = 1
+    t, s = mixer._rows(far, 2, most=(1 << 24) - 1)
+    assert s == 32 and t.is_contiguous()
+    t, s = mixer._rows(far, 2)
+    assert s == 1 << 24 and t.data_ptr() == far.data_ptr()
+    assert mixer._aligned(None) is None and mixer._aligned(off).data_ptr() % 16 == 0
+    even = z(3, 16)
+    assert mixer._aligned(even) is even
