@@ -313,3 +313,150 @@ def test_tensors_off_a_16_byte_boundary(gdn, dtype):  # noqa: F811
     same([gdn.selective_scan_step(*map(off, args), off(i["A"]), s1), s1], [gdn.selective_scan_step(*args, i["A"], s2), s2])
     same([gdn.gated_delta_rule_step(*map(off, args[:3]), off(gate), off(args[3]), s1), s1],
          [gdn.gated_delta_rule_step(*args[:3], gate, args[3], s2), s2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", None])
+def test_convolution_off_a_boundary(gdn, dtype, act):  # noqa: F811
+    """D a multiple of 4, rows off: the form of single channels gives the bits of the wide one's outputs."""
+    g, dt = gen(53), DT[dtype]
+    lens = [40, 0, 1, 90]
+    x, dy = randn(g, 1, sum(lens), 64, dt=dt), randn(g, 1, sum(lens), 64, dt=dt)
+    w, b, h0, dht = randn(g, 64, 4, dt=dt), randn(g, 64, dt=dt), randn(g, 4, 3, 64, dt=dt), randn(g, 4, 3, 64, dt=dt)
+    off = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)  # noqa: E731
+    kw = dict(cu_seqlens=cu_of(lens), activation=act)
+    for a, r in zip(gdn.causal_conv_fwd(off(x), off(w), off(b), initial_state=off(h0), **kw),
+                    gdn.causal_conv_fwd(x, w, b, initial_state=h0, **kw)):
+        assert torch.equal(a, r)
+    got = gdn.causal_conv_bwd(off(x), off(w), off(b), off(dy), initial_state=off(h0), dfinal_state=off(dht), **kw)
+    want = gdn.causal_conv_bwd(x, w, b, dy, initial_state=h0, dfinal_state=dht, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+    for a, r in zip(got[1:3], want[1:3]):  # sums, in another order
+        near("sum", a, r, 2 * SCAN[dtype])
+    s1, s2 = h0.clone(), off(h0)
+    assert torch.equal(gdn.causal_conv_step(x[0, :4], s1, w, b, activation=act),
+                       gdn.causal_conv_step(off(x[0, :4]), s2, off(w), off(b), activation=act)) and torch.equal(s1, s2)
+
+
+# ---------------------------------------------------------------- unchecked cu_seqlens
+
+# (sequences that decrease, run past the batch, overlap, begin late, are negative; 200 tokens)
+BAD = [[0, 500, 3, 10, 190, 7, 90, 200, 100], [-5, 1, 3, 3, 6, 150, 200, 200, 100000], [200, 150, 100, 64, 63, 20, 1, 0, -1],
+       [0, 200, 0, 200, 0, 200, 0, 200, 0], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 5, 9, 8, 7, 2 ** 31 - 1],
+       [100, 100, 100, 120, 120, 130, 131, 140, 150]]
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_bad_cu_seqlens_on_the_device_writes_into_the_outputs_only(gdn, dtype, bad):  # noqa: F811
+    """Results are unspecified; inputs, and what lies beside outputs and workspace, stay as they were."""
+    announce(f"bad cu {dtype} {bad}")
+    cu, N, T = torch.tensor(bad, dtype=torch.int64).to(torch.int32).cuda(), len(bad) - 1, 200
+    g, dt = gen(61), DT[dtype]
+    x, w, b, dy = randn(g, 1, T, 40, dt=dt), randn(g, 40, 4, dt=dt), randn(g, 40, dt=dt), randn(g, 1, T, 40, dt=dt)
+    raw_conv(gdn, x, w, b, randn(g, N, 3, 40, dt=dt), dy, randn(g, N, 3, 40, dt=dt), cu)
+    i = inputs(dtype, 1, 0, 2, 4, 64, 32, lens=[T] + [0] * (N - 1), seed=62)
+    raw_scan(gdn, i, cu)
+    i["h0"] = i["dht"] = None
+    raw_scan(gdn, i, cu)
+
+
+# ---------------------------------------------------------------- segments
+
+
+def test_scan_segments_of_several_chunks_in_one_segment(gdn):  # noqa: F811
+    """As many sequences as workgroups: a segment is a sequence, of three chunks, with its states."""
+    B, T = 260, 150
+    assert segment(gdn, "bf16", B, T, 1, 1, 32, 32, None, True) == 192
+    check_scan(gdn, "bf16", None, **inputs("bf16", B, T, 1, 1, 32, 32, seed=71))
+
+
+@pytest.mark.parametrize("Hq,Hv,K,V,N,seg", [(1, 1, 32, 64, 300, 128), (4, 8, 32, 32, 64, 192), (2, 16, 64, 32, 128, 128),
+                                             (8, 16, 128, 64, 32, 192)])
+@pytest.mark.parametrize("state", [False, True])
+def test_scan_segments_of_several_chunks_joined(gdn, Hq, Hv, K, V, N, seg, state):  # noqa: F811
+    """A packed batch whose segments have two or three chunks, one sequence of several of them."""
+    announce(f"segments {Hq} {Hv} {K} {V} {N} {state}")
+    lens = [int(v) for v in torch.randint(0, 2 * (seg - 64), (N,), generator=gen(72))]
+    lens[N // 2], lens[3] = 5 * seg - 7, 0
+    most = seg * N if N > 128 else seg * max(N, -(-torch.cuda.get_device_properties(0).multi_processor_count // Hq))
+    while sum(lens) > most - 8:
+        lens[lens.index(max(lens[:N // 2]))] //= 2
+    n = N - 1
+    while sum(lens) <= most * (seg - 64) // seg:
+        lens[n], n = seg, n - 1
+    assert segment(gdn, "bf16", 1, 0, Hq, Hv, K, V, lens, True) == seg, sum(lens)
+    check_scan(gdn, "bf16", lens, **inputs("bf16", 1, 0, Hq, Hv, K, V, lens=lens, state=state, seed=73))
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 40), ("bf16", 64), ("f32", 1), ("f32", 16), ("f32", 17)])
+@pytest.mark.parametrize("Hq,Hv,K,V", [(1, 1, 32, 32), (2, 6, 64, 64)])
+def test_scan_of_one_short_segment_with_states(gdn, dtype, T, Hq, Hv, K, V):  # noqa: F811
+    assert segment(gdn, dtype, 3, T, Hq, Hv, K, V, None, False) == {("f32", 17): 16}.get((dtype, T), 64 if dtype == "bf16" else 16)
+    check_scan(gdn, dtype, None, **inputs(dtype, 3, T, Hq, Hv, K, V, seed=74))
+    lens = [T, 0, 1]
+    check_scan(gdn, dtype, lens, **inputs(dtype, 1, 0, Hq, Hv, K, V, lens=lens, seed=75))
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 700), ("f32", 700), ("f32", 2100)])
+def test_scan_long(gdn, dtype, T):  # noqa: F811
+    check_scan(gdn, dtype, None, **inputs(dtype, 1, T, 2, 4, 64, 64, seed=76))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scan_backward_of_a_growing_state(gdn, dtype):  # noqa: F811
+    i = inputs(dtype, 2, 150, 1, 2, 64, 32, seed=77)
+    i["A"] = i["A"].abs() * 0.02
+    check_scan(gdn, dtype, None, **i)
+
+
+# ---------------------------------------------------------------- masked tokens and infinities
+
+
+@pytest.mark.parametrize("mask", [float("-inf"), "lowest"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_step_of_minus_infinity_masks_its_token(gdn, dtype, mask):  # noqa: F811
+    """softplus(-inf) = 0: the token adds nothing and forgets nothing, in whole chunks and single places; its output
+    is the state's as it stands.  So does the type's lowest value."""
+    i = inputs(dtype, 2, 200, 1, 2, 64, 32, seed=81)
+    low = mask if mask != "lowest" else torch.finfo(DT[dtype]).min
+    i["dt"][0, 40:140] = low
+    i["dt"][1, ::3] = low
+    i["dt"][1, :64] = low
+    j = dict(i, dt=torch.where(i["dt"] == low, -200.0, i["dt"].float()).to(DT[dtype]))  # e^-200: 0 in fp32
+    check_scan(gdn, dtype, None, **j)
+    kw = dict(D=i["D"], dt_bias=i["bias"], initial_state=i["h0"])
+    ins = lambda i: [i[k] for k in ("c", "b", "x", "dt", "A")]  # noqa: E731
+    for a, r in zip(gdn.selective_scan_fwd(*ins(i), **kw), gdn.selective_scan_fwd(*ins(j), **kw)):
+        assert torch.equal(a, r)
+    for a, r in zip(gdn.selective_scan_bwd(*ins(i), i["dy"], dht=i["dht"], **kw),
+                    gdn.selective_scan_bwd(*ins(j), i["dy"], dht=i["dht"], **kw)):
+        assert torch.equal(a, r)
+    s = i["h0"].clone()
+    args = [i[k][:, 60] for k in ("c", "b", "x", "dt")]
+    args[3] = torch.full_like(args[3], low)
+    y = gdn.selective_scan_step(*args, i["A"], s, D=i["D"], dt_bias=i["bias"])
+    assert torch.equal(s, i["h0"]) and bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("what", ["c", "b", "x", "dt", "dy"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinity_stays_in_its_sequence(gdn, dtype, what, value):  # noqa: F811
+    lens = [70, 30, 64, 5]
+    i = inputs(dtype, 1, 0, 1, 2, 64, 32, lens=lens, seed=82)
+    j = dict(i, **{what: i[what].clone()})
+    j[what][0, 75] = value
+    keep, rows = torch.ones(sum(lens), dtype=torch.bool), [0, 2, 3]
+    keep[70:100] = False
+
+    def run(i):
+        kw = dict(D=i["D"], dt_bias=i["bias"], initial_state=i["h0"], cu_seqlens=cu_of(lens))
+        ins = [i[k] for k in ("c", "b", "x", "dt", "A")]
+        return gdn.selective_scan_fwd(*ins, **kw) + gdn.selective_scan_bwd(*ins, i["dy"], dht=i["dht"], **kw)
+
+    for n, a, r in zip(("y", "ht") + SCAN_OUT, run(j), run(i)):
+        if n in ("ht", "dh0"):
+            assert torch.equal(a[rows], r[rows]), n
+        elif n not in ("dA", "dD", "ddt_bias"):
+            assert torch.equal(a[0, keep], r[0, keep]), n
