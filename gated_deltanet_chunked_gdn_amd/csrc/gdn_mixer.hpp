@@ -91,11 +91,6 @@ struct Raw {
   }
 } __attribute__((aligned(sizeof(E) * VEC)));
 
-template <typename E>
-constexpr int vec_of() {
-  return 16 / (int)sizeof(E);
-}
-
 // 1 / (1 + exp(-z)): v_exp_f32 and v_rcp_f32 (each within an ulp or so); 0 and
 // 1 at the ends, since exp(-z) runs to infinity and to 0.
 __device__ __forceinline__ float sigmoidf(float z) {

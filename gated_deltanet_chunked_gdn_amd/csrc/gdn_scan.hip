@@ -44,28 +44,26 @@ struct Sweep {
   const void *L, *U, *P;
   int64_t ls, us, ps;  // elements from one token to the next
   int l_v, u_v, p_v;   // operand lies with the v-heads (else the c/b heads)
-  int LD;              // lane dimension (K or V)
+  int LD;              // lane dimension (K or V, 64 at the most)
 };
 
-template <typename E, int RD, int MODE>
+template <int RD, int MODE>
 __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s) {
   constexpr bool REV = MODE == kRLocal || MODE == kDx || MODE == kDb;
   constexpr bool OUT = MODE != kLocal && MODE != kRLocal;
   constexpr bool LANE_V = MODE != kDc && MODE != kDb;
   __shared__ __align__(16) float us[TB][RD], ps[OUT ? TB : 1][RD];
   __shared__ float del[TB], dec[TB];
-  const int lane = threadIdx.x, slices = (s.LD + 63) >> 6;
-  const int sl = blockIdx.x % slices, h = blockIdx.x / slices % a.Hv;
-  const int64_t slot = blockIdx.x / slices / a.Hv;
+  const int lane = threadIdx.x, h = blockIdx.x % a.Hv;
+  const int64_t slot = blockIdx.x / a.Hv;
   const SlotLoc loc = locate(a, slot);
   if (!loc.used || (MODE == kLocal && loc.last)) return;
   const int hq = h / (a.Hv / a.Hq);
-  const int l = sl * 64 + lane;
-  const bool on = l < s.LD;
-  const int lc = on ? l : s.LD - 1;  // idle lanes of a 32-wide operand read along, and write nothing
-  const E *L = static_cast<const E *>(s.L) + (int64_t)(s.l_v ? h : hq) * s.LD + lc;
-  const E *U = static_cast<const E *>(s.U) + (int64_t)(s.u_v ? h : hq) * RD;
-  const E *P = OUT ? static_cast<const E *>(s.P) + (int64_t)(s.p_v ? h : hq) * RD : nullptr;
+  const bool on = lane < s.LD;
+  const int lc = on ? lane : s.LD - 1;  // idle lanes of a 32-wide operand read along, and write nothing
+  const float *L = static_cast<const float *>(s.L) + (int64_t)(s.l_v ? h : hq) * s.LD + lc;
+  const float *U = static_cast<const float *>(s.U) + (int64_t)(s.u_v ? h : hq) * RD;
+  const float *P = OUT ? static_cast<const float *>(s.P) + (int64_t)(s.p_v ? h : hq) * RD : nullptr;
   const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.D ? a.D[h] : 0.f;
   const int64_t kv = (int64_t)a.K * a.V;
   const int64_t sr = LANE_V ? a.V : 1, so = LANE_V ? lc : (int64_t)lc * a.V;
@@ -89,12 +87,12 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
       const int j = i / RD, r = i % RD;
       const int jc = j < nb ? j : nb - 1;
       const int64_t t = REV ? loc.t1 - 1 - (b0 + jc) : loc.t0 + b0 + jc;
-      us[j][r] = to_f32(U[t * s.us + r]);
-      if (OUT) ps[j][r] = to_f32(P[t * s.ps + r]);
+      us[j][r] = U[t * s.us + r];
+      if (OUT) ps[j][r] = P[t * s.ps + r];
     }
     if (lane < nb) {
       const int64_t t = REV ? loc.t1 - 1 - (b0 + lane) : loc.t0 + b0 + lane;
-      const float z = to_f32(static_cast<const E *>(a.dt)[t * a.Hv + h]) + bias;
+      const float z = static_cast<const float *>(a.dt)[t * a.Hv + h] + bias;
       const float d = a.softplus ? softplusf(z) : z;
       del[lane] = d;
       dec[lane] = d * A;
@@ -104,7 +102,7 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
     for (int j = 0; j < TB; ++j) {
       const int jc = j < nb ? j : nb - 1;
       const int64_t t = REV ? loc.t1 - 1 - (b0 + jc) : loc.t0 + b0 + jc;
-      lv[j] = to_f32(L[t * s.ls]);
+      lv[j] = L[t * s.ls];
     }
     __syncthreads();
 #pragma unroll 1
@@ -134,16 +132,16 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
       }
       if (MODE == kOut) {
         const float x = mine;
-        if (on) static_cast<E *>(a.y)[(t * a.Hv + h) * a.V + l] = from_f32<E>(out + skip * x);
+        if (on) static_cast<float *>(a.y)[(t * a.Hv + h) * a.V + lane] = out + skip * x;
       } else if (MODE == kDc || MODE == kDb) {
         float *part = MODE == kDc ? w.dc_part(a) : w.db_part(a);
-        if (on) part[(t * a.Hv + h) * a.K + l] = MODE == kDc ? out + f * up : delta * out;
+        if (on) part[(t * a.Hv + h) * a.K + lane] = MODE == kDc ? out + f * up : delta * out;
       } else if (MODE == kDx) {
-        const float x = to_f32(static_cast<const E *>(a.x)[t * a.xs + (int64_t)h * a.V + lc]);
-        if (on) static_cast<E *>(a.dx)[(t * a.Hv + h) * a.V + l] = from_f32<E>(delta * (out + f * up) + skip * mine);
+        const float x = static_cast<const float *>(a.x)[t * a.xs + (int64_t)h * a.V + lc];
+        if (on) static_cast<float *>(a.dx)[(t * a.Hv + h) * a.V + lane] = delta * (out + f * up) + skip * mine;
         const float v = wave_sum(on ? x * out : 0.f), xd = wave_sum(on ? x * mine : 0.f);
         if (lane == 0) {
-          const int64_t i = ((int64_t)sl * a.Hv + h) * a.s.tokens + t;
+          const int64_t i = (int64_t)h * a.s.tokens + t;
           w.r_part(a)[i] = v;
           w.m_part(a)[i] = xd * up;
         }
@@ -156,14 +154,14 @@ __global__ __launch_bounds__(64) void sweep_kernel(ScanArgs a, Layout w, Sweep s
     if (on)
       for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
     // (in the backward the reverse pass, which has every segment: one writer)
-    if ((MODE == kRLocal || !a.dy) && lane == 0 && sl == 0) w.decay(a)[slot * a.Hv + h] = total;
+    if ((MODE == kRLocal || !a.dy) && lane == 0) w.decay(a)[slot * a.Hv + h] = total;
   }
   if (MODE == kOut && loc.last && a.ht && on) {
     float *dst = a.ht + (loc.n * (int64_t)a.Hv + h) * kv;
     for (int r = 0; r < RD; ++r) dst[r * sr + so] = S[r];
   }
   if (MODE == kDx) {
-    if (lane == 0) w.dd_part(a)[((int64_t)sl * a.slots + slot) * a.Hv + h] = dD;
+    if (lane == 0) w.dd_part(a)[slot * a.Hv + h] = dD;
   }
 }
 
@@ -430,7 +428,6 @@ __global__ __launch_bounds__(64) void heads_kernel(ScanArgs a, Layout w) {
 
 // dc, db: the sum over the heads of a group, 4 elements a thread.  (Tokens that
 // no sequence has have no parts, and their rows are not the kernel's.)
-template <typename E>
 __global__ __launch_bounds__(256) void group_kernel(ScanArgs a, Layout w) {
   const int64_t k4 = a.K / 4, n = a.s.tokens * a.Hq * k4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -449,20 +446,18 @@ __global__ __launch_bounds__(256) void group_kernel(ScanArgs a, Layout w) {
     c += pc[r * k4];
     b += pb[r * k4];
   }
-  st4(static_cast<E *>(a.dc) + i * 4, c[0], c[1], c[2], c[3]);
-  st4(static_cast<E *>(a.db) + i * 4, b[0], b[1], b[2], b[3]);
+  reinterpret_cast<f32x4 *>(a.dc)[i] = c;
+  reinterpret_cast<f32x4 *>(a.db)[i] = b;
 }
 
-template <typename E, int MODE>
+template <int MODE>
 hipError_t sweep(const char *name, const ScanArgs &a, const Layout &w, const Sweep &s, int rd, hipStream_t st) {
-  const unsigned blocks = (unsigned)(a.slots * a.Hv * ((s.LD + 63) / 64));
+  const unsigned blocks = (unsigned)(a.slots * a.Hv);
   KernelTimer kt(name, st);
   if (rd == 32)
-    sweep_kernel<E, 32, MODE><<<blocks, 64, 0, st>>>(a, w, s);
-  else if (rd == 64)
-    sweep_kernel<E, 64, MODE><<<blocks, 64, 0, st>>>(a, w, s);
+    sweep_kernel<32, MODE><<<blocks, 64, 0, st>>>(a, w, s);
   else
-    sweep_kernel<E, 128, MODE><<<blocks, 64, 0, st>>>(a, w, s);
+    sweep_kernel<64, MODE><<<blocks, 64, 0, st>>>(a, w, s);
   return hipGetLastError();
 }
 
@@ -481,19 +476,18 @@ unsigned carry_blocks(const ScanArgs &a) {
   return (unsigned)(((int64_t)a.s.N * a.Hv * a.K * a.V / 4 + 255) / 256);
 }
 
-template <typename E>
 hipError_t fwd(const ScanArgs &a, hipStream_t st) {
   const Layout w = layout(a, false);
   hipError_t e = hipSuccess;
   const Sweep out{a.x, a.b, a.c, a.xs, a.bs, a.cs, 1, 0, 0, a.V};
   if (!a.one_seg) {
-    e = sweep<E, kLocal>("scan_local", a, w, out, a.K, st);
+    e = sweep<kLocal>("scan_local", a, w, out, a.K, st);
     if (e != hipSuccess) return e;
     KernelTimer kt("scan_carry", st);
     carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  return sweep<E, kOut>("scan_out", a, w, out, a.K, st);
+  return sweep<kOut>("scan_out", a, w, out, a.K, st);
 }
 
 hipError_t fwd_mma(const ScanArgs &a, hipStream_t st) {
@@ -521,7 +515,6 @@ hipError_t bwd_mma(const ScanArgs &a, hipStream_t st) {
   return launch_mma_grad(a, w, st);
 }
 
-template <typename E>
 hipError_t bwd(const ScanArgs &a, hipStream_t st) {
   const Layout w = layout(a, true);
   const int64_t qs = (int64_t)a.Hv * a.V;  // dy is contiguous
@@ -532,16 +525,16 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
   hipError_t e;
 #define GDN_DO(x) \
   if ((e = (x)) != hipSuccess) return e
-  GDN_DO((sweep<E, kLocal>("scan_local", a, w, out, a.K, st)));
-  GDN_DO((sweep<E, kRLocal>("scan_rlocal", a, w, dx, a.K, st)));
+  GDN_DO((sweep<kLocal>("scan_local", a, w, out, a.K, st)));
+  GDN_DO((sweep<kRLocal>("scan_rlocal", a, w, dx, a.K, st)));
   {
     KernelTimer kt("scan_carry", st);
     carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
     GDN_DO(hipGetLastError());
   }
-  GDN_DO((sweep<E, kDc>("scan_dc", a, w, dc, a.V, st)));
-  GDN_DO((sweep<E, kDx>("scan_dx", a, w, dx, a.K, st)));
-  GDN_DO((sweep<E, kDb>("scan_db", a, w, db, a.V, st)));
+  GDN_DO((sweep<kDc>("scan_dc", a, w, dc, a.V, st)));
+  GDN_DO((sweep<kDx>("scan_dx", a, w, dx, a.K, st)));
+  GDN_DO((sweep<kDb>("scan_db", a, w, db, a.V, st)));
   {
     KernelTimer kt("scan_gates", st);
     gates(a, w, st);
@@ -551,7 +544,7 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
   if (a.s.tokens) {
     KernelTimer kt("scan_group", st);
     const int64_t n = a.s.tokens * a.Hq * (a.K / 4);
-    group_kernel<E><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, w);
+    group_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, w);
     GDN_DO(hipGetLastError());
   }
 #undef GDN_DO
@@ -562,15 +555,15 @@ hipError_t bwd(const ScanArgs &a, hipStream_t st) {
 }  // namespace scan
 
 // Segments: as long as the whole sequence unless that leaves compute units
-// without work, then as many as give each two workgroups of the matrix
-// kernels (bf16, whole chunks of 64) or eight waves of the sweeps (fp32, which walk
-// token by token: down to 16 tokens).  fp32 backward: 64 tokens at the most,
+// without work, then as many as give each a workgroup of the matrix kernels
+// (bf16, whole chunks of 64) or eight waves of the sweeps (fp32, which walk token
+// by token: down to 16 tokens).  fp32 backward: 64 tokens at the most,
 // what a workgroup of the gates' kernel has.
 ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
   ScanArgs a = a0;
   // workgroups a segment
   const int slices = a.Hv / a.Hq * (a.V / 32);
-  const int64_t per = a.dtype == 1 ? (int64_t)a.Hq * (slices / scan::slices_per_block(slices)) : (int64_t)a.Hv * ((a.V + 63) / 64);
+  const int64_t per = a.dtype == 1 ? (int64_t)a.Hq * (slices / scan::slices_per_block(slices)) : a.Hv;
   int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 8) + per - 1) / per;  // segments over the whole batch
   if (want < a.s.N) want = a.s.N;
   int64_t seg = (a.s.tokens + want - 1) / want;
@@ -587,10 +580,10 @@ ScanPlan scan_plan(const ScanArgs &a0, bool bwd) {
 }
 
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
-  return a.dtype == 1 ? scan::fwd_mma(a, st) : scan::fwd<float>(a, st);
+  return a.dtype == 1 ? scan::fwd_mma(a, st) : scan::fwd(a, st);
 }
 hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
-  return a.dtype == 1 ? scan::bwd_mma(a, st) : scan::bwd<float>(a, st);
+  return a.dtype == 1 ? scan::bwd_mma(a, st) : scan::bwd(a, st);
 }
 
 }  // namespace gdn

@@ -42,7 +42,7 @@ struct Layout {
   // [slots][Hv][K][V]: the gradient of a segment's first state from its own
   // tokens, then of its last state from what follows
   __host__ __device__ float *zend(const ScanArgs &a) const { return at(a, o_zend); }
-  // [slices][Hv][tokens] each: parts of a_t (bf16), r_t and m_t
+  // [slices (fp32: 1)][Hv][tokens] each: parts of a_t (bf16), r_t and m_t
   __host__ __device__ float *a_part(const ScanArgs &a) const { return at(a, o_a); }
   __host__ __device__ float *r_part(const ScanArgs &a) const { return at(a, o_r); }
   __host__ __device__ float *m_part(const ScanArgs &a) const { return at(a, o_m); }
@@ -93,9 +93,9 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
   }
   if (bwd && !a.one_seg) w.o_zend = piece(heads * kv * 4);
   if (bwd && a.dtype != 1) {
-    w.o_r = piece(tok * ((a.V + 63) / 64) * 4);
-    w.o_m = piece(tok * ((a.V + 63) / 64) * 4);
-    w.o_dd = piece(heads * ((a.V + 63) / 64) * 4);
+    w.o_r = piece(tok * 4);
+    w.o_m = piece(tok * 4);
+    w.o_dd = piece(heads * 4);
     w.o_head = piece(heads * 3 * 4);
     w.o_dc = piece(tok * a.K * 4);
     w.o_db = piece(tok * a.K * 4);
