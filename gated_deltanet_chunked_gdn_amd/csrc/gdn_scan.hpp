@@ -31,7 +31,7 @@ struct SlotLoc {
 // Byte offsets of the workspace's pieces (each at a 256-byte boundary).
 struct Layout {
   size_t o_start = 0, o_decay = 0, o_zend = 0, o_a = 0, o_r = 0, o_ri = 0, o_half = 0, o_quarter = 0, o_m = 0, o_dd = 0, o_x = 0, o_head = 0,
-         o_dc = 0, o_db = 0, o_ai = 0, o_shi = 0, o_slo = 0, o_z = 0, total = 0;
+         o_dc = 0, o_db = 0, o_ai = 0, o_shi = 0, o_slow = 0, o_z = 0, total = 0;
   int64_t chunks = 0;      // slots of 64-token chunks (bf16 backward)
   __host__ __device__ float *at(const ScanArgs &a, size_t o) const { return reinterpret_cast<float *>(a.ws + o); }
   __host__ __device__ bf16 *bat(const ScanArgs &a, size_t o) const { return reinterpret_cast<bf16 *>(a.ws + o); }
@@ -65,11 +65,12 @@ struct Layout {
   __host__ __device__ float *dc_part(const ScanArgs &a) const { return at(a, o_dc); }
   __host__ __device__ float *db_part(const ScanArgs &a) const { return at(a, o_db); }
   // bf16 problems, [chunks][Hv][V / 32][K / 16][64][8] each: the state entering
-  // a chunk in two parts, and the gradient of the state leaving it.  Piece
+  // a chunk as bf16 and as the lower 16 bits of its fp32 form (split_halves), and
+  // the gradient of the state leaving it.  Piece
   // (s, lane) holds rows 16 s + rho(lane >> 5, e) of column lane & 31: what a
   // lane of the passes has in its accumulators, 1 KB a store.
   __host__ __device__ bf16 *s_hi(const ScanArgs &a) const { return bat(a, o_shi); }
-  __host__ __device__ bf16 *s_lo(const ScanArgs &a) const { return bat(a, o_slo); }
+  __host__ __device__ bf16 *s_low(const ScanArgs &a) const { return bat(a, o_slow); }
   __host__ __device__ bf16 *z(const ScanArgs &a) const { return bat(a, o_z); }
   // slot of chunk c of a segment
   __device__ int64_t chunk(const ScanArgs &a, const SlotLoc &l, int c) const {
@@ -115,7 +116,7 @@ inline Layout layout(const ScanArgs &a, bool bwd) {
     w.o_x = piece(ch * slices * 4);
     w.o_head = piece(ch * 3 * 4);
     w.o_shi = piece(ch * kv * 2);
-    w.o_slo = piece(ch * kv * 2);
+    w.o_slow = piece(ch * kv * 2);
     w.o_z = piece(ch * kv * 2);
   }
   w.total = off ? off : 256;

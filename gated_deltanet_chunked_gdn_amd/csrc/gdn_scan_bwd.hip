@@ -27,13 +27,13 @@
 //
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
 // enters them is held to fp32: the recurrences of S and Z, S and Z as
-// operands in two bf16 parts, G and M from the inputs as they are, <S, Z>
-// afresh in every chunk, and the pairs' sum of dg_t by halves and quarters of
+// operands in three bf16 parts, G and M from the inputs as they are, <S, Z>
+// afresh in every chunk from both in fp32, and the pairs' sum of dg_t by halves and quarters of
 // the chunk: pairs from both halves by i (t in the second) or by j (t in the
 // first), terms that do not cancel; so the pairs from both quarters of a half;
 // pairs inside a quarter as the sum over s >= t of a_s - delta_s r_s, where
 // they cancel if both are behind t.  (S and Z in one part would leave ddt_bias
-// 5e-4 off; <S, Z> carried along over two chunks, 3e-5; the last sum over the
+// 5e-4 off, in two parts dA of a short sequence with states up to 3e-5; <S, Z> carried along over two chunks, 3e-5; the last sum over the
 // whole chunk 2.3e-6 against 1.1e-6 by halves.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 //
@@ -68,11 +68,6 @@ __device__ __forceinline__ float fold16(float (&r)[16], int lane) {
   }
   const bool b = lane & 8;
   return (b ? r[1] : r[0]) + __shfl_xor(b ? r[0] : r[1], 8);
-}
-
-// fp32 dot product of two bf16x8, added to c
-__device__ __forceinline__ float dot8(const bf16x8 &a, const bf16x8 &b, float c) {
-  return dot_piece<bf16>(__builtin_bit_cast(uint4, a), __builtin_bit_cast(uint4, b), c);
 }
 
 // Token of this lane's tile: sum over the 32 columns of acc (rows column,
@@ -144,7 +139,8 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       }
     return;
   }
-  bf16x8 sh[K / 16], sl[K / 16];
+  bf16x8 sh[K / 16];
+  uint4 sl[K / 16];
   // one chunk's rows on their way to LDS.  (An object of the loop's body: one
   // outside it, loaded under a condition, would hold its registers throughout.)
   struct In {
@@ -172,7 +168,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
 #pragma unroll
     for (int s = 0; s < K / 16; ++s) {
       sh[s] = *reinterpret_cast<const bf16x8 *>(w.s_hi(a) + at + s * 512);
-      sl[s] = *reinterpret_cast<const bf16x8 *>(w.s_lo(a) + at + s * 512);
+      sl[s] = *reinterpret_cast<const uint4 *>(w.s_low(a) + at + s * 512);
     }
   };
   auto commit = [&](const In &r, int tid) {
@@ -213,16 +209,15 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       const bf16 *k0 = k + r32 * KP + 8 * h2;
 #pragma unroll
       for (int s = 0; s < K / 16; ++s) {
-        const Split zf = split(Z[s >> 1], s & 1);
+        const Split3 zf = split(Z[s >> 1], s & 1);
         *reinterpret_cast<bf16x8 *>(w.z(a) + at + s * 512) = zf.hi;
-        xd = dot8(sh[s], zf.hi, xd);
-        xd = dot8(sh[s], zf.lo, xd);
-        xd = dot8(sl[s], zf.hi, xd);
+        xd = dot_halves(sh[s], sl[s], Z[s >> 1], s & 1, xd);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const bf16x8 kf = lds16(k0 + 32 * i * KP + 16 * s);
-          Y[i] = mma32(zf.hi, kf, Y[i]);
           Y[i] = mma32(zf.lo, kf, Y[i]);
+          Y[i] = mma32(zf.mid, kf, Y[i]);
+          Y[i] = mma32(zf.hi, kf, Y[i]);
         }
         if (s & 1) __builtin_amdgcn_sched_barrier(0);
       }

@@ -35,8 +35,8 @@ namespace {
 // What a pass over a segment's chunks does:
 //   kLocal   the segment's last state from zero and its decay (for carry_kernel)
 //   kOut     y, from the segment's start state, and the sequence's last state
-//   kStates  the state entering every chunk, as two bf16 parts, and the part
-//            of a_i that comes from it, p_i c_i . S dy_i (backward)
+//   kStates  the state entering every chunk, as bf16 and what fp32 has below
+//            it, and the part of a_i that comes from it, p_i c_i . S dy_i (backward)
 //   kRLocal  reverse: the gradient of the segment's first state from its own
 //            outputs; a.b, a.x hold c and dy: Z = 2^{gamma_L} Z + C^T (2^{gamma} dY)
 enum { kLocal, kOut, kStates, kRLocal };
@@ -73,6 +73,12 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
     src = a.one_seg ? (a.h0 ? a.h0 + (loc.n * (int64_t)a.Hv + h) * kv : nullptr) : w.start(a) + (slot * a.Hv + h) * kv;
   if (src) {
     state_io<K, V>(S, const_cast<float *>(src) + v0, false, lane);
+    if (MODE == kStates) {
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[j][i] = quiet(S[j][i]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < KT; ++j) S[j] = zero16();
@@ -133,14 +139,15 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
       f32x16 U[2] = {zero16(), zero16()};  // U^T = S^T C^T
 #pragma unroll
       for (int s = 0; s < K / 16; ++s) {
-        const Split x = split(S[s >> 1], s & 1);
+        const SplitHalves x = split_halves(S[s >> 1], s & 1);
         *reinterpret_cast<bf16x8 *>(w.s_hi(a) + at + s * 512) = x.hi;
-        *reinterpret_cast<bf16x8 *>(w.s_lo(a) + at + s * 512) = x.lo;
+        *reinterpret_cast<uint4 *>(w.s_low(a) + at + s * 512) = x.low;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const bf16x8 qf = lds16(q + (32 * i + r32) * KP + 16 * s + 8 * h2);
-          U[i] = mma32(x.hi, qf, U[i]);
           U[i] = mma32(x.lo, qf, U[i]);
+          U[i] = mma32(x.mid, qf, U[i]);
+          U[i] = mma32(x.hi, qf, U[i]);
         }
         if (s & 1) __builtin_amdgcn_sched_barrier(0);
       }

@@ -194,19 +194,65 @@ __device__ __forceinline__ Split3 split_scaled(const bf16x8 &x, const float *w) 
   return r;
 }
 
-// bf16 parts hi + lo, to 2^-18
-struct Split {
-  bf16x8 hi, lo;
-};
-// bf16 parts of operand slots 8 s .. 8 s + 7 of an accumulator tile
-__device__ __forceinline__ Split split(const f32x16 &x, int s) {
-  Split r;
+// Operand slots 8 s .. 8 s + 7 of an accumulator tile as the sum of three bf16
+// numbers, each rounded to nearest: exact but for fp32's last bit or so.
+__device__ __forceinline__ Split3 split(const f32x16 &x, int s) {
+  Split3 r;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     r.hi[e] = (bf16)x[8 * s + e];
-    r.lo[e] = (bf16)(x[8 * s + e] - (float)r.hi[e]);
+    const float r1 = x[8 * s + e] - (float)r.hi[e];
+    r.mid[e] = (bf16)r1;
+    r.lo[e] = (bf16)(r1 - (float)r.mid[e]);
   }
   return r;
+}
+// The same, hi rounded by an integer sum (halves away from 0), and the fp32
+// numbers' lower 16 bits: these and hi are the numbers again (dot_halves), in
+// the room of two bf16 parts.  (A NaN whose upper bits are all ones would
+// round to 0: quiet() first.)
+struct SplitHalves : Split3 {
+  uint4 low;
+};
+__device__ __forceinline__ SplitHalves split_halves(const f32x16 &x, int s) {
+  SplitHalves r;
+  uint32_t hi[4], low[4];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    uint32_t u[2], b[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float f = x[8 * s + e + k];
+      b[k] = __builtin_bit_cast(uint32_t, f);
+      u[k] = b[k] + 0x8000u;
+      const float r1 = f - __builtin_bit_cast(float, u[k] & 0xFFFF0000u);
+      r.mid[e + k] = (bf16)r1;
+      r.lo[e + k] = (bf16)(r1 - (float)r.mid[e + k]);
+    }
+    hi[e / 2] = __builtin_amdgcn_perm(u[1], u[0], 0x07060302);
+    low[e / 2] = __builtin_amdgcn_perm(b[1], b[0], 0x05040100);
+  }
+  r.hi = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+  r.low = make_uint4(low[0], low[1], low[2], low[3]);
+  return r;
+}
+__device__ __forceinline__ float quiet(float x) {
+  return x == x ? x : __builtin_bit_cast(float, 0x7FC00000u);
+}
+// c plus the products of such numbers and slots 8 s .. of a tile, in fp32.
+__device__ __forceinline__ float dot_halves(const bf16x8 &hi, const uint4 &low, const f32x16 &z, int s, float c) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  const uint4 h4 = __builtin_bit_cast(uint4, hi);
+  const uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {low.x, low.y, low.z, low.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // (hi is one more where the lower half is 0x8000 or above)
+    const uint32_t up = (l[i] >> 15) & 0x00010001u;
+    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, h[i]) - __builtin_bit_cast(u16x2, up));
+    c += __builtin_bit_cast(float, __builtin_amdgcn_perm(b, l[i], 0x05040100)) * z[8 * s + 2 * i];
+    c += __builtin_bit_cast(float, __builtin_amdgcn_perm(b, l[i], 0x07060302)) * z[8 * s + 2 * i + 1];
+  }
+  return c;
 }
 
 // Sum over the 32 columns of an accumulator tile (rows column, lane token)

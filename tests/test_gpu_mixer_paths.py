@@ -460,3 +460,42 @@ def test_an_infinity_stays_in_its_sequence(gdn, dtype, what, value):  # noqa: F8
             assert torch.equal(a[rows], r[rows]), n
         elif n not in ("dA", "dD", "ddt_bias"):
             assert torch.equal(a[0, keep], r[0, keep]), n
+
+
+# ---------------------------------------------------------------- precision of the gates' gradients
+
+
+@pytest.mark.parametrize("part", ["S Z", "c S dy", "b Z x"])
+@pytest.mark.parametrize("dtype,K,V", [("bf16", 32, 32), ("bf16", 64, 64), ("bf16", 128, 64), ("bf16", 32, 128), ("f32", 32, 32),
+                                       ("f32", 64, 64)])
+def test_scan_gate_sums_take_states_as_they_are(gdn, dtype, K, V, part):  # noqa: F811
+    """dA of sequences of two tokens, from a state, a state's gradient, or both.  dg_t = e^{g_t} <S_{t-1}, Z_t> is a
+    sum of K V products; with random signs it is about e^{g_t} |S| |Z| / sqrt(K V), and so is each factor's rounding
+    to a part u of itself about u times that.  fp32's u is 2^-24; the sums' own roundings and those of delta and the
+    decays are a few of those, 2^-20 leaves 16.  (A factor in two bf16 parts has u = 2^-18.)"""
+    announce(f"gate sums {dtype} {K} {V} {part}")
+    N, Hv = 40, 8
+    i = inputs(dtype, N, 2, 1, Hv, K, V, seed=91)
+    i["A"] = -torch.ones(Hv, device="cuda")
+    if part == "c S dy":
+        i["dht"] = None
+    if part == "b Z x":
+        i["h0"] = None
+    if part != "c S dy":
+        i["dy"].zero_()
+    x, b, c, dy = (d64(i[k]) for k in ("x", "b", "c", "dy"))
+    delta = delta_of(d64(i["dt"]), d64(i["bias"]), True)
+    dec = torch.exp(delta * d64(i["A"]))[..., None, None]
+    zero = torch.zeros(N, Hv, K, V, dtype=torch.float64, device="cuda")
+    S0, Z2 = (zero if t is None else d64(t) for t in (i["h0"], i["dht"]))
+    S1 = dec[:, 0] * S0 + delta[:, 0, :, None, None] * b[:, 0, :, :, None] * x[:, 0, :, None]
+    Z1 = c[:, 1, :, :, None] * dy[:, 1, :, None] + Z2
+    Z0 = c[:, 0, :, :, None] * dy[:, 0, :, None] + dec[:, 1] * Z1
+    dg = torch.stack([(dec[:, 0] * S0 * Z0).sum((2, 3)), (dec[:, 1] * S1 * Z1).sum((2, 3))], 1)
+    size = torch.stack([dec[:, 0, :, 0, 0] * S0.norm(dim=(2, 3)) * Z0.norm(dim=(2, 3)),
+                        dec[:, 1, :, 0, 0] * S1.norm(dim=(2, 3)) * Z1.norm(dim=(2, 3))], 1) / (K * V) ** 0.5
+    got = gdn.selective_scan_bwd(i["c"], i["b"], i["x"], i["dt"], i["A"], i["dy"], dht=i["dht"], dt_bias=i["bias"],
+                                 initial_state=i["h0"])[4]
+    off = (d64(got) - (delta * dg).sum((0, 1))).abs()
+    most = 2.0 ** -20 * ((delta * size) ** 2).sum((0, 1)).sqrt()
+    assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
