@@ -42,16 +42,18 @@ struct Layout {
   // [slots][Hv][K][V]: the gradient of a segment's first state from its own
   // tokens, then of its last state from what follows
   __host__ __device__ float *zend(const ScanArgs &a) const { return at(a, o_zend); }
-  // [slices (fp32: 1)][Hv][tokens] each: parts of a_t (bf16), r_t and m_t
+  // [slices (fp32: 1)][Hv][tokens] each: parts of the pairs inside token t's
+  // quarter of a chunk that count for dg_t (bf16), of r_t and m_t
   __host__ __device__ float *a_part(const ScanArgs &a) const { return at(a, o_a); }
   __host__ __device__ float *r_part(const ScanArgs &a) const { return at(a, o_r); }
   __host__ __device__ float *m_part(const ScanArgs &a) const { return at(a, o_m); }
-  // bf16, the same: what of a_t comes from the state entering the chunk, and
-  // of r_t from the gradient of the state leaving it (a_part, r_part: the rest)
+  // bf16, the same: a_t, and what of r_t comes from the gradient of the state
+  // leaving the chunk
   __host__ __device__ float *ai_part(const ScanArgs &a) const { return at(a, o_ai); }
   __host__ __device__ float *ri_part(const ScanArgs &a) const { return at(a, o_ri); }
-  // and what pairs of tokens from both halves of a chunk add, to r in the
-  // first half, to a in the second; pairs from both quarters of a half likewise
+  // and the pairs of tokens from both halves of a chunk, by the earlier token (in
+  // r) in the first half, by the later in the second; from both quarters of a half
+  // likewise
   __host__ __device__ float *half_part(const ScanArgs &a) const { return at(a, o_half); }
   __host__ __device__ float *quarter_part(const ScanArgs &a) const { return at(a, o_quarter); }
   // parts of dD: [slices][slots, bf16: chunks][Hv]
@@ -136,23 +138,6 @@ hipError_t launch_mma_locals(const ScanArgs &a, const Layout &w, hipStream_t st)
 // bf16, gdn_scan_bwd.hip
 hipError_t launch_mma_grad(const ScanArgs &a, const Layout &w, hipStream_t st);
 
-// The chain of dg over 64 tokens (bf16), lane 0 the last: sums from lane 0 on
-// of `val` onto `next` (<S, Z> of the state behind them), begun again where a
-// token forgets all (`cut`): dg_t = e^{g_t} <S_{t-1}, Z_t> is 0 there.  In 64
-// bits, since dg cancels against r and m in the sums over all tokens.
-__device__ __forceinline__ double dg_chain(double val, int cut, double next, int lane) {
-  double dg = cut ? 0.0 : val;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double below = __shfl_up(dg, d);
-    const int cut_below = __shfl_up(cut, d);
-    if (lane >= d && !cut) {
-      dg += below;
-      cut = cut_below;
-    }
-  }
-  return cut ? dg : dg + next;
-}
 // Lane 0 the last token: the sum of v from a lane's token on, and over the
 // tokens before it.
 __device__ __forceinline__ double sum_upto(double v, int lane) {

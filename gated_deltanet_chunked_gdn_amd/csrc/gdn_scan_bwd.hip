@@ -12,14 +12,14 @@
 //
 // and for the gates, with W_ij = E_ij G_ij M_ij,
 //
-//   a_i = sum_{j < i} W_ij delta_j + p_i c_i . S dy_i
-//   r_j = sum_{i > j} W_ij,   z_j = w_j b_j . Z x_j,   m_j = W_jj
-//   dg_t = 2^{gamma_L} <S, Z> + sum_{s >= t} p_s c_s . S dy_s + sum_{s < t} delta_s z_s
+//   a_i = p_i c_i . S dy_i,   z_j = w_j b_j . Z x_j
+//   r_j = sum_{i > j} W_ij,   m_j = W_jj
+//   dg_t = 2^{gamma_L} <S, Z> + sum_{i >= t} a_i + sum_{j < t} delta_j z_j
 //          + sum_{j < t <= i} W_ij delta_j
 //   d delta_t = r_t + z_t + m_t + A dg_t
 //
-// The pass that forms the states (kStates, gdn_scan_mma.hip) also has the
-// state's part of a_i.  Two kernels share the rest.  grad_kernel walks a
+// The pass that forms the states (kStates, gdn_scan_mma.hip) also has a_i.  Two
+// kernels share the rest.  grad_kernel walks a
 // segment's chunks from its end with Z in accumulators (32 columns of a head a
 // wave, as the forward): dx, the gates' sums, and Z of every chunk, rounded to
 // bf16, for the other.  pair_kernel has dc and db: one chunk of one head group
@@ -28,13 +28,14 @@
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
 // enters them is held to fp32: the recurrences of S and Z, S and Z as
 // operands in three bf16 parts, G and M from the inputs as they are, <S, Z>
-// afresh in every chunk from both in fp32, and the pairs' sum of dg_t by halves and quarters of
-// the chunk: pairs from both halves by i (t in the second) or by j (t in the
-// first), terms that do not cancel; so the pairs from both quarters of a half;
-// pairs inside a quarter as the sum over s >= t of a_s - delta_s r_s, where
-// they cancel if both are behind t.  (S and Z in one part would leave ddt_bias
-// 5e-4 off, in two parts dA of a short sequence with states up to 3e-5; <S, Z> carried along over two chunks, 3e-5; the last sum over the
-// whole chunk 2.3e-6 against 1.1e-6 by halves.)
+// afresh in every chunk from both in fp32, and the pairs' sum of dg_t by halves
+// and quarters of the chunk, so that every pair enters only where it counts:
+// pairs from both halves by i (t in the second) or by j (t in the first), pairs
+// from both quarters of a half likewise, pairs inside a quarter by the sum over
+// their rectangle j < t <= i.  (As sums of all pairs to t less those behind t,
+// the pairs inside a quarter put dA up to 2e-5 off where strong decays lie among
+// mild ones.  S and Z in two bf16 parts would leave dA of a short sequence with
+// states 3e-5 off; <S, Z> carried along over two chunks, ddt_bias 3e-5.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 //
 // 2 x 4096 tokens x 64 heads, K 128, V 64: passes from zero 78 us, carries 17,
@@ -100,6 +101,33 @@ __device__ __forceinline__ void put_rows(const f32x16 &acc, float skip, const bf
     const auto r = __builtin_amdgcn_permlane32_swap(o[b].y, o[b + 1].y, false, false);
     buf_store16(make_uint4(p[0], r[0], p[1], r[1]), out, off + (off == kOutside ? 0u : (uint32_t)(16 * b + 16 * h2)));
   }
+}
+
+// v[4 b + e]: W_ij delta_j of the row i = 8 b + 4 h2 + e and this lane's column j
+// of a diagonal tile.  Where i and j are of one quarter it becomes, for j < i, the
+// sum of the column from row i to the quarter's end: the sum of these over the
+// quarter's columns is that of the pairs j < t <= i at t = i.
+__device__ __forceinline__ void own_rectangles(float (&v)[16], int j, int h2) {
+  const bool late = j & 16;
+  float s[16];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    s[4 * b + 3] = v[4 * b + 3];
+#pragma unroll
+    for (int e = 2; e >= 0; --e) s[4 * b + e] = v[4 * b + e] + s[4 * b + e + 1];
+  }
+  // the quarter's rows in fours: this lane's first, the other half's, again each
+  const float second = late ? s[12] : s[4];
+  const float o0 = __shfl_xor(late ? s[8] : s[0], 32), o1 = __shfl_xor(second, 32);
+  const float after[2] = {second + o1 + (h2 ? 0.f : o0), h2 ? 0.f : o1};
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = 4 * b + e;
+      const float sum = 8 * b + 4 * h2 + e > j ? s[k] + after[b & 1] : 0.f;
+      v[k] = (b >> 1) == late ? sum : v[k];
+    }
 }
 
 // The next forgetting token of the half above j (32: none)
@@ -290,6 +318,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) T = mma32(df[2 * it + s], slots(P, s), T);
+        if (it == jt) own_rectangles(ar, r32, h2);
         rs[0] += __shfl_xor(rs[0], 32);
         rs[1] += __shfl_xor(rs[1], 32);
         const float lo = fold16(ar, lane), hi = __shfl_xor(lo, 16);  // j in the tile's first, second 16 columns (lanes of the first)
@@ -567,23 +596,10 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
   }
 }
 
-// Tokens of `width` in a row, tok = rows - 1 - lane: the chain of dg_chain over
-// the pairs inside them.
-__device__ __forceinline__ double inner_chain(double val, int cut, int tok, int lane, int width) {
-  double dg = cut ? 0. : val;
-  for (int d = 1; d < width; d <<= 1) {
-    const double later = __shfl_up(dg, d);
-    const int cut_later = __shfl_up(cut, d);
-    if (lane >= d && ((tok + d) ^ tok) < width && !cut) {
-      dg += later;
-      cut = cut_later;
-    }
-  }
-  return dg;
-}
-// The pairs from two such neighbours: for t in the second, the sum of v over
-// its tokens from t on (a_i); in the first, over its tokens before t (delta_j
-// r_j).  (No cut: the terms are 0 where a token between i and j forgets all.)
+// Tokens of `width` in a row, tok = rows - 1 - lane, and the pairs from two such
+// neighbours: for t in the second, the sum of v over its tokens from t on (a_i);
+// in the first, over its tokens before t (delta_j r_j).  (The
+// terms are 0 where a token between i and j forgets all.)
 __device__ __forceinline__ double outer_sum(double v, int tok, int lane, int width) {
   const bool second = tok & width;
   const double prior = __shfl_down(v, 1);
@@ -595,8 +611,9 @@ __device__ __forceinline__ double outer_sum(double v, int tok, int lane, int wid
   }
   return v;
 }
-// The gates of one chunk and head: dg from the chunk's <S, Z> and its a, r, z,
-// then ddt and the chunk's parts of dA, ddt_bias, dD.  Lanes are tokens, lane
+// The gates of one chunk and head: dg from the chunk's <S, Z>, its a, z and
+// pairs (in 64 bits, since dg cancels against r and m in the sums over all
+// tokens), then ddt and the chunk's parts of dA, ddt_bias, dD.  Lanes are tokens, lane
 // 0 the last.
 __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) {
   const int lane = threadIdx.x & 63;
@@ -632,11 +649,11 @@ __global__ __launch_bounds__(256) void chunk_gates_kernel(ScanArgs a, Layout w) 
   const float z = (float)static_cast<const bf16 *>(a.dt)[t * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
   const float delta = a.softplus ? softplusf(z) : z;
   const int tok = rows - 1 - lane;
-  const bool cut = on && delta * A * kLog2e < kForget, late32 = tok & 32, late16 = tok & 16;
-  const double dg = dg_chain(on ? ai : 0., cut, x, lane) + sum_before(on ? delta * ri : 0., lane) +
+  const bool late32 = tok & 32, late16 = tok & 16;
+  const double dg = x + sum_upto(on ? ai : 0., lane) + sum_before(on ? delta * ri : 0., lane) +
                     outer_sum(on ? (late32 ? half : delta * half) : 0., tok, lane, 32) +
                     outer_sum(on ? (late16 ? quarter : delta * quarter) : 0., tok, lane, 16) +
-                    inner_chain(on ? av - delta * rv : 0., cut, tok, lane, 16);
+                    (on ? av : 0.);
   double dd = rv + (late16 ? 0. : quarter) + (late32 ? 0. : half) + ri + mv + A * dg;
   if (a.softplus) dd *= 1.f / (1.f + expf(-z));
   if (on) static_cast<bf16 *>(a.ddt)[t * a.Hv + h] = (bf16)(float)dd;

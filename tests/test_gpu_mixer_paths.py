@@ -499,3 +499,32 @@ def test_scan_gate_sums_take_states_as_they_are(gdn, dtype, K, V, part):  # noqa
     off = (d64(got) - (delta * dg).sum((0, 1))).abs()
     most = 2.0 ** -20 * ((delta * size) ** 2).sum((0, 1)).sqrt()
     assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
+
+
+@pytest.mark.parametrize("K,V", [(32, 32), (64, 64)])
+@pytest.mark.parametrize("T", [5, 16, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scan_gate_sums_of_a_few_tokens(gdn, dtype, T, K, V):  # noqa: F811
+    """dA where tokens that forget nearly all lie among tokens that forget little: theirs is the longest step and the
+    least dg, far below the products of the pairs on either side.  The bound is the one above, 2^-20 of
+    delta_t e^{g_t} |S_{t-1}| |Z_t| / sqrt(K V) for each token, joined as independent errors are."""
+    announce(f"gate sums of {T} tokens {dtype} {K} {V}")
+    N, Hv = 40, 6
+    i = inputs(dtype, N, T, 1, Hv, K, V, state=False, seed=92)
+    i["A"] = -torch.ones(Hv, device="cuda")
+    step = torch.tensor([0.001, 0.001, 0.02, 0.3, 9.0, 14.0])[torch.randint(0, 6, (N, T, Hv), generator=gen(93))]
+    i["dt"] = step.to(DT[dtype]).cuda()
+    x, b, c, dy, delta = (d64(i[k]) for k in ("x", "b", "c", "dy", "dt"))
+    dec = torch.exp(-delta)[..., None, None]
+    S, Z = [torch.zeros(N, Hv, K, V, dtype=torch.float64, device="cuda")], [None] * T
+    for t in range(T):
+        S.append(dec[:, t] * S[t] + delta[:, t, :, None, None] * b[:, t, :, :, None] * x[:, t, :, None])
+    after = torch.zeros_like(S[0])
+    for t in range(T - 1, -1, -1):
+        Z[t] = c[:, t, :, :, None] * dy[:, t, :, None] + after
+        after = dec[:, t] * Z[t]
+    want = sum((delta[:, t] * (dec[:, t] * S[t] * Z[t]).sum((2, 3))).sum(0) for t in range(T))
+    size = sum(((delta[:, t] * dec[:, t, :, 0, 0] * S[t].norm(dim=(2, 3)) * Z[t].norm(dim=(2, 3))) ** 2).sum(0) for t in range(T))
+    got = gdn.selective_scan_bwd(i["c"], i["b"], i["x"], i["dt"], i["A"], i["dy"], dt_softplus=False)[4]
+    off, most = (d64(got) - want).abs(), 2.0 ** -20 * (size / (K * V)).sqrt()
+    assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
