@@ -215,6 +215,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
   fetch_state(nc - 1, tid0 & 63);
   if (src) {
     state_io<K, V>(Z, const_cast<float *>(src), false, tid0 & 63);
+    scale(Z, Turn(loc.index * (a.seg / 64) + nc - 1).begins());
   } else {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) Z[kt] = zero16();
@@ -224,8 +225,9 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     const int64_t t0 = loc.t0 + 64 * (int64_t)c;
+    const Turn turn(loc.index * (a.seg / 64) + c);
     FineGates &g = G[wave];
-    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
+    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane, turn.of(lane));
     const bf16 *q = Ql, *k = Kl, *x = Xl[wave], *dy = Dl[wave];
     const int64_t sums = ((int64_t)vs * a.Hv + h) * a.s.tokens + t0;  // of a_part, r_part, m_part
     const float eL = gt.all();
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
 #pragma unroll
       for (int s = 0; s < K / 16; ++s) {
         const Split3 zf = split(Z[s >> 1], s & 1);
-        *reinterpret_cast<bf16x8 *>(w.z(a) + at + s * 512) = zf.hi;
+        *reinterpret_cast<uint4 *>(w.z(a) + at + s * 512) = turn.right(zf.hi);
         xd = dot_halves(sh[s], sl[s], Z[s >> 1], s & 1, xd);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -250,11 +252,11 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
         if (s & 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    const float xo = wave_sum(xd) * eL;
+    const float xo = wave_sum(xd) * (eL * turn.begins());
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int tok = 32 * i + r32;
-      const float v = row_dot(Y[i], x + tok * VP, h2) * g.w1[tok];
+      const float v = row_dot(Y[i], x + tok * VP, h2) * (g.w1[tok] * turn.begins());
       if (h2 == 0 && tok < rows) w.ri_part(a)[sums + tok] = v;
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       const float gj = g.gam[tj], lj = g.rest[tj], dj = g.del[tj];
       const int lim = next_bit(above(jt ? gt.m1 : gt.m0, r32));  // the first token of the half that no longer sees j
       f32x16 T = Y[jt];
-      const float wj = g.w1[tj];
+      const float wj = g.w1[tj] * turn.begins();
 #pragma unroll
       for (int i = 0; i < 16; ++i) T[i] *= wj;
       float ms = 0.f;
@@ -352,14 +354,12 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
     fetch(in, c > 0 ? c - 1 : 0, tid);
     __builtin_amdgcn_sched_barrier(0);
     // Z = 2^{gamma_L} Z + C^T (p dY)
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) Z[kt][i] *= eL;
+    scale(Z, eL);
     const TrA tq(q, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const Split3 y = split_scaled(df[s], &g.p[16 * s + 4 * h2]);
+      if (s == 1) scale(Z, -1.f);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 qf = tq.at(s, kt, KP);
@@ -377,6 +377,7 @@ __global__ __launch_bounds__(64 * NW, 2) void grad_kernel(ScanArgs a, Layout w, 
       __syncthreads();
     }
   }
+  scale(Z, Turn(loc.index * (a.seg / 64)).ends());
   if (dh0) state_io<K, V>(Z, dh0, true, opaque_tid() & 63);
 }
 

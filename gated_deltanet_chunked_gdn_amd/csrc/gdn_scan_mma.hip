@@ -77,7 +77,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
 #pragma unroll
       for (int j = 0; j < KT; ++j)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[j][i] = quiet(S[j][i]);
+        for (int i = 0; i < 16; ++i) S[j][i] = quiet(S[j][i]) * Turn(loc.index * (a.seg / 64)).begins();
     }
   } else {
 #pragma unroll
@@ -115,13 +115,14 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
     commit(r, tid);
   }
   __syncthreads();
-  float total = 0.f;
+  float total = 0.f, ends = 1.f;
   for (int step = 0; step < nc; ++step) {
     const int c = REV ? nc - 1 - step : step;
     const int tid = opaque_tid(), lane = tid & 63, h2 = lane >> 5, r32 = lane & 31;
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
+    const Turn turn(loc.index * (a.seg / 64) + c);
     Gates &g = lds.g[wave];
-    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane);
+    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane, REV ? turn.of(lane) : 1.f, OUT ? 1.f : turn.of(lane));
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
     In in;
     fetch(in, step + 1 < nc ? step + 1 : step, tid);
@@ -140,7 +141,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
 #pragma unroll
       for (int s = 0; s < K / 16; ++s) {
         const SplitHalves x = split_halves(S[s >> 1], s & 1);
-        *reinterpret_cast<bf16x8 *>(w.s_hi(a) + at + s * 512) = x.hi;
+        *reinterpret_cast<uint4 *>(w.s_hi(a) + at + s * 512) = turn.right(x.hi);
         *reinterpret_cast<uint4 *>(w.s_low(a) + at + s * 512) = x.low;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -155,7 +156,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
       float *ai = w.ai_part(a) + ((int64_t)(v0 / 32) * a.Hv + h) * a.s.tokens + t0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float v = acc_dot(U[i], dyv[i]) * g.p[32 * i + r32];
+        const float v = acc_dot(U[i], dyv[i]) * (g.p[32 * i + r32] * turn.begins());
         if (h2 == 0 && 32 * i + r32 < rows) ai[32 * i + r32] = v;
       }
     }
@@ -231,14 +232,12 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
     }
     // S = 2^{gamma_L} S + B^T (w X)
     const float eL = gt.all();
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[kt][i] *= eL;
+    scale(S, eL);
     const TrA tk(k, KP, lane);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const Split3 x = split_scaled(vf[s], (REV ? g.p : g.w) + 16 * s + 4 * h2);
+      if (!OUT && s == 1) scale(S, -1.f);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         const bf16x8 kf = tk.at(s, kt, KP);
@@ -247,6 +246,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
         S[kt] = mma32(kf, x.hi, S[kt]);
       }
     }
+    ends = turn.ends();
     __syncthreads();  // every wave is done with b and c
     commit(in, tid);
     __syncthreads();
@@ -254,6 +254,7 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
   if (MODE == kLocal || REV) {
     if (REV && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;
     float *dst = (REV ? w.zend(a) : w.start(a)) + (slot * a.Hv + h) * kv + v0;
+    scale(S, ends);
     state_io<K, V>(S, dst, true, lane);
     // (in the backward the reverse pass has the decays: one writer)
     if (MODE == kLocal && w.chunks == 0 && lane == 0 && v0 == 0) w.decay(a)[slot * a.Hv + h] = total / kLog2e;

@@ -133,8 +133,39 @@ __device__ __forceinline__ uint32_t upto(uint32_t m, int i) { return m & (0xFFFF
 __device__ __forceinline__ uint32_t above(uint32_t m, int i) { return m & ~(0xFFFFFFFFu >> (31 - i)); }
 __device__ __forceinline__ int last_bit(uint32_t m) { return m ? 31 - __builtin_clz(m) : 0; }
 
+// The bf16 matrix instructions round what lies below their sum's last bit down,
+// not to nearest: of random operands -0.02 to -0.06 of 2^-24 of the summands'
+// sizes an instruction, whatever their sign.  A state that forgets little gathers
+// that for as long as it lives, and <S, Z> over all K V elements: dA came out 1e-6
+// low in every head (2e-7 off, of either sign, as it is).  So the backward's updates of S and Z turn signs over: a
+// chunk's first 16 tokens (where a sum from zero loses most) with one sign, the
+// other 48 with the other, and the chunks of a sequence in turn with either first.
+struct Turn {
+  bool odd;  // chunk, uniform
+  __device__ __forceinline__ Turn(int64_t chunk) : odd(__builtin_amdgcn_readfirstlane((int)chunk) & 1) {}
+  // An odd chunk begins with the state and ends with its negative, an even one the
+  // other way round.
+  __device__ __forceinline__ float begins() const { return odd ? 1.f : -1.f; }
+  __device__ __forceinline__ float ends() const { return odd ? -1.f : 1.f; }
+  // of a token's weight; the state turns over behind the first 16
+  __device__ __forceinline__ float of(int token) const { return odd == (token < 16) ? 1.f : -1.f; }
+  // eight bf16 numbers of the state that the chunk begins with
+  __device__ __forceinline__ uint4 right(const bf16x8 &x) const {
+    const uint32_t m = odd ? 0u : 0x80008000u;
+    const uint4 u = __builtin_bit_cast(uint4, x);
+    return make_uint4(u.x ^ m, u.y ^ m, u.z ^ m, u.w ^ m);
+  }
+};
+template <int KT>
+__device__ __forceinline__ void scale(f32x16 (&S)[KT], float f) {
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[kt][i] *= f;
+}
+
 template <typename G>
-__device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softplus, bool live, int lane) {
+__device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softplus, bool live, int lane, float psign = 1.f, float wsign = 1.f) {
   const float d = live ? (softplus ? softplusf(z) : z) : 0.f;
   const float g = d * A2;
   const bool cut = g < kForget;
@@ -150,10 +181,10 @@ __device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softpl
   if constexpr (fine) s.rest[lane] = rest;
   s.del[lane] = d;
   const uint32_t before = upto(lane < 32 ? t.m0 : t.m1, i) | (lane < 32 ? 0u : t.m0);
-  s.p[lane] = before ? 0.f : exp2_hw(lane < 32 ? gam + rest : (h0 + gam) + (r0 + rest));
+  s.p[lane] = before ? 0.f : psign * exp2_hw(lane < 32 ? gam + rest : (h0 + gam) + (r0 + rest));
   const float w1 = later | (lane < 32 ? t.m1 : 0u) ? 0.f : exp2_hw(lane < 32 ? ((h0 - gam) + h1) + ((r0 - rest) + r1) : (h1 - gam) + (r1 - rest));
   s.w1[lane] = w1;
-  if constexpr (!fine) s.w[lane] = w1 * d;
+  if constexpr (!fine) s.w[lane] = w1 * d * wsign;
   if (lane < 32) {
     const float u1 = later ? 0.f : exp2_hw((h0 - gam) + (r0 - rest));
     s.u1[lane] = u1;

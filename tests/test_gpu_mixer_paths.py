@@ -528,3 +528,27 @@ def test_scan_gate_sums_of_a_few_tokens(gdn, dtype, T, K, V):  # noqa: F811
     got = gdn.selective_scan_bwd(i["c"], i["b"], i["x"], i["dt"], i["A"], i["dy"], dt_softplus=False)[4]
     off, most = (d64(got) - want).abs(), 2.0 ** -20 * (size / (K * V)).sqrt()
     assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
+
+
+@pytest.mark.parametrize("dtype,K,V", [("bf16", 128, 64), ("bf16", 64, 64), ("f32", 64, 64)])
+def test_scan_gate_sums_of_long_memory(gdn, dtype, K, V):  # noqa: F811
+    """dA of tokens that forget little, with the operands that a SiLU leaves (of positive mean): a rounding to one side
+    in the states' sums would add up over the tokens that it lives for and over the K V elements of <S, Z>.  A state
+    carries roundings of a few 2^-24 of itself, for as long as it lives, so that dA's terms are off together, and all
+    by 2^-22 of their sizes at the most."""
+    announce(f"gate sums of long memory {dtype} {K} {V}")
+    T, Hv = 2048, 8
+    i = inputs(dtype, 1, T, 1, Hv, K, V, state=False, seed=94)
+    g = gen(95)
+    for k in ("c", "b", "x"):
+        i[k] = torch.nn.functional.silu(i[k].float()).to(DT[dtype])
+    i["A"], i["bias"], i["softplus"] = -torch.ones(Hv, device="cuda"), None, False
+    step = torch.logspace(-3, -2, Hv) * torch.exp(0.5 * torch.randn(1, T, Hv, generator=g))
+    i["dt"] = step.to(DT[dtype]).cuda()
+    leaves = [d64(i[k]) for k in ("c", "b", "x", "dt", "A")]
+    A = leaves[4].expand(1, T, Hv).clone().requires_grad_()
+    y, _ = scan64(None, *leaves[:4], A, None, None, None, False)
+    terms, = torch.autograd.grad((y * d64(i["dy"])).sum(), [A])
+    got = gdn.selective_scan_bwd(*[i[k] for k in ("c", "b", "x", "dt", "A")], i["dy"], dt_softplus=False)[4]
+    off, most = (d64(got) - terms.sum((0, 1))).abs(), 2.0 ** -22 * terms.abs().sum((0, 1))
+    assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
