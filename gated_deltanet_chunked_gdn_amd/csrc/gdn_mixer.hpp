@@ -91,20 +91,26 @@ struct Raw {
   }
 } __attribute__((aligned(sizeof(E) * VEC)));
 
-// 1 / (1 + exp(-z)): v_exp_f32 and v_rcp_f32 (each within an ulp or so); 0 and
-// 1 at the ends, since exp(-z) runs to infinity and to 0.
+// 1 / (1 + exp(-z)): v_exp_f32 of a rounded -z log2(e) (off by |z| 2^-24) and
+// v_rcp_f32; 0 and 1 at the ends, since exp(-z) runs to infinity and to 0.
 __device__ __forceinline__ float sigmoidf(float z) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
 // log(1 + exp(z)) = max(z, 0) + log1p(t), t = exp(-|z|): finite for every finite
 // z and right to fp32's relative accuracy where it is small (the step sizes of
-// a state-space layer begin at 0.001).  log1p(t) = t log(u) / (u - 1) with u =
-// 1 + t as rounded: the rounding of u cancels in the quotient (Kahan's form of
-// log1p), where log(u) alone would lose t's last digits.
+// a state-space layer begin at 0.001): an exponential of full accuracy, and
+// log1p(t) = 2 artanh(s), s = t / (2 + t) <= 1/3, as its power series (nine
+// terms leave 1e-10).  The hardware's exponential and logarithm left 7e-7 at
+// 0.001, all of one sign.
 __device__ __forceinline__ float softplusf(float z) {
-  const float t = __expf(-fabsf(z)), u = 1.f + t;
-  const float l = u == 1.f ? t : t * (__logf(u) * __builtin_amdgcn_rcpf(u - 1.f));
-  return fmaxf(z, 0.f) + l;
+  const float t = expf(-fabsf(z)), d = 2.f + t;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = r * (2.f - d * r);
+  const float s = t * r, q = s * s;
+  float p = 1.f / 17.f;
+#pragma unroll
+  for (int n = 15; n >= 3; n -= 2) p = p * q + 1.f / (float)n;
+  return fmaxf(z, 0.f) + 2.f * (s + s * q * p);
 }
 
 // a weight held in the problem's type or in fp32

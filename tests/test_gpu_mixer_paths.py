@@ -552,3 +552,31 @@ def test_scan_gate_sums_of_long_memory(gdn, dtype, K, V):  # noqa: F811
     got = gdn.selective_scan_bwd(*[i[k] for k in ("c", "b", "x", "dt", "A")], i["dy"], dt_softplus=False)[4]
     off, most = (d64(got) - terms.sum((0, 1))).abs(), 2.0 ** -22 * terms.abs().sum((0, 1))
     assert bool((off <= most).all()), f"dA: {(off / most).tolist()} of the bound"
+
+
+# ---------------------------------------------------------------- the step sizes
+
+
+@pytest.mark.parametrize("lo,hi", [(-85, -30), (-30, -12), (-12, -6), (-6, -2), (-2, 2), (2, 60)])
+def test_softplus_is_exact_to_a_few_steps_of_fp32(gdn, lo, hi):  # noqa: F811
+    """delta = softplus(dt) as a step leaves it in a zero state (b = x = 1).  An exponential within an ulp (two half
+    steps) and a few roundings of a half step each behind it: 8 half steps, 2^-21, at the most.  (dt of -7 is a step
+    of 0.001, where such layers begin.)"""
+    Hv, B = 64, 512
+    z = (lo + (hi - lo) * torch.rand(B, Hv, generator=gen(96))).cuda()
+    st = torch.zeros(B, Hv, 32, 32, device="cuda")
+    one = torch.ones(B, 1, 32, device="cuda")
+    gdn.selective_scan_step(one, one, torch.ones(B, Hv, 32, device="cuda"), z, torch.zeros(Hv, device="cuda"), st)
+    want = torch.clamp(z.double(), min=0) + torch.log1p(torch.exp(-z.double().abs()))
+    off = ((st[:, :, 0, 0].double() - want) / want).abs().max()
+    assert bool(off <= 2.0 ** -21), float(off)
+    for dtype in (torch.float32, torch.bfloat16):  # the prompts' forms
+        dt = z.view(B, 1, Hv).to(dtype)
+        e = torch.ones(B, 1, 1, 32, device="cuda", dtype=dt.dtype)
+        _, ht = gdn.selective_scan_fwd(e, e, torch.ones(B, 1, Hv, 32, device="cuda", dtype=dt.dtype), dt, torch.zeros(Hv, device="cuda"))
+        want = torch.clamp(dt.double(), min=0) + torch.log1p(torch.exp(-dt.double().abs()))
+        # (bf16: delta x enters the products as three bf16 numbers, and a part below 2^-126, which is no normal number,
+        # counts as 0 there: the second and the third may be missing, at most 2^-126 each)
+        tiny = 2.0 ** -125 if dtype == torch.bfloat16 else 0.0
+        off, most = (ht[:, :, 0, 0].double() - want[:, 0]).abs(), 2.0 ** -21 * want[:, 0] + tiny
+        assert bool((off <= most).all()), float((off / most).max())
