@@ -7,9 +7,10 @@
 // All of it moves data far longer than it computes: x and y once (the
 // backward: x, dy and dx), so each kernel is one pass with the window in
 // registers.  16384 tokens x 8192 channels in bf16 forward: 108 us, 5.0 TB/s
-// (a large copy here: 5.4); 2 x 4096 x 8192 backward with the sums: 105 us,
-// 3.8 TB/s (three streams, half the waves by registers).  A token's step is a
-// launch: 9 us a call at 32 x 8192.
+// (a large copy here: 5.4); 2 x 4096 x 8192 backward with the sums: 106 to 114
+// us a call by what ran before it (118 + 5 in a kernel trace), 3.3 to 3.8 TB/s
+// (three streams, half the waves by registers).  A token's step is a launch: 9 us
+// a call at 32 x 8192.
 #include <initializer_list>
 
 #include "gdn_internal.h"
@@ -451,8 +452,8 @@ int64_t conv_bwd_tiles(int64_t tokens, int D) {
 }
 
 // Whole sequences: four channels a thread (8 bytes in bf16).  Eight, 16 bytes,
-// leave 3 waves a SIMD (backward: 1) and cost 129 us against 122 (backward
-// 130 against 123) at 16384 x 8192 (2 x 4096 x 8192).
+// leave 3 waves a SIMD (backward: 1) and are 6 % slower in both directions at
+// 16384 x 8192 (2 x 4096 x 8192), both timed in turn.
 static bool wide4(const ConvArgs &a, std::initializer_list<const void *> rows) {
   const uintptr_t mask = a.dtype == 1 ? 7 : 15;
   for (const void *p : rows)

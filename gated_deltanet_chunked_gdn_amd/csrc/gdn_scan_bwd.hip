@@ -38,10 +38,11 @@
 // states 3e-5 off; <S, Z> carried along over two chunks, ddt_bias 3e-5.)
 // dx, dc and db are bf16 themselves and take their operands rounded.
 //
-// 2 x 4096 tokens x 64 heads, K 128, V 64: passes from zero 78 us, carries 17,
-// states 112, grad_kernel 176, pair_kernel 129, gates 26.  S and Z of every
-// chunk, 0.8 GB written and read again, are what the middle three move beside
-// the tensors, at 3.3 to 3.6 TB/s.
+// 2 x 4096 tokens x 64 heads, K 128, V 64: passes from zero 78 us, carries 24,
+// states 119, grad_kernel 194, pair_kernel 130, gates 24 (of which the exactness
+// of the gates' sums takes 7 in the states and 20 in grad_kernel).  S and Z of
+// every chunk, 0.8 GB written and read again, are what the middle three move
+// beside the tensors, at 3.0 to 3.5 TB/s.
 #include "gdn_internal.h"
 #include "gdn_scan_mma.hpp"
 

@@ -11,9 +11,9 @@
 // their way while one is worked on.  (One wave a SIMD with 64 columns: 171 us
 // for the out pass at 8192 tokens x 64 heads, K 128, V 64, the state in
 // accumulation registers that vector instructions reach only by moves; this
-// form 68 us, and 73 with the exact state updates below.)  The pass from zero
-// takes 41 us there: both are bound by latency, one workgroup a compute unit
-// going in step from barrier to barrier.
+// form 68 us, and 75 with the exact state updates below.)  The pass from zero
+// takes 42 us there.  Both have one workgroup a compute unit, whose waves go in
+// step from barrier to barrier.
 //
 // Everything is arranged so that accumulators are operands without moving
 // (gdn_slice.hpp): S tiles (rows k, lane v) give S^T for c; C B^T is formed
@@ -226,7 +226,9 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
           buf_store16(make_uint4(p[0], r[0], p[1], r[1]), yr,
                       row < rows ? (uint32_t)(row * ys * 2 + (8 * b + 8 * h2) * 2) : kOutside);
         }
-        // (the second half's reads, moved up into the first, would spill)
+        // (the second half's reads, moved up into the first, would spill in every
+        // form; as it is, two-wave workgroups with K = 128 spill 36 registers, and
+        // <64, 64> with one wave 4)
         __builtin_amdgcn_sched_barrier(0);
       }
     }

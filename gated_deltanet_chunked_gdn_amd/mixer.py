@@ -318,8 +318,9 @@ def selective_scan_fwd(c, b, x, dt, A, D=None, dt_bias=None, dt_softplus: bool =
     dt_softplus): S_t = exp(delta_t A) S_{t-1} + delta_t b_t x_t^T and
     y_t = S_t^T c_t + D x_t.  c, b [B, T, Hq, K] (read by v-head h at head
     h // (Hv // Hq)), x [B, T, Hv, V], dt [B, T, Hv] in one dtype; A, D,
-    dt_bias float32 [Hv]; states float32 [N, Hv, K, V].  The token rows of c,
-    b and x may be slices of a wider tensor.  A state that grows (A > 0) is
+    dt_bias float32 [Hv]; states float32 [N, Hv, K, V]; K, V in {32, 64, 128}
+    in bfloat16, {32, 64} in float32 (the step: all three).  The token rows of
+    c, b and x may be slices of a wider tensor.  A state that grows (A > 0) is
     computed as it is, up to what float32 holds.  A NaN or an infinity in a
     token reaches the tokens of its 64-token chunk, earlier ones too, and all
     later ones of its sequence; no other sequence."""

@@ -234,7 +234,7 @@ int gdn_causal_conv_step(const gdn_conv_t *p, const void *x, void *state, const 
  * multiples of 16 bytes and (but for the step) below 2^24 elements.
  * Held in fp32: delta, the decays, the states, the gates' gradients and every
  * sum over tokens.  In bf16 problems the products inside a 64-token chunk and
- * the state as an operand of y, dc and db are rounded to bf16.  A NaN or an
+ * the state and its gradient as operands of y, dc and db are rounded to bf16.  A NaN or an
  * infinity in a token's inputs reaches the other tokens of its chunk, earlier
  * ones too, and all later ones of its sequence; never another sequence. */
 typedef struct {

@@ -580,3 +580,38 @@ def test_softplus_is_exact_to_a_few_steps_of_fp32(gdn, lo, hi):  # noqa: F811
         tiny = 2.0 ** -125 if dtype == torch.bfloat16 else 0.0
         off, most = (ht[:, :, 0, 0].double() - want[:, 0]).abs(), 2.0 ** -21 * want[:, 0] + tiny
         assert bool((off <= most).all()), float((off / most).max())
+
+
+# ---------------------------------------------------------------- again, and in graphs
+
+
+@pytest.mark.parametrize("dtype,T", [("f32", 400), ("bf16", 700)])
+def test_scan_replayed_from_two_graphs_gives_the_eager_bits(gdn, dtype, T):  # noqa: F811
+    """Both directions over segments that a carry joins, on two sets of inputs, replayed in turn with eager calls
+    between (each graph has its own workspace)."""
+    lens = [T, 0, 1, T // 3]
+    cu = cu_of(lens).cuda()
+
+    def call(seed):
+        i = inputs(dtype, 1, 0, 2, 4, 64, 64, lens=lens, seed=seed)
+        kw = dict(D=i["D"], dt_bias=i["bias"], initial_state=i["h0"], cu_seqlens=cu, check_cu_seqlens=False)
+        ins = [i[k] for k in ("c", "b", "x", "dt", "A")]
+        return lambda: gdn.selective_scan_fwd(*ins, **kw) + gdn.selective_scan_bwd(*ins, i["dy"], dht=i["dht"], **kw)
+
+    runs = [call(98), call(99)]
+    want = [f() for f in runs]
+    torch.cuda.synchronize()
+    graphs = []
+    for f in runs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs = f()
+        graphs.append((gr, outs))
+    for _ in range(4):
+        for (gr, outs), w in zip(graphs, want):
+            for t in outs:
+                t.zero_()
+            gr.replay()
+            eager = runs[0]()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, r) for a, r in zip(outs, w)) and all(torch.equal(a, r) for a, r in zip(eager, want[0]))
