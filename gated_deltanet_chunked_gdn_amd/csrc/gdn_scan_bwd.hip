@@ -19,11 +19,11 @@
 //   d delta_t = r_t + z_t + m_t + A dg_t
 //
 // The pass that forms the states (kStates, gdn_scan_mma.hip) also has a_i.  Two
-// kernels share the rest.  grad_kernel walks a
-// segment's chunks from its end with Z in accumulators (32 columns of a head a
-// wave, as the forward): dx, the gates' sums, and Z of every chunk, rounded to
-// bf16, for the other.  pair_kernel has dc and db: one chunk of one head group
-// a workgroup, the heads in turn, so that their sums stay in registers.
+// kernels share the rest.  grad_kernel walks a segment's chunks from its end with
+// Z in accumulators (32 columns of a head a wave, as the forward): dx, the gates'
+// sums, and Z of every chunk, rounded to bf16, for the other.  pair_kernel has dc
+// and db: one chunk of one head group a workgroup, the heads in turn, so that
+// their sums stay in registers.
 //
 // The gates' sums reach dA and ddt_bias, fp32 sums over all tokens, so what
 // enters them is held to fp32: the recurrences of S and Z, S and Z as
@@ -600,8 +600,8 @@ __global__ __launch_bounds__(512, 2) void pair_kernel(ScanArgs a, Layout w) {
 
 // Tokens of `width` in a row, tok = rows - 1 - lane, and the pairs from two such
 // neighbours: for t in the second, the sum of v over its tokens from t on (a_i);
-// in the first, over its tokens before t (delta_j r_j).  (The
-// terms are 0 where a token between i and j forgets all.)
+// in the first, over its tokens before t (delta_j r_j).  (The terms are 0 where a
+// token between i and j forgets all.)
 __device__ __forceinline__ double outer_sum(double v, int tok, int lane, int width) {
   const bool second = tok & width;
   const double prior = __shfl_down(v, 1);

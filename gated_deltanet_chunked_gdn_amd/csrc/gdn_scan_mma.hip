@@ -36,7 +36,7 @@ namespace {
 //   kLocal   the segment's last state from zero and its decay (for carry_kernel)
 //   kOut     y, from the segment's start state, and the sequence's last state
 //   kStates  the state entering every chunk, as bf16 and what fp32 has below
-//            it, and the part of a_i that comes from it, p_i c_i . S dy_i (backward)
+//            it, and a_i = p_i c_i . S dy_i (backward)
 //   kRLocal  reverse: the gradient of the segment's first state from its own
 //            outputs; a.b, a.x hold c and dy: Z = 2^{gamma_L} Z + C^T (2^{gamma} dY)
 enum { kLocal, kOut, kStates, kRLocal };
@@ -122,7 +122,8 @@ __device__ __forceinline__ void chunks(const ScanArgs &a, const Layout &w, int b
     const int rows = nt - 64 * c < 64 ? nt - 64 * c : 64;
     const Turn turn(loc.index * (a.seg / 64) + c);
     Gates &g = lds.g[wave];
-    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane, REV ? turn.of(lane) : 1.f, OUT ? 1.f : turn.of(lane));
+    const GateTotals gt = gates(g, z + bias, A2, a.softplus, lane < rows, lane, REV ? turn.of(lane) : 1.f,
+                                OUT ? 1.f : turn.of(lane));
     total += gt.m0 | gt.m1 ? -INFINITY : gt.t0 + gt.t1;
     In in;
     fetch(in, step + 1 < nc ? step + 1 : step, tid);

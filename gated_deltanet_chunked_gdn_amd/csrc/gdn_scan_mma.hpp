@@ -137,9 +137,10 @@ __device__ __forceinline__ int last_bit(uint32_t m) { return m ? 31 - __builtin_
 // not to nearest: of random operands -0.02 to -0.06 of 2^-24 of the summands'
 // sizes an instruction, whatever their sign.  A state that forgets little gathers
 // that for as long as it lives, and <S, Z> over all K V elements: dA came out 1e-6
-// low in every head (2e-7 off, of either sign, as it is).  So the backward's updates of S and Z turn signs over: a
+// low in every head.  So the backward's updates of S and Z turn signs over: a
 // chunk's first 16 tokens (where a sum from zero loses most) with one sign, the
-// other 48 with the other, and the chunks of a sequence in turn with either first.
+// other 48 with the other, and the chunks of a sequence in turn with either first
+// (dA 2e-7 off, of either sign, for 5 % of the reverse pass).
 struct Turn {
   bool odd;  // chunk, uniform
   __device__ __forceinline__ Turn(int64_t chunk) : odd(__builtin_amdgcn_readfirstlane((int)chunk) & 1) {}
@@ -147,7 +148,7 @@ struct Turn {
   // other way round.
   __device__ __forceinline__ float begins() const { return odd ? 1.f : -1.f; }
   __device__ __forceinline__ float ends() const { return odd ? -1.f : 1.f; }
-  // of a token's weight; the state turns over behind the first 16
+  // of a token's weight (p or w of its gates); the state turns over behind the first 16
   __device__ __forceinline__ float of(int token) const { return odd == (token < 16) ? 1.f : -1.f; }
   // eight bf16 numbers of the state that the chunk begins with
   __device__ __forceinline__ uint4 right(const bf16x8 &x) const {
@@ -165,7 +166,8 @@ __device__ __forceinline__ void scale(f32x16 (&S)[KT], float f) {
 }
 
 template <typename G>
-__device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softplus, bool live, int lane, float psign = 1.f, float wsign = 1.f) {
+__device__ __forceinline__ GateTotals gates(G &s, float z, float A2, bool softplus, bool live, int lane, float psign = 1.f,
+                                                  float wsign = 1.f) {
   const float d = live ? (softplus ? softplusf(z) : z) : 0.f;
   const float g = d * A2;
   const bool cut = g < kForget;
