@@ -8,7 +8,7 @@
 // backward: x, dy and dx), so each kernel is one pass with the window in
 // registers.  16384 tokens x 8192 channels in bf16 forward: 108 us, 5.0 TB/s
 // (a large copy here: 5.4); 2 x 4096 x 8192 backward with the sums: 106 to 114
-// us a call by what ran before it (118 + 5 in a kernel trace), 3.3 to 3.8 TB/s
+// us a call by what ran before it (114 to 119 + 5 in kernel traces), 3.3 to 3.8 TB/s
 // (three streams, half the waves by registers).  A token's step is a launch: 9 us
 // a call at 32 x 8192.
 #include <initializer_list>
