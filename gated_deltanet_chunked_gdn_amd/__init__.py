@@ -333,5 +333,5 @@ def chunk_gated_delta_rule_bwd(q, k, v, g, beta, A, do, dht=None, scale=None,
 
 
 from .mixer import (  # noqa: E402  (needs the names above)
-    causal_conv_bwd, causal_conv_fwd, causal_conv_step, gated_delta_rule_step, layer_norm_bwd, layer_norm_fwd,
-    selective_scan_bwd, selective_scan_fwd, selective_scan_step)
+    causal_conv_bwd, causal_conv_fwd, causal_conv_step, gated_delta_rule_step, group_norm_bwd, group_norm_fwd, layer_norm_bwd,
+    layer_norm_fwd, linear_attention_bwd, linear_attention_fwd, linear_attention_step, selective_scan_bwd, selective_scan_fwd, selective_scan_step)

@@ -1,0 +1,384 @@
+// Linear attention with a decay for each head (gdn_linear.hpp has the
+// formulas): the passes in fp32 matrix instructions, and what joins segments
+// and heads.
+//
+// A workgroup has a segment of one head and 32 of the state's columns; chunks
+// of 32 tokens.  The state is in accumulators and, for the chunk that reads
+// it, in LDS.
+#include "gdn_internal.h"
+#include "gdn_linear.hpp"
+
+namespace gdn {
+namespace attn {
+namespace {
+
+constexpr int C = 32;        // tokens a chunk
+constexpr int kAhead = 8;    // segments whose states a carry has in flight
+constexpr int kThreads = 256;
+
+// What a launch does: the state a segment adds (forwards; or forwards and
+// backwards, for the backward), o, or the three gradients.
+enum { kLocal, kLocals, kForward, kGrads };
+
+template <int D>
+struct Lds {
+  static constexpr int P = D + 4;  // row pitches: a column of 16 rows meets every bank once
+  float a[C * P], b[C * P], c[C * 36], p[C * 36], s[32 * P], pw[C + 1];
+};
+
+// A chunk's rows of COLS columns in the registers of a workgroup; rows past
+// its end are zeros.
+template <typename E, int COLS>
+struct Rows {
+  static constexpr int PER = 16 / (int)sizeof(E), PIECES = C * COLS / PER, N = (PIECES + kThreads - 1) / kThreads;
+  uint4 r[N];
+  __device__ __forceinline__ void load(const E *p, int64_t stride, int rows, int tid) {
+    const uint32_t bytes = rows > 0 ? (uint32_t)(((rows - 1) * stride + COLS) * sizeof(E)) : 0u;
+    const auto rsrc = raw_buffer(p, bytes);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = tid + i * kThreads, row = pc / (COLS / PER), col = pc % (COLS / PER);
+      r[i] = buf_load16(rsrc, row < rows ? (uint32_t)(row * stride * sizeof(E) + col * 16) : 0xFFFFFFF0u);
+    }
+  }
+  __device__ __forceinline__ void store(float *lds, int pitch, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = tid + i * kThreads, row = pc / (COLS / PER), col = pc % (COLS / PER);
+      if (PIECES % kThreads != 0 && pc >= PIECES) continue;
+      const E *e = reinterpret_cast<const E *>(&r[i]);
+#pragma unroll
+      for (int j = 0; j < PER; j += 4)
+        *reinterpret_cast<f32x4 *>(lds + row * pitch + col * PER + j) =
+            f32x4{to_f32(e[j]), to_f32(e[j + 1]), to_f32(e[j + 2]), to_f32(e[j + 3])};
+    }
+  }
+};
+
+__device__ __forceinline__ f32x4 prod(const f32x4 &x, const f32x4 &y, f32x4 c) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c = Mma<float>::mma(x[k], y[k], c);
+  return c;
+}
+
+// DA: width of a and b, DC: of c and the output, of which the workgroup has
+// 32 columns from c0.
+template <typename E, int DA, int DC, bool OUT>
+__device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const SlotLoc &loc, float *state, int h, int c0, Lds<DA> &lds) {
+  constexpr int P = Lds<DA>::P, KT = DA / 32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), l16 = lane & 15, q = lane >> 4;
+  const float g2 = log2_decay(args.g[h]);
+  if (tid <= C) lds.pw[tid] = power(g2, tid);
+
+  // this wave's tiles of the state: rows 16 kt + 4 q + e of column 16 ct + l16
+  auto kt = [&](int i) { return (wave + 4 * i) >> 1; };
+  const int ct = wave & 1;
+  auto state_io = [&](f32x4(&S)[KT], float *ptr, bool store) {
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      const int r = 16 * kt(i) + 4 * q, c = c0 + 16 * ct + l16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float *at = ptr + (p.tr ? (int64_t)c * DA + r + e : (int64_t)(r + e) * DC + c);
+        if (store)
+          *at = S[i][e];
+        else
+          S[i][e] = *at;
+      }
+    }
+  };
+  f32x4 S[KT];
+  if (OUT && p.start) {
+    state_io(S, const_cast<float *>(p.start), false);
+  } else {
+#pragma unroll
+    for (int i = 0; i < KT; ++i) S[i] = zero4();
+  }
+  const int nt = (int)(loc.t1 - loc.t0), nc = (nt + C - 1) / C;
+  struct In {
+    Rows<E, DA> a, b;
+    Rows<E, 32> c;
+  };
+  auto fetch = [&](In &r, int step) {
+    const int ch = p.rev ? nc - 1 - step : step;
+    const int64_t t = loc.t0 + (int64_t)C * ch;
+    const int rows = nt - C * ch < C ? nt - C * ch : C;
+    if (OUT) r.a.load(static_cast<const E *>(p.a) + t * p.as, p.as, rows, tid);
+    r.b.load(static_cast<const E *>(p.b) + t * p.bs, p.bs, rows, tid);
+    r.c.load(static_cast<const E *>(p.c) + t * p.cs + c0, p.cs, rows, tid);
+  };
+  // (what multiplies into the state lies with a's columns in o and dv: the rows
+  // b of o and dq, a of dk and dv, whose tokens run backwards)
+  In in;
+  if (nc > 0) fetch(in, 0);
+  for (int step = 0; step < nc; ++step) {
+    const int ch = p.rev ? nc - 1 - step : step;
+    const int n = nt - C * ch < C ? nt - C * ch : C;
+    __syncthreads();  // the chunk before is done with LDS
+    if (OUT) in.a.store(lds.a, P, tid);
+    in.b.store(lds.b, P, tid);
+    in.c.store(lds.c, 36, tid);
+    if (OUT) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+        *reinterpret_cast<f32x4 *>(lds.s + (16 * ct + l16) * P + 16 * kt(i) + 4 * q) = S[i];
+    }
+    __syncthreads();
+    if (step + 1 < nc) fetch(in, step + 1);
+    // decays of the token from the state before the chunk, and from it to the state behind
+    auto w_in = [&](int i) { return p.rev ? lds.pw[n - 1 - i > 0 ? n - 1 - i : 0] : lds.pw[i + 1]; };
+    auto w_up = [&](int j) { return p.rev ? lds.pw[j + 1] : lds.pw[n - 1 - j > 0 ? n - 1 - j : 0]; };
+    f32x4 O = zero4();
+    const int it = wave >> 1, jt = wave & 1;
+    if (OUT) {
+      // a wave's 16 x 16 of the pairs, and of the state's share of the output
+      f32x4 pair = zero4();
+#pragma unroll
+      for (int s = 0; s < DA / 16; ++s) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(lds.a + (16 * it + l16) * P + 16 * s + 4 * q);
+        const f32x4 y = *reinterpret_cast<const f32x4 *>(lds.b + (16 * jt + l16) * P + 16 * s + 4 * q);
+        const f32x4 z = *reinterpret_cast<const f32x4 *>(lds.s + (16 * jt + l16) * P + 16 * s + 4 * q);
+        pair = prod(x, y, pair);
+        O = prod(x, z, O);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * it + 4 * q + e, d = p.rev ? 16 * jt + l16 - i : i - (16 * jt + l16);
+        lds.p[i * 36 + 16 * jt + l16] = d >= 0 ? pair[e] * (lds.pw[d >= 0 ? d : 0] * p.scale_p) : 0.f;
+        O[e] *= w_in(i) * p.scale_in;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < C / 16; ++s) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(lds.p + (16 * it + l16) * 36 + 16 * s + 4 * q);
+        f32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = lds.c[(16 * s + 4 * q + e) * 36 + 16 * jt + l16];
+        O = prod(x, y, O);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * it + 4 * q + e;
+        const int64_t at = (loc.t0 + (int64_t)C * ch + i) * p.os + c0 + 16 * jt + l16;
+        if (i >= n) continue;
+        if (p.part)
+          static_cast<float *>(p.out)[at] = O[e];
+        else
+          static_cast<E *>(p.out)[at] = from_f32<E>(O[e]);
+      }
+    }
+    // S = l^n S + sum_j u_j b_j c_j^T
+    const float all = lds.pw[n];
+    f32x4 cw[C / 16];
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * s + 4 * q + e;
+        cw[s][e] = lds.c[j * 36 + 16 * ct + l16] * (w_up(j) * p.scale_up);
+      }
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[i][e] *= all;
+#pragma unroll
+      for (int s = 0; s < C / 16; ++s) {
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = lds.b[(16 * s + 4 * q + e) * P + 16 * kt(i) + l16];
+        S[i] = prod(x, cw[s], S[i]);
+      }
+    }
+  }
+  if (!OUT)
+    state_io(S, state, true);
+  else if (p.last)
+    state_io(S, p.last, true);
+}
+
+template <typename E, int K, int V, int WHAT>
+__global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, int64_t per) {
+  constexpr int D = K > V ? K : V;
+  __shared__ __align__(16) char mem[sizeof(Lds<(WHAT == kGrads ? D : K)>)];
+  const int64_t part = blockIdx.x / per, item = blockIdx.x % per;
+  int kind = kO;
+  if (WHAT == kLocals) kind = part ? kDv : kO;
+  int64_t unit = item;  // (slot, head, 32 columns)
+  if (WHAT == kGrads) kind = part == 0 ? kDv : part == 1 ? kDk : kDq;
+  const bool tr = WHAT == kGrads && kind != kDv;
+  const int slices = (tr ? K : V) / 32;
+  const int64_t head = unit / slices;
+  const int c0 = (int)(unit % slices) * 32, h = (int)(head % a.Hv);
+  const int64_t slot = head / a.Hv;
+  if (slot >= a.slots) return;
+  const SlotLoc loc = locate(a.s, a.seg, slot);
+  if (!loc.used) return;
+  Pass p = make_pass<E>(a, w, kind, loc, slot, h);
+  if constexpr (WHAT == kLocal || WHAT == kLocals) {
+    if (p.rev ? loc.index == 0 : loc.last) return;
+    // the state is built of b and c
+    float *dst = (p.rev ? w.zend(a) : w.start(a)) + (slot * a.Hv + h) * (int64_t)K * V;
+    sweep<E, K, V, false>(a, p, loc, dst, h, c0, *reinterpret_cast<Lds<K> *>(mem));
+  } else if constexpr (WHAT == kForward) {
+    sweep<E, K, V, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<K> *>(mem));
+  } else {
+    if (tr)
+      sweep<E, V, K, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<V> *>(mem));
+    else
+      sweep<E, K, V, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<K> *>(mem));
+  }
+}
+
+// The segments of a sequence in order, 4 elements of the state a thread: each
+// slot gets the state that its segment begins with.
+template <bool REV>
+__device__ __forceinline__ void carry(const AttnArgs &a, const Layout &w, int64_t i) {
+  const int64_t kv4 = (int64_t)a.K * a.V / 4, heads = i / kv4;
+  if (heads >= (int64_t)a.s.N * a.Hv) return;
+  const int h = (int)(heads % a.Hv), n = (int)(heads / a.Hv);
+  const Span sp = seq_span(a.s, n);
+  const int64_t ns = segs_of(sp, a.seg), step = a.Hv * kv4;
+  f32x4 *at = reinterpret_cast<f32x4 *>(REV ? w.zend(a) : w.start(a)) + (first_slot(a.s, sp, n, a.seg) * a.Hv + h) * kv4 + i % kv4;
+  const f32x4 *given = reinterpret_cast<const f32x4 *>(REV ? a.dht : a.h0);
+  f32x4 cur = given ? given[i] : zero4();
+  const float g2 = log2_decay(a.g[h]), whole = power(g2, a.seg);
+  const float rest = REV ? power(g2, (int)(sp.end - sp.first - (ns - 1) * a.seg)) : whole;  // of the sequence's last segment
+  for (int64_t s0 = 0; s0 < ns; s0 += kAhead) {
+    f32x4 add[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      // (the last one's own part is not wanted)
+      const int64_t s = s0 + j < ns - 1 ? s0 + j : -1;
+      add[j] = s >= 0 ? at[(REV ? ns - 1 - s : s) * step] : zero4();
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t s = s0 + j;
+      if (s >= ns) break;
+      at[(REV ? ns - 1 - s : s) * step] = cur;
+      const float d = REV && s == 0 ? rest : whole;
+      cur = cur * d + add[j];
+    }
+  }
+}
+__global__ __launch_bounds__(256) void carry_kernel(AttnArgs a, Layout w, int64_t blocks) {
+  const int64_t b = blockIdx.x;
+  if (b < blocks)
+    carry<false>(a, w, b * 256 + threadIdx.x);
+  else
+    carry<true>(a, w, (b - blocks) * 256 + threadIdx.x);
+}
+
+// dq, dk of a q-head: the sum over its v-heads, 4 elements a thread.  (Tokens
+// that no sequence has have no parts, and their rows are not the kernel's.)
+template <typename E>
+__global__ __launch_bounds__(256) void group_kernel(AttnArgs a, Layout w) {
+  const int64_t k4 = a.K / 4, n = a.s.tokens * a.Hq * k4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int R = a.Hv / a.Hq;
+  const int64_t e = i % k4, th = i / k4;  // th = token * Hq + hq
+  if (a.s.cu) {
+    const int64_t t = th / a.Hq;
+    const Span sp = seq_span(a.s, seq_of(a.s, t));
+    if (t < sp.first || t >= sp.end) return;
+  }
+  const f32x4 *pq = reinterpret_cast<const f32x4 *>(w.dq_part(a)) + th * R * k4 + e;
+  const f32x4 *pk = reinterpret_cast<const f32x4 *>(w.dk_part(a)) + th * R * k4 + e;
+  f32x4 q = zero4(), k = zero4();
+  for (int r = 0; r < R; ++r) {
+    q += pq[r * k4];
+    k += pk[r * k4];
+  }
+  st4(static_cast<E *>(a.dq) + 4 * i, q[0], q[1], q[2], q[3]);
+  st4(static_cast<E *>(a.dk) + 4 * i, k[0], k[1], k[2], k[3]);
+}
+
+template <typename E, int K, int V, int WHAT>
+hipError_t go(const AttnArgs &a, const Layout &w, hipStream_t st) {
+  const int most = WHAT == kGrads && K > V ? K : V;
+  const int64_t per = a.slots * a.Hv * (most / 32);
+  const int parts = WHAT == kGrads ? 3 : WHAT == kLocals ? 2 : 1;
+  KernelTimer kt(WHAT == kGrads ? "attn_grads" : WHAT == kForward ? "attn_out" : "attn_local", st);
+  pass_kernel<E, K, V, WHAT><<<(unsigned)(per * parts), kThreads, 0, st>>>(a, w, per);
+  return hipGetLastError();
+}
+template <typename E, int WHAT>
+hipError_t pick(const AttnArgs &a, const Layout &w, hipStream_t st) {
+  switch (a.K * 1000 + a.V) {
+    case 32032: return go<E, 32, 32, WHAT>(a, w, st);
+    case 32064: return go<E, 32, 64, WHAT>(a, w, st);
+    case 32128: return go<E, 32, 128, WHAT>(a, w, st);
+    case 64032: return go<E, 64, 32, WHAT>(a, w, st);
+    case 64064: return go<E, 64, 64, WHAT>(a, w, st);
+    case 64128: return go<E, 64, 128, WHAT>(a, w, st);
+    case 128032: return go<E, 128, 32, WHAT>(a, w, st);
+    case 128064: return go<E, 128, 64, WHAT>(a, w, st);
+    default: return go<E, 128, 128, WHAT>(a, w, st);
+  }
+}
+template <int WHAT>
+hipError_t pass(const AttnArgs &a, const Layout &w, hipStream_t st) {
+  return a.dtype == 1 ? pick<bf16, WHAT>(a, w, st) : pick<float, WHAT>(a, w, st);
+}
+
+unsigned carry_blocks(const AttnArgs &a) {
+  return (unsigned)(((int64_t)a.s.N * a.Hv * a.K * a.V / 4 + 255) / 256);
+}
+
+}  // namespace
+}  // namespace attn
+
+// Segments: as long as the whole sequence unless that leaves compute units
+// without two workgroups each; then as many as give each so many.
+AttnPlan attn_plan(const AttnArgs &a0, bool bwd) {
+  AttnArgs a = a0;
+  const int64_t per = (int64_t)a.Hv * (a.V / 32);  // workgroups a segment
+  int64_t want = (compute_units() * 2 + per - 1) / per;
+  if (want < a.s.N) want = a.s.N;
+  int64_t seg = (a.s.tokens + want - 1) / want;
+  seg = (seg + 63) / 64 * 64;
+  if (seg < 64) seg = 64;
+  AttnPlan p;
+  p.seg = (int)seg;
+  a.slots = p.slots = scan::slots_of(a.s, p.seg);
+  a.one_seg = p.one_seg = a.s.T <= seg;
+  p.ws = attn::layout(a, bwd).total;
+  return p;
+}
+
+hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t st) {
+  using namespace attn;
+  const Layout w = layout(a, false);
+  if (!a.one_seg) {
+    hipError_t e = pass<kLocal>(a, w, st);
+    if (e != hipSuccess) return e;
+    KernelTimer kt("attn_carry", st);
+    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return pass<kForward>(a, w, st);
+}
+
+hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t st) {
+  using namespace attn;
+  const Layout w = layout(a, true);
+  hipError_t e;
+  if (!a.one_seg) {
+    if ((e = pass<kLocals>(a, w, st)) != hipSuccess) return e;
+    KernelTimer kt("attn_carry", st);
+    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if ((e = pass<kGrads>(a, w, st)) != hipSuccess) return e;
+  if (a.Hv == a.Hq || a.s.tokens == 0) return hipSuccess;
+  KernelTimer kt("attn_group", st);
+  const unsigned blocks = (unsigned)((a.s.tokens * a.Hq * (a.K / 4) + 255) / 256);
+  if (a.dtype == 1)
+    group_kernel<bf16><<<blocks, 256, 0, st>>>(a, w);
+  else
+    group_kernel<float><<<blocks, 256, 0, st>>>(a, w);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

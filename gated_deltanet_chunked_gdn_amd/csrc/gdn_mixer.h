@@ -1,7 +1,7 @@
 // Internal interface between the C ABI of the sequence-mixer operators
 // (gdn_mixer_api.cpp: validation, workspace carving) and their kernels: the
-// short causal convolution, the selective scan, the single-token steps and
-// the layer norm.
+// short causal convolution, the selective scan, linear attention, the
+// single-token steps, the layer norm and the group norm.
 #pragma once
 
 #include <stddef.h>
@@ -61,10 +61,11 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st);
 
 // One token of the recurrences: state [slots][Hv][K][V] fp32, updated in
-// place.  delta: the gated delta rule (g, beta, scale, l2), else the
-// selective scan (dt, A, D, dt_bias, softplus).
+// place: the gated delta rule (g, beta, scale, l2), the selective scan (dt, A,
+// D, dt_bias, softplus) or linear attention (g by head, scale).
+enum StepRule { kStepScan, kStepDelta, kStepDecay };
 struct StepArgs {
-  int B, Hq, Hv, K, V, dtype, delta, l2, softplus, slots;
+  int B, Hq, Hv, K, V, dtype, rule, l2, softplus, slots;
   float scale;
   int64_t qs, ks, vs;  // elements from one batch row of q (c), k (b), v (x) to the next
   const void *q, *k, *v, *beta;  // beta: dt of the scan
@@ -99,5 +100,46 @@ struct ScanPlan {
 ScanPlan scan_plan(const ScanArgs &a, bool bwd);
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st);
+
+// Linear attention with a decay for each v-head, in segments as the scan.
+struct AttnArgs {
+  Seqs s;
+  int Hq, Hv, K, V, dtype;
+  int seg;
+  int64_t slots;
+  bool one_seg;        // no sequence has two segments
+  float scale;
+  int64_t qs, ks, vs;  // elements from one token to the next of q, k, v
+  const void *q, *k, *v, *dO;
+  const float *g, *h0, *dht;  // g: the log decays [Hv]
+  void *o, *dq, *dk, *dv;
+  float *ht, *dh0;
+  char *ws;
+};
+struct AttnPlan {
+  int seg;
+  int64_t slots;
+  bool one_seg;
+  size_t ws;
+};
+AttnPlan attn_plan(const AttnArgs &a, bool bwd);
+hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t st);
+hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t st);
+
+// Group norm of N samples of S positions and C = G Dg channels, channels last.
+struct GroupArgs {
+  int64_t N, S;
+  int G, Dg, dtype, wdtype, silu;
+  float eps;
+  const void *x, *w, *b, *gate, *dy;
+  void *y, *dx, *dw, *db, *dgate;
+  float *mean, *rstd;  // [N][G], written by the forward, read by the backward
+  char *ws;
+};
+bool group_fits(const GroupArgs &a);  // into launches of less than 2^32 threads
+size_t group_fwd_bytes(const GroupArgs &a);
+size_t group_bwd_bytes(const GroupArgs &a);
+hipError_t launch_group_fwd(const GroupArgs &a, hipStream_t st);
+hipError_t launch_group_bwd(const GroupArgs &a, hipStream_t st);
 
 }  // namespace gdn

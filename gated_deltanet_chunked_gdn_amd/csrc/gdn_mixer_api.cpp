@@ -169,6 +169,85 @@ int check_norm(const gdn_norm_t *p, gdn::NormArgs *a) {
   return GDN_OK;
 }
 
+// ---- linear attention
+int check_attn(const gdn_attn_t *p, bool step, bool bwd, gdn::AttnArgs *a) {
+  if (!p) return set_error(GDN_ERR_INVALID_ARG, "problem descriptor is NULL");
+  if (p->B <= 0 || p->T < 0 || p->Hq <= 0 || p->Hv <= 0 || p->K <= 0 || p->V <= 0)
+    return set_error(GDN_ERR_INVALID_ARG, "dimensions must be positive (B=%d T=%d Hq=%d Hv=%d K=%d V=%d)", p->B,
+                     p->T, p->Hq, p->Hv, p->K, p->V);
+  if (!known(p->dtype)) return set_error(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_F32 or GDN_BF16", p->dtype);
+  if (p->Hv % p->Hq != 0)
+    return set_error(GDN_ERR_UNSUPPORTED, "Hv=%d is not a multiple of Hq=%d", p->Hv, p->Hq);
+  auto ok = [](int d) { return d == 32 || d == 64 || d == 128; };
+  if (!ok(p->K) || !ok(p->V))
+    return set_error(GDN_ERR_UNSUPPORTED, "K=%d V=%d not supported: 32, 64 and 128 are", p->K, p->V);
+  if (!(p->scale == p->scale)) return set_error(GDN_ERR_INVALID_ARG, "scale is NaN");
+  if (step && (p->T != 1 || p->cu_seqlens))
+    return set_error(GDN_ERR_INVALID_ARG, "a step has T = 1 and no cu_seqlens (T=%d)", p->T);
+  const int rc = check_seqs(p->B, p->T, p->N, p->cu_seqlens, p->cu_seqlens_host);
+  if (rc != GDN_OK) return rc;
+  const int64_t qw = (int64_t)p->Hq * p->K, vw = (int64_t)p->Hv * p->V;
+  const int64_t qs = p->q_stride ? p->q_stride : qw, ks = p->k_stride ? p->k_stride : qw,
+                vs = p->v_stride ? p->v_stride : vw;
+  if (qs < qw || ks < qw || vs < vw)
+    return set_error(GDN_ERR_INVALID_ARG, "a stride is below its row (q %lld k %lld v %lld)", (long long)qs,
+                     (long long)ks, (long long)vs);
+  const int64_t per = 16 / (int64_t)elem(p->dtype);
+  // (the passes address a chunk's rows, contiguous ones among them, by 32-bit
+  // byte offsets, the step its one row by itself)
+  constexpr int64_t kRow = (int64_t)1 << 24;
+  if (!step && (qs >= kRow || ks >= kRow || vs >= kRow || (int64_t)p->Hv * p->K >= kRow))
+    return set_error(GDN_ERR_UNSUPPORTED, "q, k and v rows must lie less than 2^24 elements apart");
+  if (qs % per || ks % per || vs % per)
+    return set_error(GDN_ERR_LAYOUT, "q, k and v strides must be multiples of 16 bytes");
+  *a = gdn::AttnArgs{};
+  a->s = gdn::Seqs{p->cu_seqlens, p->cu_seqlens ? p->N : p->B, p->T, (int64_t)p->B * p->T};
+  a->Hq = p->Hq;
+  a->Hv = p->Hv;
+  a->K = p->K;
+  a->V = p->V;
+  a->dtype = p->dtype;
+  a->scale = p->scale;
+  a->qs = qs;
+  a->ks = ks;
+  a->vs = vs;
+  // (a launch has fewer than 2^32 threads: up to twelve workgroups of 256 a
+  // slot and head, two threads for four elements of a state, one for four of dq)
+  constexpr int64_t kBlocks = (int64_t)1 << 24;
+  const int64_t heads = (int64_t)p->Hv * (step ? 0 : gdn::attn_plan(*a, bwd).slots);
+  if (a->s.tokens * p->Hv * 128 > ((int64_t)1 << 40) || (int64_t)a->s.N * p->Hv >= kGrid || heads * 12 >= kBlocks ||
+      (!step && ((int64_t)a->s.N * p->Hv * p->K * p->V / 512 >= kBlocks || (bwd && a->s.tokens * p->Hq * p->K / 1024 >= kBlocks))))
+    return set_error(GDN_ERR_UNSUPPORTED, "problem too large");
+  return GDN_OK;
+}
+
+// ---- group norm
+int check_group(const gdn_group_t *p, gdn::GroupArgs *a) {
+  if (!p) return set_error(GDN_ERR_INVALID_ARG, "problem descriptor is NULL");
+  if (p->N < 0 || p->S <= 0 || p->G <= 0 || p->Dg <= 0)
+    return set_error(GDN_ERR_INVALID_ARG, "dimensions must be positive (N=%lld S=%lld G=%d Dg=%d)", (long long)p->N,
+                     (long long)p->S, p->G, p->Dg);
+  if (!known(p->dtype)) return set_error(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_F32 or GDN_BF16", p->dtype);
+  if (p->weight_dtype != GDN_F32 && p->weight_dtype != p->dtype)
+    return set_error(GDN_ERR_UNSUPPORTED, "weight_dtype %d is neither fp32 nor the problem's", p->weight_dtype);
+  if (p->silu != 0 && p->silu != 1) return set_error(GDN_ERR_INVALID_ARG, "silu must be 0 or 1 (got %d)", p->silu);
+  if (!(p->eps >= 0)) return set_error(GDN_ERR_INVALID_ARG, "eps must not be negative");
+  if ((int64_t)p->G * p->Dg >= (1 << 24) || p->S >= kGrid || p->N >= kGrid || p->N * p->G >= kGrid ||
+      (double)p->N * (double)p->S * p->G * p->Dg >= 1e12)
+    return set_error(GDN_ERR_UNSUPPORTED, "problem too large");
+  *a = gdn::GroupArgs{};
+  a->N = p->N;
+  a->S = p->S;
+  a->G = p->G;
+  a->Dg = p->Dg;
+  a->dtype = p->dtype;
+  a->wdtype = p->weight_dtype;
+  a->silu = p->silu;
+  a->eps = p->eps;
+  if (!gdn::group_fits(*a)) return set_error(GDN_ERR_UNSUPPORTED, "problem too large for the launch grid");
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -395,7 +474,7 @@ int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, co
   a.K = p->K;
   a.V = p->V;
   a.dtype = p->dtype;
-  a.delta = 1;
+  a.rule = gdn::kStepDelta;
   a.l2 = p->qk_l2norm;
   a.slots = slots;
   a.scale = p->scale;
@@ -470,6 +549,180 @@ int gdn_layer_norm_bwd(const gdn_norm_t *p, const void *dy, const void *x, const
   a.dgate = dgate;
   a.partial = static_cast<float *>(workspace);
   return hip(gdn::launch_norm_bwd(a, static_cast<hipStream_t>(stream)), "layer norm backward");
+}
+
+size_t gdn_linear_attention_fwd_workspace_size(const gdn_attn_t *p) {
+  gdn::clear_error();
+  gdn::AttnArgs a;
+  return check_attn(p, false, false, &a) == GDN_OK ? gdn::attn_plan(a, false).ws : 0;
+}
+size_t gdn_linear_attention_bwd_workspace_size(const gdn_attn_t *p) {
+  gdn::clear_error();
+  gdn::AttnArgs a;
+  return check_attn(p, false, true, &a) == GDN_OK ? gdn::attn_plan(a, true).ws : 0;
+}
+
+int gdn_linear_attention_fwd(const gdn_attn_t *p, const void *q, const void *k, const void *v, const float *log_decay,
+                             const float *h0, void *o, float *ht, void *workspace, size_t ws_bytes, void *stream) {
+  gdn::clear_error();
+  gdn::AttnArgs a;
+  int rc = check_attn(p, false, false, &a);
+  if (rc != GDN_OK) return rc;
+  if (!log_decay || (a.s.tokens > 0 && (!q || !k || !v || !o)))
+    return set_error(GDN_ERR_INVALID_ARG, "q, k, v, log_decay and o are required");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(h0, 16) || !aligned(ht, 16) ||
+      !aligned(log_decay, 4))
+    return set_error(GDN_ERR_LAYOUT, "q, k, v, o and the states must be 16-byte aligned; log_decay to its elements");
+  const gdn::AttnPlan pl = gdn::attn_plan(a, false);
+  if ((rc = check_ws(workspace, ws_bytes, pl.ws)) != GDN_OK) return rc;
+  a.seg = pl.seg;
+  a.slots = pl.slots;
+  a.one_seg = pl.one_seg;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = log_decay;
+  a.h0 = h0;
+  a.o = o;
+  a.ht = ht;
+  a.ws = static_cast<char *>(workspace);
+  return hip(gdn::launch_attn_fwd(a, static_cast<hipStream_t>(stream)), "linear attention");
+}
+
+int gdn_linear_attention_bwd(const gdn_attn_t *p, const void *q, const void *k, const void *v, const float *log_decay,
+                             const float *h0, const void *d_o, const float *dht, void *dq, void *dk, void *dv, float *dh0,
+                             void *workspace, size_t ws_bytes, void *stream) {
+  gdn::clear_error();
+  gdn::AttnArgs a;
+  int rc = check_attn(p, false, true, &a);
+  if (rc != GDN_OK) return rc;
+  if (!log_decay || (a.s.tokens > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)))
+    return set_error(GDN_ERR_INVALID_ARG, "q, k, v, log_decay, do, dq, dk and dv are required");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(dk, 16) ||
+      !aligned(dv, 16) || !aligned(h0, 16) || !aligned(dht, 16) || !aligned(dh0, 16) || !aligned(log_decay, 4))
+    return set_error(GDN_ERR_LAYOUT,
+                     "q, k, v, do, dq, dk, dv and the states must be 16-byte aligned; log_decay to its elements");
+  const gdn::AttnPlan pl = gdn::attn_plan(a, true);
+  if ((rc = check_ws(workspace, ws_bytes, pl.ws)) != GDN_OK) return rc;
+  a.seg = pl.seg;
+  a.slots = pl.slots;
+  a.one_seg = pl.one_seg;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.dO = d_o;
+  a.g = log_decay;
+  a.h0 = h0;
+  a.dht = dht;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dh0 = dh0;
+  a.ws = static_cast<char *>(workspace);
+  return hip(gdn::launch_attn_bwd(a, static_cast<hipStream_t>(stream)), "linear attention backward");
+}
+
+int gdn_linear_attention_step(const gdn_attn_t *p, const void *q, const void *k, const void *v, const float *log_decay,
+                              float *state, const int32_t *state_indices, int32_t slots, void *o, void *stream) {
+  gdn::clear_error();
+  gdn::AttnArgs s;
+  int rc = check_attn(p, true, false, &s);
+  if (rc != GDN_OK) return rc;
+  if (!q || !k || !v || !log_decay || !state || !o)
+    return set_error(GDN_ERR_INVALID_ARG, "q, k, v, log_decay, state and o are required");
+  if ((rc = check_slots(state_indices, slots, p->B)) != GDN_OK) return rc;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(state, 16) || !aligned(log_decay, 4))
+    return set_error(GDN_ERR_LAYOUT, "q, k, v, o and state must be 16-byte aligned; log_decay to its elements");
+  gdn::StepArgs a = {};
+  a.B = p->B;
+  a.Hq = p->Hq;
+  a.Hv = p->Hv;
+  a.K = p->K;
+  a.V = p->V;
+  a.dtype = p->dtype;
+  a.rule = gdn::kStepDecay;
+  a.slots = slots;
+  a.scale = p->scale;
+  a.qs = s.qs;
+  a.ks = s.ks;
+  a.vs = s.vs;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = log_decay;
+  a.state = state;
+  a.index = state_indices;
+  a.o = o;
+  return hip(gdn::launch_step(a, static_cast<hipStream_t>(stream)), "linear attention step");
+}
+
+size_t gdn_group_norm_fwd_workspace_size(const gdn_group_t *p) {
+  gdn::clear_error();
+  gdn::GroupArgs a;
+  return check_group(p, &a) == GDN_OK ? gdn::group_fwd_bytes(a) : 0;
+}
+size_t gdn_group_norm_bwd_workspace_size(const gdn_group_t *p) {
+  gdn::clear_error();
+  gdn::GroupArgs a;
+  return check_group(p, &a) == GDN_OK ? gdn::group_bwd_bytes(a) : 0;
+}
+
+int gdn_group_norm_fwd(const gdn_group_t *p, const void *x, const void *weight, const void *bias, const void *gate,
+                       void *y, float *mean, float *rstd, void *workspace, size_t ws_bytes, void *stream) {
+  gdn::clear_error();
+  gdn::GroupArgs a;
+  int rc = check_group(p, &a);
+  if (rc != GDN_OK) return rc;
+  if (p->N > 0 && (!x || !y || !mean || !rstd))
+    return set_error(GDN_ERR_INVALID_ARG, "x, y, mean and rstd are required");
+  if (gate && p->silu) return set_error(GDN_ERR_INVALID_ARG, "silu and a gate exclude each other");
+  const size_t e = elem(p->dtype), we = elem(p->weight_dtype);
+  if (!aligned(x, e) || !aligned(y, e) || !aligned(gate, e) || !aligned(weight, we) || !aligned(bias, we) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return set_error(GDN_ERR_LAYOUT, "a buffer is not aligned to its elements");
+  if ((rc = check_ws(workspace, ws_bytes, gdn::group_fwd_bytes(a))) != GDN_OK) return rc;
+  a.x = x;
+  a.w = weight;
+  a.b = bias;
+  a.gate = gate;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.ws = static_cast<char *>(workspace);
+  return hip(gdn::launch_group_fwd(a, static_cast<hipStream_t>(stream)), "group norm");
+}
+
+int gdn_group_norm_bwd(const gdn_group_t *p, const void *dy, const void *x, const void *weight, const void *bias,
+                       const void *gate, const float *mean, const float *rstd, void *dx, void *dweight, void *dbias,
+                       void *dgate, void *workspace, size_t ws_bytes, void *stream) {
+  gdn::clear_error();
+  gdn::GroupArgs a;
+  int rc = check_group(p, &a);
+  if (rc != GDN_OK) return rc;
+  if (p->N > 0 && (!dy || !x || !mean || !rstd || !dx || (gate && !dgate)))
+    return set_error(GDN_ERR_INVALID_ARG, "dy, x, mean, rstd, dx and dgate (with gate) are required");
+  if ((dweight && !weight) || (dbias && !bias) || (dgate && !gate))
+    return set_error(GDN_ERR_INVALID_ARG, "a gradient is asked for without its weight, bias or gate");
+  if (gate && p->silu) return set_error(GDN_ERR_INVALID_ARG, "silu and a gate exclude each other");
+  const size_t e = elem(p->dtype), we = elem(p->weight_dtype);
+  if (!aligned(dy, e) || !aligned(x, e) || !aligned(gate, e) || !aligned(dx, e) || !aligned(dgate, e) ||
+      !aligned(weight, we) || !aligned(bias, we) || !aligned(dweight, we) || !aligned(dbias, we) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return set_error(GDN_ERR_LAYOUT, "a buffer is not aligned to its elements");
+  if ((rc = check_ws(workspace, ws_bytes, gdn::group_bwd_bytes(a))) != GDN_OK) return rc;
+  a.dy = dy;
+  a.x = x;
+  a.w = weight;
+  a.b = bias;
+  a.gate = gate;
+  a.mean = const_cast<float *>(mean);
+  a.rstd = const_cast<float *>(rstd);
+  a.dx = dx;
+  a.dw = dweight;
+  a.db = dbias;
+  a.dgate = dgate;
+  a.ws = static_cast<char *>(workspace);
+  return hip(gdn::launch_group_bwd(a, static_cast<hipStream_t>(stream)), "group norm backward");
 }
 
 }  // extern "C"

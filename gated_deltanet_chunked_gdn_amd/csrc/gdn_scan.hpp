@@ -164,30 +164,31 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 
-__device__ __forceinline__ SlotLoc locate(const ScanArgs &a, int64_t slot) {
-  int lo = 0, hi = a.s.N - 1;
-  if (!a.s.cu) {
-    lo = (int)(slot / segs_of(Span{0, a.s.T}, a.seg));
+__device__ __forceinline__ SlotLoc locate(const Seqs &q, int seg, int64_t slot) {
+  int lo = 0, hi = q.N - 1;
+  if (!q.cu) {
+    lo = (int)(slot / segs_of(Span{0, q.T}, seg));
   } else {
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (first_slot(a.s, seq_span(a.s, mid), mid, a.seg) <= slot)
+      if (first_slot(q, seq_span(q, mid), mid, seg) <= slot)
         lo = mid;
       else
         hi = mid - 1;
     }
   }
-  const Span sp = seq_span(a.s, lo);
-  const int64_t s = slot - first_slot(a.s, sp, lo, a.seg), ns = segs_of(sp, a.seg);
+  const Span sp = seq_span(q, lo);
+  const int64_t s = slot - first_slot(q, sp, lo, seg), ns = segs_of(sp, seg);
   SlotLoc l;
   l.n = lo;
   l.used = s >= 0 && s < ns;
   l.index = s;
   l.last = s == ns - 1;
-  l.t0 = sp.first + s * a.seg;
-  l.t1 = l.t0 + a.seg < sp.end ? l.t0 + a.seg : sp.end;
+  l.t0 = sp.first + s * seg;
+  l.t1 = l.t0 + seg < sp.end ? l.t0 + seg : sp.end;
   return l;
 }
+__device__ __forceinline__ SlotLoc locate(const ScanArgs &a, int64_t slot) { return locate(a.s, a.seg, slot); }
 
 }  // namespace scan
 }  // namespace gdn

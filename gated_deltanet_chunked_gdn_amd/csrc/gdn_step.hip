@@ -3,8 +3,9 @@
 //
 //   gated delta rule   S = e^g S;  u = beta (v - S^T k);  S += k u^T;  o = scale S^T q
 //   selective scan     S = e^(delta A) S + b (delta x)^T;  y = S^T c + D x
+//   linear attention   S = e^g S + k v^T;  o = scale S^T q      (g: a head's)
 //
-// Both are S' = a S + k u^T, o = s (a S^T q + (q . k) u), so the two dot
+// All are S' = a S + k u^T, o = s (a S^T q + (q . k) u), so the two dot
 // products of every column with k and q are taken in one pass over the old
 // state, before u is known: the state is read once, held in registers and
 // written once.  8 K V bytes a head set the time.
@@ -44,9 +45,10 @@ __device__ __forceinline__ void load_n(float (&r)[N], const E *p) {
   }
 }
 
-template <typename E, int K, bool DELTA>
+template <typename E, int K, int RULE>
 __global__ __launch_bounds__(64 * kMostWaves) void step_kernel(StepArgs a) {
   constexpr int R = K / 8;  // rows a lane
+  constexpr bool DELTA = RULE == kStepDelta;
   const int lane = threadIdx.x & 63, cl = lane & 7, rl = lane >> 3;
   const int slices = a.V >> 5;
   const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 6) + wave_of(threadIdx.x);
@@ -78,7 +80,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void step_kernel(StepArgs a) {
   load_n<E, R>(q, static_cast<const E *>(a.q) + row * a.qs + hq * K + rl * R);
   load_n<E, R>(k, static_cast<const E *>(a.k) + row * a.ks + hq * K + rl * R);
   load_n<E, 4>(v, static_cast<const E *>(a.v) + row * a.vs + (int64_t)h * a.V + col);
-  const float be = to_f32(static_cast<const E *>(a.beta)[row * a.Hv + h]);
+  const float be = RULE == kStepDecay ? 0.f : to_f32(static_cast<const E *>(a.beta)[row * a.Hv + h]);
 
   if (DELTA && a.l2) {
     float qq = 0.f, kk = 0.f;
@@ -120,6 +122,13 @@ __global__ __launch_bounds__(64 * kMostWaves) void step_kernel(StepArgs a) {
       u[i] = be * (v[i] - decay * sk[i]);
       out[i] = a.scale * (decay * sq[i] + qk * u[i]);
     }
+  } else if (RULE == kStepDecay) {
+    decay = expf(a.g[h]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[i] = v[i];
+      out[i] = a.scale * (decay * sq[i] + qk * u[i]);
+    }
   } else {
     const float z = be + (a.dt_bias ? a.dt_bias[h] : 0.f);
     const float delta = a.softplus ? softplusf(z) : z;
@@ -147,12 +156,15 @@ hipError_t go(const StepArgs &a, hipStream_t st) {
   // a compute unit each while there are no more waves than those
   const int waves = units > compute_units() ? kMostWaves : 1;
   const unsigned blocks = (unsigned)((units + waves - 1) / waves);
-  if (a.delta) {
+  if (a.rule == kStepDelta) {
     KernelTimer kt("delta_step", st);
-    step_kernel<E, K, true><<<blocks, 64 * waves, 0, st>>>(a);
+    step_kernel<E, K, kStepDelta><<<blocks, 64 * waves, 0, st>>>(a);
+  } else if (a.rule == kStepDecay) {
+    KernelTimer kt("attn_step", st);
+    step_kernel<E, K, kStepDecay><<<blocks, 64 * waves, 0, st>>>(a);
   } else {
     KernelTimer kt("scan_step", st);
-    step_kernel<E, K, false><<<blocks, 64 * waves, 0, st>>>(a);
+    step_kernel<E, K, kStepScan><<<blocks, 64 * waves, 0, st>>>(a);
   }
   return hipGetLastError();
 }

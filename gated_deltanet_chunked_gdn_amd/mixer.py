@@ -3,7 +3,9 @@
   causal_conv_fwd / _bwd / _step     short causal convolution (with SiLU)
   selective_scan_fwd / _bwd / _step  selective state-space scan
   gated_delta_rule_step              the gated delta rule for single tokens
+  linear_attention_fwd / _bwd / _step  linear attention with a decay for each head
   layer_norm_fwd / _bwd              layer norm (or RMS norm), optional output gate
+  group_norm_fwd / _bwd              group norm, channels last, with an activation or an output gate
 
 Argument marshalling over libgdn.so (include/gdn.h) like the chunked entry
 points: torch supplies outputs, workspace and the current stream of the
@@ -41,6 +43,15 @@ class NormProblem(ctypes.Structure):
     _fields_ = [("rows", _I64)] + [(n, _I32) for n in ("D", "dtype", "weight_dtype", "rms")] + [("eps", ctypes.c_float)]
 
 
+class AttnProblem(ctypes.Structure):
+    _fields_ = [(n, _I32) for n in ("B", "T", "Hq", "Hv", "K", "V", "N", "dtype")] + [("scale", ctypes.c_float)] + [
+        (n, _I64) for n in ("q_stride", "k_stride", "v_stride")] + [("cu_seqlens", _P), ("cu_seqlens_host", _P)]
+
+
+class GroupProblem(ctypes.Structure):
+    _fields_ = [("N", _I64), ("S", _I64)] + [(n, _I32) for n in ("G", "Dg", "dtype", "weight_dtype", "silu")] + [("eps", ctypes.c_float)]
+
+
 _ready = None
 
 
@@ -49,7 +60,8 @@ def lib():
     global _ready
     if _ready is None:
         L = _base_lib()
-        cp, sp, np_, pp = (ctypes.POINTER(t) for t in (ConvProblem, ScanProblem, NormProblem, GdnProblem))
+        cp, sp, np_, pp, ap, gp = (ctypes.POINTER(t) for t in (ConvProblem, ScanProblem, NormProblem, GdnProblem,
+                                                               AttnProblem, GroupProblem))
         for name, args in (
                 ("gdn_causal_conv_fwd", [cp] + [_P] * 7),
                 ("gdn_causal_conv_bwd", [cp] + [_P] * 11 + [_S, _P]),
@@ -59,11 +71,18 @@ def lib():
                 ("gdn_selective_scan_step", [sp] + [_P] * 9 + [_I32, _P, _P]),
                 ("gdn_delta_rule_step", [pp] + [_P] * 5 + [_I64] * 3 + [_P, _P, _I32, _P, _P]),
                 ("gdn_layer_norm_fwd", [np_] + [_P] * 8),
-                ("gdn_layer_norm_bwd", [np_] + [_P] * 12 + [_S, _P])):
+                ("gdn_layer_norm_bwd", [np_] + [_P] * 12 + [_S, _P]),
+                ("gdn_linear_attention_fwd", [ap] + [_P] * 8 + [_S, _P]),
+                ("gdn_linear_attention_bwd", [ap] + [_P] * 12 + [_S, _P]),
+                ("gdn_linear_attention_step", [ap] + [_P] * 6 + [_I32, _P, _P]),
+                ("gdn_group_norm_fwd", [gp] + [_P] * 8 + [_S, _P]),
+                ("gdn_group_norm_bwd", [gp] + [_P] * 12 + [_S, _P])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, ctypes.c_int
         for name, arg in (("gdn_causal_conv_bwd_workspace_size", cp), ("gdn_selective_scan_fwd_workspace_size", sp),
-                          ("gdn_selective_scan_bwd_workspace_size", sp), ("gdn_layer_norm_bwd_workspace_size", np_)):
+                          ("gdn_selective_scan_bwd_workspace_size", sp), ("gdn_layer_norm_bwd_workspace_size", np_),
+                          ("gdn_linear_attention_fwd_workspace_size", ap), ("gdn_linear_attention_bwd_workspace_size", ap),
+                          ("gdn_group_norm_fwd_workspace_size", gp), ("gdn_group_norm_bwd_workspace_size", gp)):
             f = getattr(L, name)
             f.argtypes, f.restype = [arg], _S
         _ready = L
@@ -426,6 +445,106 @@ def gated_delta_rule_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_
     return o
 
 
+# ---------------------------------------------------------------- linear attention
+
+
+def _attn_problem(q, k, v, log_decay, scale, lead):
+    what = "[B, T, Hq, K]" if lead == 2 else "[B, Hq, K]"
+    if q.dim() != lead + 2 or k.shape != q.shape or v.dim() != lead + 2 or v.shape[:lead] != q.shape[:lead]:
+        raise ValueError(f"q, k must be {what} and v as them over the v-heads")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k and v must share one dtype")
+    _sizes(*q.shape, *v.shape)
+    Hv = v.shape[lead]
+    if log_decay is None or log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (Hv,):
+        raise ValueError(f"log_decay must be float32 [{Hv}]")
+    K = q.shape[lead + 1]
+    dt = _dtype(q, "q, k and v")
+    if scale is None and K == 0:
+        raise ValueError("K must be positive")
+    most = (1 << 24) - 1 if lead == 2 else 1 << 62
+    (qr, qs), (kr, ks), (vr, vs) = (_rows(t, lead, True, most) for t in (q, k, v))
+    p = AttnProblem(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[lead], Hv, K, v.shape[lead + 1], q.shape[0], dt,
+                    float(K ** -0.5 if scale is None else scale), qs, ks, vs, None, None)
+    return p, qr, kr, vr, log_decay.contiguous()
+
+
+def linear_attention_fwd(q, k, v, log_decay, scale=None, initial_state=None, cu_seqlens=None,
+                         output_final_state: bool = True, check_cu_seqlens: bool = True):
+    """Linear attention with a decay for each head.  Returns (o, final_state).
+
+    Per v-head h: S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T and
+    o_t = scale S_t^T q_t (scale: K ** -0.5 unless given).  q, k [B, T, Hq, K]
+    (read by v-head h at head h // (Hv // Hq)), v [B, T, Hv, V] in one dtype;
+    log_decay float32 [Hv], a constant of the layer: 0 keeps everything, -inf
+    nothing, and a state that grows (above 0) is computed as it is, up to what
+    float32 holds.  States float32 [N, Hv, K, V]; K, V in {32, 64, 128}.  The
+    token rows of q, k and v may be slices of a wider tensor.  A NaN or an
+    infinity in a token reaches the tokens of its 64-token chunk, earlier ones
+    too, and all later ones of its sequence; no other sequence."""
+    p, q, k, v, log_decay = _attn_problem(q, k, v, log_decay, scale, 2)
+    dev = q.device
+    sq = _Seqs(cu_seqlens, p.B, p.T, dev, check_cu_seqlens)
+    shape = (sq.N, p.Hv, p.K, p.V)
+    h0 = _aligned(initial_state)
+    _check_state(h0, "initial_state", shape)
+    _check_device(q, k, v, log_decay, h0)
+    p.N = sq.N
+    p.cu_seqlens, p.cu_seqlens_host = sq.ptrs()
+    o = torch.empty(v.shape, device=dev, dtype=v.dtype)
+    ht = torch.empty(shape, device=dev, dtype=torch.float32) if output_final_state else None
+    L = lib()
+    n = L.gdn_linear_attention_fwd_workspace_size(ctypes.byref(p))
+    ws = _workspace(n, dev)
+    _call(L.gdn_linear_attention_fwd, dev, ctypes.byref(p), _p(q), _p(k), _p(v), _p(log_decay), _p(h0), _p(o),
+          _p(ht), _p(ws), n)
+    return o, ht
+
+
+def linear_attention_bwd(q, k, v, log_decay, do, dht=None, scale=None, initial_state=None, cu_seqlens=None,
+                         check_cu_seqlens: bool = True):
+    """Backward of linear_attention_fwd.  Returns (dq, dk, dv, dh0): dq, dk
+    summed over the v-heads of a group, dh0 None without initial_state.
+    log_decay has no gradient (a decay that is learned: selective_scan_fwd's
+    A, with dt = 1).  A NaN or an infinity in a token reaches dq of its chunk
+    and later tokens, dk and dv of its chunk and earlier ones."""
+    p, q, k, v, log_decay = _attn_problem(q, k, v, log_decay, scale, 2)
+    if do is None or do.shape != v.shape or do.dtype != v.dtype:
+        raise ValueError(f"do must have v's shape {list(v.shape)} and dtype {v.dtype}")
+    dev = q.device
+    sq = _Seqs(cu_seqlens, p.B, p.T, dev, check_cu_seqlens)
+    shape = (sq.N, p.Hv, p.K, p.V)
+    do, dht, h0 = _aligned(do), _aligned(dht), _aligned(initial_state)
+    _check_state(dht, "dht", shape)
+    _check_state(h0, "initial_state", shape)
+    _check_device(q, k, v, log_decay, do, dht, h0)
+    p.N = sq.N
+    p.cu_seqlens, p.cu_seqlens_host = sq.ptrs()
+    dq, dk, dv = (torch.empty(t.shape, device=dev, dtype=t.dtype) for t in (q, k, v))
+    dh0 = None if h0 is None else torch.empty(shape, device=dev, dtype=torch.float32)
+    L = lib()
+    n = L.gdn_linear_attention_bwd_workspace_size(ctypes.byref(p))
+    ws = _workspace(n, dev)
+    _call(L.gdn_linear_attention_bwd, dev, ctypes.byref(p), _p(q), _p(k), _p(v), _p(log_decay), _p(h0), _p(do),
+          _p(dht), _p(dq), _p(dk), _p(dv), _p(dh0), _p(ws), n)
+    return dq, dk, dv, dh0
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale=None, state_indices=None):
+    """One token of linear_attention_fwd: q, k [B, Hq, K], v [B, Hv, V] ->
+    o [B, Hv, V]; state [slots, Hv, K, V] (float32) is updated in place.
+    state_indices as for causal_conv_step."""
+    p, q, k, v, log_decay = _attn_problem(q, k, v, log_decay, scale, 1)
+    _step_state(state, p.Hv, p.K, p.V)
+    idx = _indices(state_indices, p.B, state)
+    _check_device(q, k, v, log_decay, state, idx)
+    dev = q.device
+    o = torch.empty(v.shape, device=dev, dtype=v.dtype)
+    _call(lib().gdn_linear_attention_step, dev, ctypes.byref(p), _p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(idx),
+          state.shape[0], _p(o))
+    return o
+
+
 # ---------------------------------------------------------------- layer norm
 
 
@@ -481,5 +600,77 @@ def layer_norm_bwd(dy, x, weight, bias, mean, rstd, gate=None, rms: bool = False
     n = L.gdn_layer_norm_bwd_workspace_size(ctypes.byref(p))
     ws = _workspace(n, dev)
     _call(L.gdn_layer_norm_bwd, dev, ctypes.byref(p), _p(dy), _p(x), _p(weight), _p(bias), _p(gate), _p(mean),
+          _p(rstd), _p(dx), _p(dw), _p(db), _p(dgate), _p(ws), n)
+    return dx, dw, db, dgate
+
+
+# ---------------------------------------------------------------- group norm
+
+
+def _group_problem(x, groups, weight, bias, gate, activation, eps):
+    if x.dim() < 2 or x.shape[-1] == 0:
+        raise ValueError(f"x must be [N, ..., C] with C > 0, got {list(x.shape)}")
+    C = x.shape[-1]
+    if isinstance(groups, bool) or not isinstance(groups, int) or groups <= 0 or C % groups:
+        raise ValueError(f"groups must be an integer that divides C = {C}, got {groups!r}")
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    if S == 0:
+        raise ValueError(f"x must have positions, got {list(x.shape)}")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None and tuple(t.shape) != (C,):
+            raise ValueError(f"{name} must be [{C}], got {list(t.shape)}")
+    if gate is not None and (gate.shape != x.shape or gate.dtype != x.dtype):
+        raise ValueError(f"gate must have x's shape {list(x.shape)} and dtype {x.dtype}")
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    if gate is not None and activation is not None:
+        raise ValueError("gate and activation exclude each other")
+    _sizes(C)
+    return GroupProblem(x.shape[0], S, groups, C // groups, _dtype(x, "x"), _weight_dtype(x, weight, bias),
+                        int(activation == "silu"), float(eps))
+
+
+def group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, activation: Optional[str] = None, eps: float = 1e-5):
+    """Group norm of a channels-last tensor.  Returns (y, mean, rstd).
+
+    z = (x - mean) rstd weight + bias, mean and rstd over a sample's positions
+    and the channels of a group; y = z, silu(z) (activation="silu") or
+    z silu(gate).  x and gate [N, ..., C], the dimensions between being the
+    positions ([N, C]: none, a norm over each group of channels of a row, as
+    over the heads of an attention's output); weight, bias [C] in x's dtype or
+    float32; mean, rstd float32 [N, groups], for the backward."""
+    p = _group_problem(x, groups, weight, bias, gate, activation, eps)
+    x, weight, bias, gate = _contig(x), _contig(weight), _contig(bias), _contig(gate)
+    _check_device(x, weight, bias, gate)
+    dev = x.device
+    y = torch.empty_like(x)
+    mean, rstd = (torch.empty(p.N, p.G, device=dev, dtype=torch.float32) for _ in range(2))
+    L = lib()
+    n = L.gdn_group_norm_fwd_workspace_size(ctypes.byref(p))
+    ws = _workspace(n, dev)
+    _call(L.gdn_group_norm_fwd, dev, ctypes.byref(p), _p(x), _p(weight), _p(bias), _p(gate), _p(y), _p(mean), _p(rstd),
+          _p(ws), n)
+    return y, mean, rstd
+
+
+def group_norm_bwd(dy, x, groups: int, weight, bias, mean, rstd, gate=None, activation: Optional[str] = None):
+    """Backward of group_norm_fwd, from its mean and rstd.  Returns (dx,
+    dweight, dbias, dgate), each None where its tensor is."""
+    p = _group_problem(x, groups, weight, bias, gate, activation, 0.0)
+    if dy is None or dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError(f"dy must have x's shape {list(x.shape)} and dtype {x.dtype}")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are required")
+    mean, rstd = _like(mean, (p.N, p.G), torch.float32, "mean"), _like(rstd, (p.N, p.G), torch.float32, "rstd")
+    x, dy, weight, bias, gate = (_contig(t) for t in (x, dy, weight, bias, gate))
+    _check_device(x, dy, weight, bias, gate, mean, rstd)
+    dev = x.device
+    dx, dw, db, dgate = (None if t is None else torch.empty_like(t) for t in (x, weight, bias, gate))
+    L = lib()
+    n = L.gdn_group_norm_bwd_workspace_size(ctypes.byref(p))
+    ws = _workspace(n, dev)
+    _call(L.gdn_group_norm_bwd, dev, ctypes.byref(p), _p(dy), _p(x), _p(weight), _p(bias), _p(gate), _p(mean),
           _p(rstd), _p(dx), _p(dw), _p(db), _p(dgate), _p(ws), n)
     return dx, dw, db, dgate

@@ -164,7 +164,8 @@ size_t gdn_chunk_fwd_noalloc_max_bytes(void);
  * The operators around the chunked gated delta rule in a sequence mixer: the
  * short causal convolution in front of it, the selective state-space scan
  * that takes the same place, the norm behind it, and all of them (and the
- * delta rule itself) for single tokens.
+ * delta rule itself) for single tokens; and linear attention with a decay for
+ * each head, which takes that place too, with the group norm over its heads.
  *
  * Layouts are token-major as above, T the total packed tokens with
  * cu_seqlens.  Weights and their gradients are in the type that
@@ -270,6 +271,46 @@ int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, co
                         const void *beta, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                         float *state, const int32_t *state_indices, int32_t slots, void *o, void *stream);
 
+/* Linear attention with a decay for each v-head: with the state S (K x V, fp32),
+ *   S_t = exp(log_decay) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t
+ *   q, k, dq, dk  [B, T, Hq, K]   problem dtype; v-head h reads head h / (Hv / Hq)
+ *   v, o, do, dv  [B, T, Hv, V]   problem dtype
+ *   log_decay     [Hv] fp32, a constant of the layer (no gradient): 0 keeps
+ *                 everything, -inf nothing; above 0 the state grows, and is
+ *                 computed as it is up to what fp32 holds
+ *   initial_state, final_state, dht, dh0 [N, Hv, K, V] fp32
+ * K, V in {32, 64, 128}.  q, k, v, o, do, dq, dk, dv and the states are 16-byte
+ * aligned, q_stride, k_stride, v_stride multiples of 16 bytes and (but for the
+ * step) below 2^24 elements.
+ * Held in fp32: the decays, the states and every sum over tokens.  In bf16
+ * problems the products inside a 64-token chunk and the state and its gradient
+ * as operands of o, dq, dk and dv are rounded to bf16.  A NaN or an infinity
+ * in a token's inputs reaches the other tokens of its chunk, earlier ones too,
+ * and all later ones of its sequence (backwards: all earlier ones); never
+ * another sequence. */
+typedef struct {
+  int32_t B, T, Hq, Hv, K, V, N, dtype;
+  float scale;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *cu_seqlens, *cu_seqlens_host;
+} gdn_attn_t;
+size_t gdn_linear_attention_fwd_workspace_size(const gdn_attn_t *p);
+size_t gdn_linear_attention_bwd_workspace_size(const gdn_attn_t *p);
+/* Required: q k v log_decay o; final_state NULL = not wanted. */
+int gdn_linear_attention_fwd(const gdn_attn_t *p, const void *q, const void *k, const void *v,
+                             const float *log_decay, const float *h0, void *o, float *ht, void *workspace,
+                             size_t ws_bytes, void *stream);
+/* Required: q k v log_decay do dq dk dv; dht NULL = zero, dh0 NULL = not wanted. */
+int gdn_linear_attention_bwd(const gdn_attn_t *p, const void *q, const void *k, const void *v,
+                             const float *log_decay, const float *h0, const void *d_o, const float *dht,
+                             void *dq, void *dk, void *dv, float *dh0, void *workspace, size_t ws_bytes,
+                             void *stream);
+/* One token of each batch row: q, k [B, Hq, K], v, o [B, Hv, V] (T = 1, N = B),
+ * state [slots, Hv, K, V] fp32 in place. */
+int gdn_linear_attention_step(const gdn_attn_t *p, const void *q, const void *k, const void *v,
+                              const float *log_decay, float *state, const int32_t *state_indices,
+                              int32_t slots, void *o, void *stream);
+
 /* Layer norm over the last dimension, with an optional output gate:
  *   z = (x - mean) rstd weight + bias,  y = z silu(gate)
  * rstd = (mean square of x - mean, + eps)^-1/2; with rms the mean is 0.
@@ -291,6 +332,31 @@ int gdn_layer_norm_bwd(const gdn_norm_t *p, const void *dy, const void *x, const
                        const void *bias, const void *gate, const float *mean, const float *rstd,
                        void *dx, void *dweight, void *dbias, void *dgate, void *workspace,
                        size_t ws_bytes, void *stream);
+
+/* Group norm over channels-last tensors, with an activation or an output gate:
+ *   z = (x - mean) rstd weight + bias,  y = z, z sigmoid(z) (silu) or z silu(gate)
+ * mean and rstd = (mean square of x - mean, + eps)^-1/2 are of a sample's S
+ * positions and the C / G channels of a group (S = 1: a norm over each head of
+ * a token).
+ *   x, gate, y, dy, dx, dgate [N, S, C] problem dtype, contiguous, C = G Dg
+ *   weight, bias [C] weight_dtype or NULL; dweight, dbias as these
+ *   mean, rstd [N, G] fp32 */
+typedef struct {
+  int64_t N, S;
+  int32_t G, Dg, dtype, weight_dtype, silu;
+  float eps;
+} gdn_group_t;
+/* Required: x y mean rstd; silu not with gate. */
+size_t gdn_group_norm_fwd_workspace_size(const gdn_group_t *p);
+int gdn_group_norm_fwd(const gdn_group_t *p, const void *x, const void *weight, const void *bias,
+                       const void *gate, void *y, float *mean, float *rstd, void *workspace, size_t ws_bytes,
+                       void *stream);
+/* Required: dy x mean rstd dx, dgate iff gate; dweight, dbias optional, each
+ * only with its weight or bias. */
+size_t gdn_group_norm_bwd_workspace_size(const gdn_group_t *p);
+int gdn_group_norm_bwd(const gdn_group_t *p, const void *dy, const void *x, const void *weight,
+                       const void *bias, const void *gate, const float *mean, const float *rstd, void *dx,
+                       void *dweight, void *dbias, void *dgate, void *workspace, size_t ws_bytes, void *stream);
 
 /* Number of context-parallel segments the forward would launch for this
  * problem (host-only planning query; 0 if invalid). */
