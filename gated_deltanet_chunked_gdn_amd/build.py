@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 SOURCES = ["gdn_api.cpp", "gdn_fwd.hip", "gdn_fwd_slice.hip", "gdn_bwd.hip", "gdn_rev_slice.hip", "gdn_grad_slice.hip", "gdn_selftest.hip",
            "gdn_mixer_api.cpp", "gdn_conv.hip", "gdn_norm.hip", "gdn_scan.hip",
-           "gdn_scan_mma.hip", "gdn_scan_bwd.hip", "gdn_step.hip", "gdn_linear.hip", "gdn_group.hip"]
+           "gdn_scan_mma.hip", "gdn_scan_bwd.hip", "gdn_step.hip", "gdn_linear.hip", "gdn_linear_mma.hip", "gdn_group.hip"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wno-unused-command-line-argument"]

@@ -1,6 +1,6 @@
 // Linear attention with a decay for each head (gdn_linear.hpp has the
-// formulas): the passes in fp32 matrix instructions, and what joins segments
-// and heads.
+// formulas): the passes of fp32 problems, in fp32 matrix instructions, and what
+// joins segments and heads.
 //
 // A workgroup has a segment of one head and 32 of the state's columns; chunks
 // of 32 tokens.  The state is in accumulators and, for the chunk that reads
@@ -230,34 +230,34 @@ __global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, in
 }
 
 // The segments of a sequence in order, 4 elements of the state a thread: each
-// slot gets the state that its segment begins with.
+// slot but the first of a sequence gets the state that its segment begins with.
 template <bool REV>
 __device__ __forceinline__ void carry(const AttnArgs &a, const Layout &w, int64_t i) {
   const int64_t kv4 = (int64_t)a.K * a.V / 4, heads = i / kv4;
   if (heads >= (int64_t)a.s.N * a.Hv) return;
   const int h = (int)(heads % a.Hv), n = (int)(heads / a.Hv);
   const Span sp = seq_span(a.s, n);
-  const int64_t ns = segs_of(sp, a.seg), step = a.Hv * kv4;
+  const int64_t ns = segs_of(sp, a.seg), step = (REV ? -1 : 1) * a.Hv * kv4;
+  if (ns == 1) return;
   f32x4 *at = reinterpret_cast<f32x4 *>(REV ? w.zend(a) : w.start(a)) + (first_slot(a.s, sp, n, a.seg) * a.Hv + h) * kv4 + i % kv4;
+  if (REV) at -= (ns - 1) * step;
   const f32x4 *given = reinterpret_cast<const f32x4 *>(REV ? a.dht : a.h0);
   f32x4 cur = given ? given[i] : zero4();
   const float g2 = log2_decay(a.g[h]), whole = power(g2, a.seg);
-  const float rest = REV ? power(g2, (int)(sp.end - sp.first - (ns - 1) * a.seg)) : whole;  // of the sequence's last segment
-  for (int64_t s0 = 0; s0 < ns; s0 += kAhead) {
-    f32x4 add[kAhead];
+  // of the first segment on the way: backwards the sequence's last
+  float d = REV ? power(g2, (int)(sp.end - sp.first - (ns - 1) * a.seg)) : whole;
+  f32x4 add[kAhead + 1];  // (a slot is read before what the segment begins with takes its place)
+  add[kAhead] = at[0];
+  for (int64_t s0 = 0; s0 < ns - 1; s0 += kAhead) {
+    add[0] = add[kAhead];
+#pragma unroll
+    for (int j = 1; j <= kAhead; ++j) add[j] = s0 + j < ns - 1 ? at[(s0 + j) * step] : zero4();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      // (the last one's own part is not wanted)
-      const int64_t s = s0 + j < ns - 1 ? s0 + j : -1;
-      add[j] = s >= 0 ? at[(REV ? ns - 1 - s : s) * step] : zero4();
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int64_t s = s0 + j;
-      if (s >= ns) break;
-      at[(REV ? ns - 1 - s : s) * step] = cur;
-      const float d = REV && s == 0 ? rest : whole;
+      if (s0 + j >= ns - 1) break;
       cur = cur * d + add[j];
+      at[(s0 + j + 1) * step] = cur;
+      d = whole;
     }
   }
 }
@@ -319,7 +319,10 @@ hipError_t pick(const AttnArgs &a, const Layout &w, hipStream_t st) {
 }
 template <int WHAT>
 hipError_t pass(const AttnArgs &a, const Layout &w, hipStream_t st) {
-  return a.dtype == 1 ? pick<bf16, WHAT>(a, w, st) : pick<float, WHAT>(a, w, st);
+  if (a.dtype != 1) return pick<float, WHAT>(a, w, st);
+  if (WHAT == kForward) return launch_mma_out(a, w, st);
+  if (WHAT == kGrads) return launch_mma_grads(a, w, st);
+  return launch_mma_local(a, w, WHAT == kLocals, st);
 }
 
 unsigned carry_blocks(const AttnArgs &a) {
@@ -329,13 +332,12 @@ unsigned carry_blocks(const AttnArgs &a) {
 }  // namespace
 }  // namespace attn
 
-// Segments: as long as the whole sequence unless that leaves compute units
-// without two workgroups each; then as many as give each so many.
+// Segments: as long as the whole batch unless that leaves compute units without
+// work, then as many as give each a workgroup (fp32: two, of half the waves).
 AttnPlan attn_plan(const AttnArgs &a0, bool bwd) {
   AttnArgs a = a0;
   const int64_t per = (int64_t)a.Hv * (a.V / 32);  // workgroups a segment
-  int64_t want = (compute_units() * 2 + per - 1) / per;
-  if (want < a.s.N) want = a.s.N;
+  const int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 2) + per - 1) / per;
   int64_t seg = (a.s.tokens + want - 1) / want;
   seg = (seg + 63) / 64 * 64;
   if (seg < 64) seg = 64;

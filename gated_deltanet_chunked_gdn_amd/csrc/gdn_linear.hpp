@@ -33,7 +33,8 @@ using scan::SlotLoc;
 struct Layout {
   size_t o_start = 0, o_zend = 0, o_dq = 0, o_dk = 0, total = 0;
   __host__ __device__ float *at(const AttnArgs &a, size_t o) const { return reinterpret_cast<float *>(a.ws + o); }
-  // fp32 [slots][Hv][K][V]: what a segment adds to the state, then its start state
+  // fp32 [slots][Hv][K][V]: what a segment adds to the state, then (but for a
+  // sequence's first) its start state
   __host__ __device__ float *start(const AttnArgs &a) const { return at(a, o_start); }
   // the same of Z: what a segment adds, then Z behind its last token
   __host__ __device__ float *zend(const AttnArgs &a) const { return at(a, o_zend); }
@@ -100,7 +101,8 @@ __device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, in
   p.scale_in = p.rev ? 1.f : a.scale;
   p.scale_up = p.rev ? a.scale : 1.f;
   const float *given = p.rev ? a.dht : a.h0;
-  p.start = a.one_seg ? (given ? given + state : nullptr) : (p.rev ? w.zend(a) : w.start(a)) + at;
+  // (where the sequence begins, what the call gives; the carry writes the others')
+  p.start = (p.rev ? loc.last : loc.index == 0) ? (given ? given + state : nullptr) : (p.rev ? w.zend(a) : w.start(a)) + at;
   p.last = nullptr;
   // a v-head's part of a q-head's gradient, or the gradient itself
   auto shared = [&](void *d, float *parts) {
@@ -133,6 +135,11 @@ __device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, in
   }
   return p;
 }
+
+// bf16, gdn_linear_mma.hip
+hipError_t launch_mma_local(const AttnArgs &a, const Layout &w, bool both, hipStream_t st);
+hipError_t launch_mma_out(const AttnArgs &a, const Layout &w, hipStream_t st);
+hipError_t launch_mma_grads(const AttnArgs &a, const Layout &w, hipStream_t st);
 
 }  // namespace attn
 }  // namespace gdn

@@ -211,11 +211,11 @@ int check_attn(const gdn_attn_t *p, bool step, bool bwd, gdn::AttnArgs *a) {
   a->qs = qs;
   a->ks = ks;
   a->vs = vs;
-  // (a launch has fewer than 2^32 threads: up to twelve workgroups of 256 a
+  // (a launch has fewer than 2^32 threads: up to twelve workgroups of 768 a
   // slot and head, two threads for four elements of a state, one for four of dq)
   constexpr int64_t kBlocks = (int64_t)1 << 24;
   const int64_t heads = (int64_t)p->Hv * (step ? 0 : gdn::attn_plan(*a, bwd).slots);
-  if (a->s.tokens * p->Hv * 128 > ((int64_t)1 << 40) || (int64_t)a->s.N * p->Hv >= kGrid || heads * 12 >= kBlocks ||
+  if (a->s.tokens * p->Hv * 128 > ((int64_t)1 << 40) || (int64_t)a->s.N * p->Hv >= kGrid || heads * 36 >= kBlocks ||
       (!step && ((int64_t)a->s.N * p->Hv * p->K * p->V / 512 >= kBlocks || (bwd && a->s.tokens * p->Hq * p->K / 1024 >= kBlocks))))
     return set_error(GDN_ERR_UNSUPPORTED, "problem too large");
   return GDN_OK;
