@@ -197,7 +197,7 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
 }
 
 template <typename E, int K, int V, int WHAT>
-__global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, int64_t per) {
+__global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, int64_t slots, int64_t per) {
   constexpr int D = K > V ? K : V;
   __shared__ __align__(16) char mem[sizeof(Lds<(WHAT == kGrads ? D : K)>)];
   const int64_t part = blockIdx.x / per, item = blockIdx.x % per;
@@ -210,12 +210,13 @@ __global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, in
   const int64_t head = unit / slices;
   const int c0 = (int)(unit % slices) * 32, h = (int)(head % a.Hv);
   const int64_t slot = head / a.Hv;
-  if (slot >= a.slots) return;
-  const SlotLoc loc = locate(a.s, a.seg, slot);
+  if (slot >= slots) return;
+  constexpr bool LOCAL = WHAT == kLocal || WHAT == kLocals;
+  const SlotLoc loc = locate(a.s, LOCAL ? a.seg / a.parts : a.seg, slot);
   if (!loc.used) return;
-  Pass p = make_pass<E>(a, w, kind, loc, slot, h);
-  if constexpr (WHAT == kLocal || WHAT == kLocals) {
-    if (p.rev ? loc.index == 0 : loc.last) return;
+  Pass p = make_pass<E>(a, w, kind, loc, h);
+  if constexpr (LOCAL) {
+    if (!carried(a, loc, p.rev)) return;
     // the state is built of b and c
     float *dst = (p.rev ? w.zend(a) : w.start(a)) + (slot * a.Hv + h) * (int64_t)K * V;
     sweep<E, K, V, false>(a, p, loc, dst, h, c0, *reinterpret_cast<Lds<K> *>(mem));
@@ -229,44 +230,49 @@ __global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, in
   }
 }
 
-// The segments of a sequence in order, 4 elements of the state a thread: each
-// slot but the first of a sequence gets the state that its segment begins with.
+// The parts of a sequence's segments in order, 4 elements of the state a thread:
+// where a segment but the sequence's first begins (backwards: but its last ends),
+// its part gets the state there.
 template <bool REV>
 __device__ __forceinline__ void carry(const AttnArgs &a, const Layout &w, int64_t i) {
   const int64_t kv4 = (int64_t)a.K * a.V / 4, heads = i / kv4;
-  if (heads >= (int64_t)a.s.N * a.Hv) return;
-  const int h = (int)(heads % a.Hv), n = (int)(heads / a.Hv);
+  const int h = (int)(heads % a.Hv), n = (int)(heads / a.Hv), sub = a.seg / a.parts;
   const Span sp = seq_span(a.s, n);
-  const int64_t ns = segs_of(sp, a.seg), step = (REV ? -1 : 1) * a.Hv * kv4;
-  if (ns == 1) return;
-  f32x4 *at = reinterpret_cast<f32x4 *>(REV ? w.zend(a) : w.start(a)) + (first_slot(a.s, sp, n, a.seg) * a.Hv + h) * kv4 + i % kv4;
+  const int64_t segs = segs_of(sp, a.seg), ns = segs_of(sp, sub), step = (REV ? -1 : 1) * a.Hv * kv4;
+  // parts on the way, and the last that a state is written to
+  const int64_t last = REV ? ns - a.parts : (segs - 1) * a.parts;
+  if (segs == 1) return;
+  f32x4 *at = reinterpret_cast<f32x4 *>(REV ? w.zend(a) : w.start(a)) + (first_slot(a.s, sp, n, sub) * a.Hv + h) * kv4 + i % kv4;
   if (REV) at -= (ns - 1) * step;
   const f32x4 *given = reinterpret_cast<const f32x4 *>(REV ? a.dht : a.h0);
   f32x4 cur = given ? given[i] : zero4();
-  const float g2 = log2_decay(a.g[h]), whole = power(g2, a.seg);
-  // of the first segment on the way: backwards the sequence's last
-  float d = REV ? power(g2, (int)(sp.end - sp.first - (ns - 1) * a.seg)) : whole;
-  f32x4 add[kAhead + 1];  // (a slot is read before what the segment begins with takes its place)
+  const float g2 = log2_decay(a.g[h]), whole = power(g2, sub);
+  // of the first part on the way: backwards the sequence's last
+  float d = REV ? power(g2, (int)(sp.end - sp.first - (ns - 1) * sub)) : whole;
+  // a part is read before a state takes its place
+  f32x4 add[kAhead + 1];
   add[kAhead] = at[0];
-  for (int64_t s0 = 0; s0 < ns - 1; s0 += kAhead) {
+  for (int64_t s0 = 0; s0 < last; s0 += kAhead) {
     add[0] = add[kAhead];
 #pragma unroll
-    for (int j = 1; j <= kAhead; ++j) add[j] = s0 + j < ns - 1 ? at[(s0 + j) * step] : zero4();
+    for (int j = 1; j <= kAhead; ++j) add[j] = s0 + j < last ? at[(s0 + j) * step] : zero4();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (s0 + j >= ns - 1) break;
+      const int64_t s = s0 + j + 1;  // the part that follows
+      if (s > last) break;
       cur = cur * d + add[j];
-      at[(s0 + j + 1) * step] = cur;
+      if ((REV ? ns - s : s) % a.parts == 0) at[s * step] = cur;
       d = whole;
     }
   }
 }
 __global__ __launch_bounds__(256) void carry_kernel(AttnArgs a, Layout w, int64_t blocks) {
-  const int64_t b = blockIdx.x;
+  const int64_t b = blockIdx.x, i = b % blocks * 256 + threadIdx.x;
+  if (i >= (int64_t)a.s.N * a.Hv * a.K * a.V / 4) return;
   if (b < blocks)
-    carry<false>(a, w, b * 256 + threadIdx.x);
+    carry<false>(a, w, i);
   else
-    carry<true>(a, w, (b - blocks) * 256 + threadIdx.x);
+    carry<true>(a, w, i);
 }
 
 // dq, dk of a q-head: the sum over its v-heads, 4 elements a thread.  (Tokens
@@ -297,10 +303,11 @@ __global__ __launch_bounds__(256) void group_kernel(AttnArgs a, Layout w) {
 template <typename E, int K, int V, int WHAT>
 hipError_t go(const AttnArgs &a, const Layout &w, hipStream_t st) {
   const int most = WHAT == kGrads && K > V ? K : V;
-  const int64_t per = a.slots * a.Hv * (most / 32);
+  const int64_t slots = WHAT == kLocal || WHAT == kLocals ? scan::slots_of(a.s, a.seg / a.parts) : a.slots;
+  const int64_t per = slots * a.Hv * (most / 32);
   const int parts = WHAT == kGrads ? 3 : WHAT == kLocals ? 2 : 1;
   KernelTimer kt(WHAT == kGrads ? "attn_grads" : WHAT == kForward ? "attn_out" : "attn_local", st);
-  pass_kernel<E, K, V, WHAT><<<(unsigned)(per * parts), kThreads, 0, st>>>(a, w, per);
+  pass_kernel<E, K, V, WHAT><<<(unsigned)(per * parts), kThreads, 0, st>>>(a, w, slots, per);
   return hipGetLastError();
 }
 template <typename E, int WHAT>
@@ -332,19 +339,73 @@ unsigned carry_blocks(const AttnArgs &a) {
 }  // namespace
 }  // namespace attn
 
-// Segments: as long as the whole batch unless that leaves compute units without
-// work, then as many as give each a workgroup (fp32: two, of half the waves).
+namespace attn {
+namespace {
+
+// Segments of bf16 problems, and the columns that a workgroup has: what takes the
+// least by a model of the passes' time in us (measured at K = V = 128).  A step of
+// 64 tokens takes a workgroup, one a compute unit, 1.6 with 64 columns and 1.2 with
+// 32, as long as the longest segment has steps or the work fills the chip;
+// cutting sequences costs the launches for the states and reading k and v again.
+// (8192 tokens, 64 heads: 64 columns, one segment 185 and two 171, 32 columns one
+// segment 162, two 222.  2 x 4096 tokens, 32 heads, backward: 64 columns, one
+// segment 178 and two 223, 32 columns 229.  Packed, 16 sequences, 32 heads: 64
+// columns 170, 32 columns 226.)  Where the device alone knows the sequences'
+// lengths, the longest is taken to be four times the mean.
+AttnPlan plan_mma(const AttnArgs &a, bool bwd) {
+  const double cus = (double)compute_units(), steps = (double)a.s.tokens / 64, passes = bwd ? 3 : 1;
+  double longest = (double)a.longest;
+  if (a.s.cu && a.longest == a.s.T && longest > 4. * a.s.T / a.s.N) longest = 4. * a.s.T / a.s.N;
+  AttnPlan best = {};
+  double least = 1e300;
+  for (int cols = a.V < 64 ? 32 : 64; cols >= 32; cols /= 2) {
+    const double wgs = (double)a.Hv * (a.V / cols);
+    for (int64_t cuts = 1; cuts == 1 || cuts < 2 * a.longest / 64; cuts *= 2) {
+      int64_t seg = (a.longest + cuts - 1) / cuts;
+      const int parts = cuts > 1 && seg >= 512 ? 4 : 1;
+      const int64_t unit = 64 * parts;
+      seg = (seg + unit - 1) / unit * unit;
+      if (seg < unit) seg = unit;
+      if (seg > INT32_MAX) continue;
+      const double segment = longest < (double)seg ? longest : (double)seg;
+      const double full = steps * wgs * passes / cus, most = segment / 64 > full ? segment / 64 : full;
+      double t = most * (cols == 64 ? 1.6 : 1.2);
+      if (cuts > 1) t += 12 + (bwd ? 2 : 1) * steps * a.Hv * a.V / 64 / cus * (1. - 1. / cuts) * 1.3;
+      if (t < least) {
+        least = t;
+        best.seg = (int)seg;
+        best.parts = parts;
+        best.cols = cols;
+        best.one_seg = cuts == 1;
+      }
+    }
+  }
+  return best;
+}
+// fp32: segments as long as the whole batch unless that leaves compute units
+// without two workgroups each.
+AttnPlan plan_f32(const AttnArgs &a) {
+  const int64_t per = (int64_t)a.Hv * (a.V / 32);  // workgroups a segment
+  const int64_t want = (compute_units() * 2 + per - 1) / per;
+  int64_t seg = ((a.s.tokens + want - 1) / want + 63) / 64 * 64;
+  AttnPlan p;
+  p.seg = seg < 64 ? 64 : seg > INT32_MAX - 63 ? INT32_MAX / 64 * 64 : (int)seg;
+  p.parts = 1;
+  p.cols = 32;
+  p.one_seg = a.longest <= p.seg;
+  return p;
+}
+
+}  // namespace
+}  // namespace attn
+
 AttnPlan attn_plan(const AttnArgs &a0, bool bwd) {
   AttnArgs a = a0;
-  const int64_t per = (int64_t)a.Hv * (a.V / 32);  // workgroups a segment
-  const int64_t want = (compute_units() * (a.dtype == 1 ? 1 : 2) + per - 1) / per;
-  int64_t seg = (a.s.tokens + want - 1) / want;
-  seg = (seg + 63) / 64 * 64;
-  if (seg < 64) seg = 64;
-  AttnPlan p;
-  p.seg = (int)seg;
+  AttnPlan p = a.dtype == 1 ? attn::plan_mma(a, bwd) : attn::plan_f32(a);
+  a.seg = p.seg;
+  a.parts = p.parts;
   a.slots = p.slots = scan::slots_of(a.s, p.seg);
-  a.one_seg = p.one_seg = a.s.T <= seg;
+  a.one_seg = p.one_seg;
   p.ws = attn::layout(a, bwd).total;
   return p;
 }

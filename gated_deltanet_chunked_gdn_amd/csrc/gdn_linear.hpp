@@ -33,10 +33,11 @@ using scan::SlotLoc;
 struct Layout {
   size_t o_start = 0, o_zend = 0, o_dq = 0, o_dk = 0, total = 0;
   __host__ __device__ float *at(const AttnArgs &a, size_t o) const { return reinterpret_cast<float *>(a.ws + o); }
-  // fp32 [slots][Hv][K][V]: what a segment adds to the state, then (but for a
-  // sequence's first) its start state
+  // fp32 [sub slots][Hv][K][V], a sub slot a part of a segment: what it adds to
+  // the state; then, in a segment's first but not a sequence's, the state that the
+  // segment begins with
   __host__ __device__ float *start(const AttnArgs &a) const { return at(a, o_start); }
-  // the same of Z: what a segment adds, then Z behind its last token
+  // the same of Z; then, in a segment's last part but not a sequence's, Z behind it
   __host__ __device__ float *zend(const AttnArgs &a) const { return at(a, o_zend); }
   // fp32 [tokens][Hv][K] each: the v-heads' parts of dq and dk where they share heads
   __host__ __device__ float *dq_part(const AttnArgs &a) const { return at(a, o_dq); }
@@ -51,7 +52,7 @@ inline Layout layout(const AttnArgs &a, bool bwd) {
     off = (off + bytes + 255) & ~(size_t)255;
     return o;
   };
-  const size_t states = (size_t)a.slots * a.Hv * a.K * a.V * 4;
+  const size_t states = a.one_seg ? 0 : (size_t)scan::slots_of(a.s, a.seg / a.parts) * a.Hv * a.K * a.V * 4;
   if (!a.one_seg) {
     w.o_start = piece(states);
     if (bwd) w.o_zend = piece(states);
@@ -72,6 +73,14 @@ __device__ __forceinline__ float power(float g2, int n) { return __builtin_amdgc
 
 enum PassKind { kO, kDq, kDk, kDv };
 
+// Whether a part of a segment goes into the carry: of S those before a sequence's
+// last segment, of Z those behind its first.
+__device__ __forceinline__ bool carried(const AttnArgs &a, const SlotLoc &sub, bool rev) {
+  if (rev) return sub.index >= a.parts;
+  const Span sp = seq_span(a.s, sub.n);
+  return sub.index < (segs_of(sp, a.seg) - 1) * a.parts;
+}
+
 // One pass, for one v-head and segment.
 struct Pass {
   const void *a, *b, *c;      // at the head's first element of token 0
@@ -87,12 +96,12 @@ struct Pass {
 };
 
 template <typename E>
-__device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, int kind, const SlotLoc &loc, int64_t slot, int h) {
+__device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, int kind, const SlotLoc &loc, int h) {
   const int hq = h / (a.Hv / a.Hq);
   const int64_t kv = (int64_t)a.K * a.V, os = (int64_t)a.Hv * a.V;
   const E *q = static_cast<const E *>(a.q) + (int64_t)hq * a.K, *k = static_cast<const E *>(a.k) + (int64_t)hq * a.K;
   const E *v = static_cast<const E *>(a.v) + (int64_t)h * a.V, *dO = static_cast<const E *>(a.dO) + (int64_t)h * a.V;
-  const int64_t state = (loc.n * (int64_t)a.Hv + h) * kv, at = (slot * a.Hv + h) * kv;
+  const int64_t state = (loc.n * (int64_t)a.Hv + h) * kv;
   Pass p;
   p.part = a.Hv != a.Hq;
   p.rev = kind == kDk || kind == kDv;
@@ -102,7 +111,13 @@ __device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, in
   p.scale_up = p.rev ? a.scale : 1.f;
   const float *given = p.rev ? a.dht : a.h0;
   // (where the sequence begins, what the call gives; the carry writes the others')
-  p.start = (p.rev ? loc.last : loc.index == 0) ? (given ? given + state : nullptr) : (p.rev ? w.zend(a) : w.start(a)) + at;
+  if (p.rev ? loc.last : loc.index == 0) {
+    p.start = given ? given + state : nullptr;
+  } else {
+    const int sub = a.seg / a.parts;
+    const int64_t at = first_slot(a.s, seq_span(a.s, loc.n), loc.n, sub) + (p.rev ? (loc.index + 1) * a.parts - 1 : loc.index * a.parts);
+    p.start = (p.rev ? w.zend(a) : w.start(a)) + (at * a.Hv + h) * kv;
+  }
   p.last = nullptr;
   // a v-head's part of a q-head's gradient, or the gradient itself
   auto shared = [&](void *d, float *parts) {

@@ -34,7 +34,7 @@ namespace {
 // Row pitches in LDS: 32 bytes over a multiple of 64.  16-byte reads of 16 rows
 // then take 4 clocks and transpose reads of 32 bytes of 16 rows 1.4 (with 16
 // bytes over: 8 and 2.1).
-constexpr int VP = 48;  // of c's 32 columns
+constexpr int pitch(int columns) { return columns + 16; }
 typedef Mma<bf16> M;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 __device__ __forceinline__ bf16x4 tr4(const bf16 *p) { return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)p); }
@@ -42,13 +42,17 @@ __device__ __forceinline__ bf16x8 join(const bf16x4 &a, const bf16x4 &b) {
   return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// A pass's two chunks.  s: the state that enters it, a column a row, in the order
-// 16 ((v >> 2) & 1) + 4 (v >> 3) + (v & 3) (what the lanes of an output tile
-// take); w: u c in PARTS bf16 numbers.
-template <int DA, bool OUT, int PARTS>
+// The output's columns, VS of them, are dealt to a tile's rows: row 4 q + e of tile
+// t is column 32 (t / 2) + 8 q + 4 (t % 2) + e, so that a lane ends with runs of
+// eight.  Row of a column in this order:
+__device__ __forceinline__ int dealt(int v) { return 32 * (v >> 5) + 16 * ((v >> 2) & 1) + 4 * ((v >> 3) & 3) + (v & 3); }
+
+// A pass's two chunks.  s: the state that enters it, a column a row, dealt; w: u c
+// in PARTS bf16 numbers.
+template <int DA, int VS, bool OUT, int PARTS_>
 struct Lds {
-  static constexpr int P = DA + 16;
-  bf16 b[2][64 * P], c[2][OUT ? 64 * VP : 8], s[2][OUT ? 32 * P : 8], w[2][PARTS][64 * VP];
+  static constexpr int PARTS = PARTS_, P = pitch(DA), VP = pitch(VS), BUFS = OUT ? 2 : 1;
+  bf16 b[BUFS][64 * P], c[2][OUT ? 64 * VP : 8], s[2][OUT ? VS * P : 8], w[BUFS][PARTS][64 * VP];
 };
 
 // A segment's chunks in the order of a pass.
@@ -92,9 +96,11 @@ struct Stream {
 // ---- the outputs' waves
 
 // ND: blocks of 16 tokens j that the wave's tokens see.
-template <int DA, int ND, typename L>
+// PART: the output is fp32, a v-head's part (a branch around stores, which may
+// then be none, makes the compiler wait for loads of the step after).
+template <int DA, int VS, int ND, bool PART, typename L>
 __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2, int c0, int ib, const L &lds) {
-  constexpr int P = L::P, KS = DA / 32;
+  constexpr int P = L::P, VP = L::VP, KS = DA / 32, OT = VS / 16;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4, i = 16 * ib + l16;
   const bool rev = way.rev;
   float wt[ND][4];  // l^{|i-j|} of the blocks at 0, 1, .. from the wave's own
@@ -108,8 +114,9 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
   struct In {
     uint4 q[KS];
   };
-  Stream from(way, p.a, p.as, 0, DA, 2), to(way, p.out, p.os, c0, 32, p.part ? 4 : 2);
-  const int a_off = (int)(i * p.as * 2 + 16 * g), o_off = (int)((i * p.os + 8 * g) * (p.part ? 4 : 2));
+  Stream from(way, p.a, p.as, 0, DA, 2), to(way, p.out, p.os, c0, VS, PART ? 4 : 2);
+  const int a_off = (int)(i * p.as * 2 + 16 * g), o_off = (int)((i * p.os + 8 * g) * (PART ? 4 : 2));
+  const int o_line = (int)(((16 * ib + (l16 & 7)) * p.os + 8 * g) * 2 + (l16 & 8 ? 64 : 0));
   auto fetch = [&](In &in) {
     const auto r = from.next();
 #pragma unroll
@@ -120,17 +127,19 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
   const float in_rest = rev ? power(g2, way.rest() - 1 - i > 0 ? way.rest() - 1 - i : 0) * p.scale_in : in_whole;
   auto work = [&](In &in, int step) {
     const bf16 *b = lds.b[step & 1], *c = lds.c[step & 1], *s = lds.s[step & 1];
-    f32x4 O[2] = {zero4(), zero4()}, pd[ND];
+    f32x4 O[OT], pd[ND];
+#pragma unroll
+    for (int t = 0; t < OT; ++t) O[t] = zero4();
 #pragma unroll
     for (int d = 0; d < ND; ++d) pd[d] = zero4();
     // operands from LDS, a step ahead of the products that take them (left to
     // itself the compiler reads one after the other, each waited for)
-    bf16x8 m[2][ND + 2], cf[(ND + 1) / 2][2];
+    bf16x8 m[2][ND + OT], cf[(ND + 1) / 2][OT];
     auto read = [&](int k) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) m[k & 1][d] = M::ld(b + (16 * (rev ? ib + d : ib - d) + l16) * P + 32 * k + 8 * g);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) m[k & 1][ND + t] = M::ld(s + (16 * t + l16) * P + 32 * k + 8 * g);
+      for (int t = 0; t < OT; ++t) m[k & 1][ND + t] = M::ld(s + (16 * t + l16) * P + 32 * k + 8 * g);
     };
     read(0);
 #pragma unroll
@@ -138,13 +147,15 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
       if (k + 1 < KS) {
         read(k + 1);
       } else {
-        // row 4 q + e of tile t: column 8 q + 4 t + e
         const bf16 *at = c + (4 * g + (l16 >> 2)) * VP + 8 * (l16 & 3);
 #pragma unroll
         for (int d = 0; d < ND; d += 2) {
           const int j0 = rev ? ib + d : ib - d, j1 = d + 1 == ND ? j0 : rev ? j0 + 1 : j0 - 1;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) cf[d / 2][t] = join(tr4(at + 16 * j0 * VP + 4 * t), tr4(at + 16 * j1 * VP + 4 * t));
+          for (int t = 0; t < OT; ++t) {
+            const int col = 32 * (t >> 1) + 4 * (t & 1);
+            cf[d / 2][t] = join(tr4(at + 16 * j0 * VP + col), tr4(at + 16 * j1 * VP + col));
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -152,13 +163,13 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
 #pragma unroll
       for (int d = 0; d < ND; ++d) pd[d] = M::mma(m[k & 1][d], q, pd[d]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) O[t] = M::mma(m[k & 1][ND + t], q, O[t]);
+      for (int t = 0; t < OT; ++t) O[t] = M::mma(m[k & 1][ND + t], q, O[t]);
       __builtin_amdgcn_sched_barrier(0);
     }
     fetch(in);
     const float pin = way.part(step) ? in_rest : in_whole;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < OT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) O[t][r] *= pin;
 #pragma unroll
@@ -170,17 +181,39 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
         w[4 + r] = d + 1 < ND ? (bf16)(pd[d + 1 < ND ? d + 1 : d][r] * wt[d + 1 < ND ? d + 1 : d][r]) : (bf16)0.f;
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) O[t] = M::mma(cf[d / 2][t], w, O[t]);
+      for (int t = 0; t < OT; ++t) O[t] = M::mma(cf[d / 2][t], w, O[t]);
     }
     const auto r = to.next();
-    if (p.part) {
+    if constexpr (PART) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) buf_store16(__builtin_bit_cast(uint4, O[t]), r, (uint32_t)(o_off + 16 * t));
+      for (int t = 0; t < OT; ++t)
+        buf_store16(__builtin_bit_cast(uint4, O[t]), r, (uint32_t)(o_off + 128 * (t >> 1) + 16 * (t & 1)));
+      return;
+    }
+    uint4 o[OT / 2];
+#pragma unroll
+    for (int v = 0; v < OT / 2; ++v) {
+      bf16x8 x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (bf16)O[2 * v + (e >> 2)][e & 3];
+      o[v] = __builtin_bit_cast(uint4, x);
+    }
+    if constexpr (OT == 2) {
+      buf_store16(o[0], r, (uint32_t)o_off);
     } else {
-      bf16x8 o;
+      // lanes i and i + 8 of a group exchange halves of their rows, so that a store
+      // writes whole 128-byte lines of eight rows
+      const bool low = l16 < 8;
+      uint4 give, own, got;
+      const uint32_t *a0 = &o[0].x, *a1 = &o[1].x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (bf16)O[e >> 2][e & 3];
-      buf_store16(__builtin_bit_cast(uint4, o), r, (uint32_t)o_off);
+      for (int e = 0; e < 4; ++e) {
+        (&own.x)[e] = low ? a0[e] : a1[e];
+        (&give.x)[e] = low ? a1[e] : a0[e];
+        (&got.x)[e] = __builtin_bit_cast(uint32_t, dpp_mov<0x128>(__builtin_bit_cast(float, (&give.x)[e])));  // row_ror:8
+      }
+      buf_store16(low ? own : got, r, (uint32_t)o_line);
+      buf_store16(low ? got : own, r, (uint32_t)(o_line + 16 * p.os));
     }
   };
   In x, y;
@@ -203,42 +236,44 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
 
 // ---- the state's waves
 
-// OUT: beside the outputs' waves, which read the state of every chunk.  EXACT:
-// the state is wanted to fp32.  NS waves.
-template <int DA, int NS, bool OUT, bool EXACT>
-__device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, int DC, int c0, int tid, float *dst,
-                                       Lds<DA, OUT, EXACT ? 3 : 1> &lds) {
-  constexpr int P = Lds<DA, OUT, EXACT ? 3 : 1>::P, PARTS = EXACT ? 3 : 1, T = 64 * NS;
-  constexpr int KT = (DA / 8 + NS - 1) / NS;               // tiles of 16 x 16
+// OUT: beside the outputs' waves, which read the state of every chunk.  From step
+// `exact` on the state is held to fp32 (L::PARTS = 1: never).
+template <int DA, int VS, bool OUT, typename L>
+__device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, int DC, int c0, int exact, int tid, float *dst, L &lds) {
+  constexpr int P = L::P, VP = L::VP, PARTS = L::PARTS, NS = 8, T = 64 * NS;
+  // tiles of 16 x 16: KT rows by CT columns of them a wave, KW waves side by side
+  // over the rows
+  constexpr int CT = VS == 64 && DA >= 64 ? 2 : 1, CW = VS / 16 / CT, KW = NS / CW, KT = (DA / 16 + KW - 1) / KW;
   constexpr int NB = (64 * DA / 8 + T - 1) / T;            // pieces of b's rows, 8 elements each
-  constexpr int NC = 2048 / T;                             // elements of c
+  constexpr int NC = 64 * VS / T;                          // elements of c
   typedef uint32_t piece __attribute__((ext_vector_type(NC / 2)));
   static_assert(NC == 4 || NC == 8, "of one row");
-  const int lane = tid & 63, wave = wave_of(tid), l16 = lane & 15, g = lane >> 4, ct = wave & 1;
-  const bool rev = way.rev, tiles = wave < DA / 8;
-  // this wave's tiles: rows 16 kt + 4 g + e of column 16 ct + l16
-  auto kt = [&](int i) { return (wave + NS * i) >> 1; };
-  auto state_io = [&](f32x4(&S)[KT], float *ptr, bool store) {
+  const int lane = tid & 63, wave = wave_of(tid), l16 = lane & 15, g = lane >> 4, ct = wave % CW * CT;
+  const bool rev = way.rev, tiles = wave / CW < DA / 16;
+  // this wave's tiles: rows 16 kt(i) + 4 g + e of column 16 (ct + j) + l16
+  auto kt = [&](int i) { return wave / CW + KW * i; };
+  auto state_io = [&](f32x4(&S)[KT][CT], float *ptr, bool store) {
     const int64_t sr = p.tr ? 1 : DC, sc = p.tr ? DA : 1;
-    ptr += (c0 + 16 * ct + l16) * sc;
     if (!tiles) return;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float *at = ptr + (16 * kt(i) + 4 * g + e) * sr;
-        if (store)
-          *at = S[i][e];
-        else
-          S[i][e] = *at;
-      }
+      for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float *at = ptr + (16 * kt(i) + 4 * g + e) * sr + (c0 + 16 * (ct + j) + l16) * sc;
+          if (store)
+            *at = S[i][j][e];
+          else
+            S[i][j][e] = *at;
+        }
   };
   struct In {
     uint4 b[NB];
     piece c;
   };
-  const int crow = tid * NC / 32, ccol = tid * NC % 32;
-  Stream from_b(way, p.b, p.bs, 0, DA, 2), from_c(way, p.c, p.cs, c0, 32, 2);
+  const int crow = tid * NC / VS, ccol = tid * NC % VS;
+  Stream from_b(way, p.b, p.bs, 0, DA, 2), from_c(way, p.c, p.cs, c0, VS, 2);
   int b_off[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
@@ -260,23 +295,30 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
   const float u_whole = power(g2, up) * p.scale_up, u_rest = power(g2, up_rest > 0 ? up_rest : 0) * p.scale_up;
   const float all_whole = power(g2, 64), all_rest = power(g2, way.rest());
   auto commit = [&](const In &in, int step) {
-    const int buf = step & 1;
+    const int buf = OUT ? step & 1 : 0;
     const float u = way.part(step) ? u_rest : u_whole;
     bf16 *at = lds.w[buf][0] + crow * VP + ccol;
     typedef bf16 els __attribute__((ext_vector_type(NC)));
     const els c = __builtin_bit_cast(els, in.c);
-    els w[PARTS];
+    els w;
+    float f[NC];
 #pragma unroll
     for (int e = 0; e < NC; ++e) {
-      float f = (float)c[e] * u;
+      f[e] = (float)c[e] * u;
+      w[e] = (bf16)f[e];
+    }
+    *reinterpret_cast<els *>(at) = w;
+    if (PARTS > 1 && step >= exact) {
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) {
-        w[k][e] = (bf16)f;
-        f -= (float)w[k][e];
+      for (int k = 1; k < PARTS; ++k) {
+#pragma unroll
+        for (int e = 0; e < NC; ++e) {
+          f[e] -= (float)w[e];
+          w[e] = (bf16)f[e];
+        }
+        *reinterpret_cast<els *>(at + k * 64 * VP) = w;
       }
     }
-#pragma unroll
-    for (int k = 0; k < PARTS; ++k) *reinterpret_cast<els *>(at + k * 64 * VP) = w[k];
     if (OUT) *reinterpret_cast<els *>(lds.c[buf] + crow * VP + ccol) = c;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -284,20 +326,23 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
       if (64 * DA / 8 % T == 0 || pc < 64 * DA / 8) *reinterpret_cast<uint4 *>(lds.b[buf] + row * P + col * 8) = in.b[i];
     }
   };
-  f32x4 S[KT];
+  f32x4 S[KT][CT];
   auto show = [&](int buf) {
     if (!OUT || !tiles) return;
 #pragma unroll
-    for (int i = 0; i < KT; ++i) {
-      const int v = 16 * ct + l16, row = 16 * ((v >> 2) & 1) + 4 * (v >> 3) + (v & 3);
-      st4(lds.s[buf] + row * P + 16 * kt(i) + 4 * g, S[i][0], S[i][1], S[i][2], S[i][3]);
+    for (int j = 0; j < CT; ++j) {
+      bf16 *at = lds.s[buf] + dealt(16 * (ct + j) + l16) * P + 4 * g;
+#pragma unroll
+      for (int i = 0; i < KT; ++i) st4(at + 16 * kt(i), S[i][j][0], S[i][j][1], S[i][j][2], S[i][j][3]);
     }
   };
   In x, y;
   fetch(x);
   fetch(y);
 #pragma unroll
-  for (int i = 0; i < KT; ++i) S[i] = zero4();
+  for (int i = 0; i < KT; ++i)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) S[i][j] = zero4();
   if (OUT && p.start) state_io(S, const_cast<float *>(p.start), false);
   commit(x, 0);
   show(0);
@@ -305,37 +350,55 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
   // `in` is free, `next` has the chunk after this one
   auto work = [&](In &in, const In &next, int step) {
     fetch(in);
-    const bf16 *b = lds.b[step & 1], *w = lds.w[step & 1][0];
+    const bf16 *b = lds.b[OUT ? step & 1 : 0], *w = lds.w[OUT ? step & 1 : 0][0];
     const float all = way.part(step) ? all_rest : all_whole;
     const int row = 4 * g + (l16 >> 2);  // of this lane's share of a transpose read
     auto tr = [&](const bf16 *m, int pitch, int s, int tile) {
       const bf16 *at = m + (32 * s + row) * pitch + 16 * tile + 4 * (l16 & 3);
       return join(tr4(at), tr4(at + 16 * pitch));
     };
+    bf16x8 wf[2][PARTS][CT], bf[2][KT];
+    if (tiles) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int j = 0; j < CT; ++j) wf[s][0][j] = tr(w, VP, s, ct + j);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) bf[s][i] = tr(b, P, s, kt(i));
+      }
+      if (PARTS > 1 && step >= exact) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int k = 1; k < PARTS; ++k)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) wf[s][k][j] = tr(w + k * 64 * VP, VP, s, ct + j);
+      }
+    }
+    if (!OUT) __syncthreads();  // one set of rows: more workgroups a compute unit instead
+    __builtin_amdgcn_sched_barrier(0);
+    commit(next, step + 1);  // under the reads
+    __builtin_amdgcn_sched_barrier(0);
     if (tiles) {
 #pragma unroll
       for (int i = 0; i < KT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[i][e] *= all;
-      bf16x8 wf[2][PARTS], bf[2][KT];
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+          for (int e = 0; e < 4; ++e) S[i][j][e] *= all;
+      auto add = [&](int k) {
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) wf[s][k] = tr(w + k * 64 * VP, VP, s, ct);
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < KT; ++i) bf[s][i] = tr(b, P, s, kt(i));
+          for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) S[i][j] = M::mma(bf[s][i], wf[s][k][j], S[i][j]);
+      };
+      if (PARTS > 1 && step >= exact) {
+#pragma unroll
+        for (int k = PARTS - 1; k > 0; --k) add(k);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      commit(next, step + 1);  // under the reads
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int k = PARTS - 1; k >= 0; --k)
-#pragma unroll
-          for (int i = 0; i < KT; ++i) S[i] = M::mma(bf[s][i], wf[s][k], S[i]);
-    } else {
-      commit(next, step + 1);
+      add(0);
     }
     show((step + 1) & 1);
   };
@@ -359,21 +422,26 @@ struct Place {
   SlotLoc loc;
   int64_t slot;
   int h, c0, kind;
-  bool out;  // past the work
 };
-// Items in the order (slot, head, pass, columns): what shares rows runs together
-// on one XCD.
-__device__ __forceinline__ Place place(const AttnArgs &a, int first, int kinds, int slices) {
+// Items in the order (head, slot, pass, columns): what shares rows runs together
+// on one XCD, and every XCD has all sequences (with slots first, those of one
+// length, or the parts that nothing is asked of, were an XCD's own).
+__device__ __forceinline__ Place place(const AttnArgs &a, int seg, int64_t slots, int first, int kinds, int slices, int VS) {
   int64_t item = xcd_remap(blockIdx.x, gridDim.x);
   Place p;
-  p.c0 = (int)(item % slices) * 32;
+  p.c0 = (int)(item % slices) * VS;
   item /= slices;
   p.kind = first + (int)(item % kinds);
   item /= kinds;
-  p.h = (int)(item % a.Hv);
-  p.slot = item / a.Hv;
-  p.loc = locate(a.s, a.seg, p.slot);
-  p.out = !p.loc.used;
+  p.slot = item % slots;
+  p.h = (int)(item / slots);
+  // the q-heads dealt to the XCDs in turn: neighbours often decay alike, and what
+  // a head costs goes by its decay
+  if (a.Hq % 8 == 0) {
+    const int per = a.Hv / 8, R = a.Hv / a.Hq, l = p.h % per;
+    p.h = (l / R * 8 + p.h / per) * R + l % R;
+  }
+  p.loc = locate(a.s, seg, p.slot);
   return p;
 }
 __device__ __forceinline__ Way way_of(const SlotLoc &loc, bool rev) {
@@ -385,58 +453,96 @@ __device__ __forceinline__ Way way_of(const SlotLoc &loc, bool rev) {
   return w;
 }
 
+// The step from which a pass whose state is returned at the sequence's end holds
+// it to fp32: what comes before is left to 2^-20 there, and its own error of
+// half a bf16 step to 2^-28.  (Exact throughout: 8192 tokens, 64 heads of 128:
+// 121 us against 118, where the heads that forget least decide.)
+__device__ __forceinline__ int exact_from(const AttnArgs &a, const SlotLoc &loc, const Way &way, float g2) {
+  const Span sp = seq_span(a.s, loc.n);
+  const float near = 20.f / fmaxf(-g2, 1e-7f);  // tokens from the end
+  // from the pass's first token to the sequence's end on its way
+  const int64_t all = way.rev ? way.t0 + way.nt - sp.first : sp.end - way.t0;
+  if (!(near < (float)all)) return 0;
+  const int64_t step = (all - (int64_t)near) / 64 - 1;
+  return step < 0 ? 0 : step < way.nc ? (int)step : way.nc;
+}
+
 // The passes first .. first + kinds - 1, whose a and b are DA wide and whose
-// output is DC.
-template <int DA, bool EXACT>
+// output is DC.  EXACT: some return their state.
+template <int DA, int VS, bool EXACT, bool PART>
 __global__ __launch_bounds__(768, 3) void mma_kernel(AttnArgs a, Layout w, int first, int kinds, int DC) {
-  __shared__ __align__(16) Lds<DA, true, EXACT ? 3 : 1> lds;
-  const Place at = place(a, first, kinds, DC / 32);
-  if (at.out) return;
-  const Pass p = make_pass<bf16>(a, w, at.kind, at.loc, at.slot, at.h);
+  __shared__ __align__(16) Lds<DA, VS, true, EXACT ? 3 : 1> lds;
+  const Place at = place(a, a.seg, a.slots, first, kinds, DC / VS, VS);
+  if (!at.loc.used) return;
+  const Pass p = make_pass<bf16>(a, w, at.kind, at.loc, at.h);
   const Way way = way_of(at.loc, p.rev);
   const float g2 = log2_decay(a.g[at.h]);
   const int wave = wave_of(threadIdx.x);
   if (wave >= 4) {
-    states<DA, 8, true, EXACT>(p, way, g2, DC, at.c0, threadIdx.x - 256, nullptr, lds);
+    states<DA, VS, true>(p, way, g2, DC, at.c0, p.last ? exact_from(a, at.loc, way, g2) : way.nc, threadIdx.x - 256, nullptr, lds);
     return;
   }
   switch (p.rev ? 4 - wave : wave + 1) {
-    case 1: outputs<DA, 1>(p, way, g2, at.c0, wave, lds); break;
-    case 2: outputs<DA, 2>(p, way, g2, at.c0, wave, lds); break;
-    case 3: outputs<DA, 3>(p, way, g2, at.c0, wave, lds); break;
-    default: outputs<DA, 4>(p, way, g2, at.c0, wave, lds);
+    case 1: outputs<DA, VS, 1, PART>(p, way, g2, at.c0, wave, lds); break;
+    case 2: outputs<DA, VS, 2, PART>(p, way, g2, at.c0, wave, lds); break;
+    case 3: outputs<DA, VS, 3, PART>(p, way, g2, at.c0, wave, lds); break;
+    default: outputs<DA, VS, 4, PART>(p, way, g2, at.c0, wave, lds);
   }
 }
 
-// What a segment adds to S (o's pass) and, with two kinds, to Z (dv's).
-template <int DA>
-__global__ __launch_bounds__(256) void mma_local_kernel(AttnArgs a, Layout w, int kinds) {
-  __shared__ __align__(16) Lds<DA, false, 3> lds;
-  const Place at = place(a, 0, kinds, a.V / 32);
-  if (at.out) return;
-  const Pass p = make_pass<bf16>(a, w, at.kind ? kDv : kO, at.loc, at.slot, at.h);
-  if (p.rev ? at.loc.index == 0 : at.loc.last) return;
+// What a part of a segment adds to S (o's pass) and, with two kinds, to Z (dv's).
+// Tokens whose decay to the next segment is 0 in fp32 add nothing and are not read.
+template <int DA, int VS>
+__global__ __launch_bounds__(512, 4) void mma_local_kernel(AttnArgs a, Layout w, int64_t slots, int kinds) {
+  __shared__ __align__(16) Lds<DA, VS, false, 3> lds;
+  Place at = place(a, a.seg / a.parts, slots, 0, kinds, a.V / VS, VS);
+  if (!at.loc.used) return;
+  const Pass p = make_pass<bf16>(a, w, at.kind ? kDv : kO, at.loc, at.h);
+  if (!carried(a, at.loc, p.rev)) return;
   float *dst = (p.rev ? w.zend(a) : w.start(a)) + (at.slot * a.Hv + at.h) * (int64_t)DA * a.V;
-  states<DA, 4, false, true>(p, way_of(at.loc, p.rev), log2_decay(a.g[at.h]), a.V, at.c0, threadIdx.x, dst, lds);
+  const float g2 = log2_decay(a.g[at.h]);
+  // tokens between the part and the segment's border, and how far it sees
+  const int sub = a.seg / a.parts, part = (int)(at.loc.index % a.parts);
+  const int64_t n = at.loc.t1 - at.loc.t0, past = (int64_t)sub * (p.rev ? part : a.parts - 1 - part);
+  if (g2 * (float)(n + past) < -151.f) {
+    const int64_t seen = (int64_t)(151.f / -g2) + 1 - past, most = seen < 0 ? 0 : seen < n ? seen : n;
+    if (p.rev)
+      at.loc.t1 = at.loc.t0 + most;
+    else
+      at.loc.t0 += (n - most) / 64 * 64;
+  }
+  const Way way = way_of(at.loc, p.rev);
+  states<DA, VS, false>(p, way, g2, a.V, at.c0, (p.rev ? a.dh0 : a.ht) ? exact_from(a, at.loc, way, g2) : way.nc, threadIdx.x, dst, lds);
 }
 
-// exact: a state of these passes is returned
-hipError_t run(const char *name, const AttnArgs &a, const Layout &w, int DA, int DC, int first, int kinds, bool exact, hipStream_t st) {
-  const unsigned blocks = (unsigned)(a.slots * a.Hv * kinds * (DC / 32));
-  KernelTimer kt(name, st);
-  auto go = [&](auto exact) {
-    constexpr bool X = decltype(exact)::value;
-    if (DA == 32)
-      mma_kernel<32, X><<<blocks, 768, 0, st>>>(a, w, first, kinds, DC);
-    else if (DA == 64)
-      mma_kernel<64, X><<<blocks, 768, 0, st>>>(a, w, first, kinds, DC);
+template <typename F>
+void with_sizes(int DA, int DC, int cols, F f) {
+  auto wide = [&](auto da) {
+    if (DC == 32 || cols == 32)
+      f(da, std::integral_constant<int, 32>());
     else
-      mma_kernel<128, X><<<blocks, 768, 0, st>>>(a, w, first, kinds, DC);
+      f(da, std::integral_constant<int, 64>());
   };
-  if (exact)
-    go(std::true_type());
+  if (DA == 32)
+    wide(std::integral_constant<int, 32>());
+  else if (DA == 64)
+    wide(std::integral_constant<int, 64>());
   else
-    go(std::false_type());
+    wide(std::integral_constant<int, 128>());
+}
+
+// exact: a state of these passes is returned; part: they write v-heads' parts
+hipError_t run(const char *name, const AttnArgs &a, const Layout &w, int DA, int DC, int first, int kinds, bool exact, bool part, hipStream_t st) {
+  KernelTimer kt(name, st);
+  with_sizes(DA, DC, a.cols, [&](auto da, auto vs) {
+    const unsigned blocks = (unsigned)(a.slots * a.Hv * kinds * (DC / vs));
+    if (part)
+      mma_kernel<da, vs, false, true><<<blocks, 768, 0, st>>>(a, w, first, kinds, DC);
+    else if (exact)
+      mma_kernel<da, vs, true, false><<<blocks, 768, 0, st>>>(a, w, first, kinds, DC);
+    else
+      mma_kernel<da, vs, false, false><<<blocks, 768, 0, st>>>(a, w, first, kinds, DC);
+  });
   return hipGetLastError();
 }
 
@@ -444,24 +550,21 @@ hipError_t run(const char *name, const AttnArgs &a, const Layout &w, int DA, int
 
 hipError_t launch_mma_local(const AttnArgs &a, const Layout &w, bool both, hipStream_t st) {
   const int kinds = both ? 2 : 1;
-  const unsigned blocks = (unsigned)(a.slots * a.Hv * kinds * (a.V / 32));
   KernelTimer kt("attn_local", st);
-  if (a.K == 32)
-    mma_local_kernel<32><<<blocks, 256, 0, st>>>(a, w, kinds);
-  else if (a.K == 64)
-    mma_local_kernel<64><<<blocks, 256, 0, st>>>(a, w, kinds);
-  else
-    mma_local_kernel<128><<<blocks, 256, 0, st>>>(a, w, kinds);
+  with_sizes(a.K, a.V, 64, [&](auto da, auto vs) {
+    const int64_t slots = scan::slots_of(a.s, a.seg / a.parts);
+    mma_local_kernel<da, vs><<<(unsigned)(slots * a.Hv * kinds * (a.V / vs)), 512, 0, st>>>(a, w, slots, kinds);
+  });
   return hipGetLastError();
 }
 hipError_t launch_mma_out(const AttnArgs &a, const Layout &w, hipStream_t st) {
-  return run("attn_out", a, w, a.K, a.V, kO, 1, a.ht != nullptr, st);
+  return run("attn_out", a, w, a.K, a.V, kO, 1, a.ht != nullptr, false, st);
 }
 hipError_t launch_mma_grads(const AttnArgs &a, const Layout &w, hipStream_t st) {
-  const bool exact = a.dh0 != nullptr;
-  if (a.K == a.V && !exact) return run("attn_grads", a, w, a.K, a.V, kDq, 3, false, st);
-  const hipError_t e = run("attn_grads", a, w, a.V, a.K, kDq, 2, false, st);
-  return e != hipSuccess ? e : run("attn_grads", a, w, a.K, a.V, kDv, 1, exact, st);
+  const bool exact = a.dh0 != nullptr, part = a.Hv != a.Hq;
+  if (a.K == a.V && !exact && !part) return run("attn_grads", a, w, a.K, a.V, kDq, 3, false, false, st);
+  const hipError_t e = run("attn_grads", a, w, a.V, a.K, kDq, 2, false, part, st);
+  return e != hipSuccess ? e : run("attn_grads", a, w, a.K, a.V, kDv, 1, exact, false, st);
 }
 
 }  // namespace attn

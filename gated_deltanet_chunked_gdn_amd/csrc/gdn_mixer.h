@@ -105,7 +105,9 @@ hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st);
 struct AttnArgs {
   Seqs s;
   int Hq, Hv, K, V, dtype;
-  int seg;
+  int64_t longest;     // sequence, as far as the host knows
+  int seg, parts;      // tokens of a segment, and the parts it is taken in where states are summed up
+  int cols;            // of a state that a workgroup of the bf16 passes has, at the most
   int64_t slots;
   bool one_seg;        // no sequence has two segments
   float scale;
@@ -117,7 +119,7 @@ struct AttnArgs {
   char *ws;
 };
 struct AttnPlan {
-  int seg;
+  int seg, parts, cols;
   int64_t slots;
   bool one_seg;
   size_t ws;

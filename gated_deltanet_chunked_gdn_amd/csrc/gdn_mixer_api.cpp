@@ -211,6 +211,14 @@ int check_attn(const gdn_attn_t *p, bool step, bool bwd, gdn::AttnArgs *a) {
   a->qs = qs;
   a->ks = ks;
   a->vs = vs;
+  a->longest = p->T;
+  if (p->cu_seqlens_host) {
+    a->longest = 0;
+    for (int n = 0; n < p->N; ++n) {
+      const int64_t len = (int64_t)p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
+      if (len > a->longest) a->longest = len;
+    }
+  }
   // (a launch has fewer than 2^32 threads: up to twelve workgroups of 768 a
   // slot and head, two threads for four elements of a state, one for four of dq)
   constexpr int64_t kBlocks = (int64_t)1 << 24;
@@ -576,6 +584,8 @@ int gdn_linear_attention_fwd(const gdn_attn_t *p, const void *q, const void *k, 
   const gdn::AttnPlan pl = gdn::attn_plan(a, false);
   if ((rc = check_ws(workspace, ws_bytes, pl.ws)) != GDN_OK) return rc;
   a.seg = pl.seg;
+  a.parts = pl.parts;
+  a.cols = pl.cols;
   a.slots = pl.slots;
   a.one_seg = pl.one_seg;
   a.q = q;
@@ -605,6 +615,8 @@ int gdn_linear_attention_bwd(const gdn_attn_t *p, const void *q, const void *k, 
   const gdn::AttnPlan pl = gdn::attn_plan(a, true);
   if ((rc = check_ws(workspace, ws_bytes, pl.ws)) != GDN_OK) return rc;
   a.seg = pl.seg;
+  a.parts = pl.parts;
+  a.cols = pl.cols;
   a.slots = pl.slots;
   a.one_seg = pl.one_seg;
   a.q = q;
