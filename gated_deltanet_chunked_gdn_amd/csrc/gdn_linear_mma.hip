@@ -237,7 +237,9 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
 // ---- the state's waves
 
 // OUT: beside the outputs' waves, which read the state of every chunk.  From step
-// `exact` on the state is held to fp32 (L::PARTS = 1: never).
+// `exact` on the state is held to fp32, by three parts of u c instead of two
+// (L::PARTS = 2: never; one part left dq and dk 1.6 times as far from 64 bits as
+// rounding the output alone, two 1.4).
 template <int DA, int VS, bool OUT, typename L>
 __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, int DC, int c0, int exact, int tid, float *dst, L &lds) {
   constexpr int P = L::P, VP = L::VP, PARTS = L::PARTS, NS = 8, T = 64 * NS;
@@ -308,17 +310,16 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
       w[e] = (bf16)f[e];
     }
     *reinterpret_cast<els *>(at) = w;
-    if (PARTS > 1 && step >= exact) {
+    auto rest = [&](int k) {
 #pragma unroll
-      for (int k = 1; k < PARTS; ++k) {
-#pragma unroll
-        for (int e = 0; e < NC; ++e) {
-          f[e] -= (float)w[e];
-          w[e] = (bf16)f[e];
-        }
-        *reinterpret_cast<els *>(at + k * 64 * VP) = w;
+      for (int e = 0; e < NC; ++e) {
+        f[e] -= (float)w[e];
+        w[e] = (bf16)f[e];
       }
-    }
+      *reinterpret_cast<els *>(at + k * 64 * VP) = w;
+    };
+    rest(1);
+    if (PARTS > 2 && step >= exact) rest(2);
     if (OUT) *reinterpret_cast<els *>(lds.c[buf] + crow * VP + ccol) = c;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -362,17 +363,17 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
 #pragma unroll
-        for (int j = 0; j < CT; ++j) wf[s][0][j] = tr(w, VP, s, ct + j);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < CT; ++j) wf[s][k][j] = tr(w + k * 64 * VP, VP, s, ct + j);
 #pragma unroll
         for (int i = 0; i < KT; ++i) bf[s][i] = tr(b, P, s, kt(i));
       }
-      if (PARTS > 1 && step >= exact) {
+      if (PARTS > 2 && step >= exact) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int k = 1; k < PARTS; ++k)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) wf[s][k][j] = tr(w + k * 64 * VP, VP, s, ct + j);
+          for (int j = 0; j < CT; ++j) wf[s][PARTS - 1][j] = tr(w + 2 * 64 * VP, VP, s, ct + j);
       }
     }
     if (!OUT) __syncthreads();  // one set of rows: more workgroups a compute unit instead
@@ -394,10 +395,8 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
 #pragma unroll
             for (int j = 0; j < CT; ++j) S[i][j] = M::mma(bf[s][i], wf[s][k][j], S[i][j]);
       };
-      if (PARTS > 1 && step >= exact) {
-#pragma unroll
-        for (int k = PARTS - 1; k > 0; --k) add(k);
-      }
+      if (PARTS > 2 && step >= exact) add(2);
+      add(1);
       add(0);
     }
     show((step + 1) & 1);
@@ -454,12 +453,11 @@ __device__ __forceinline__ Way way_of(const SlotLoc &loc, bool rev) {
 }
 
 // The step from which a pass whose state is returned at the sequence's end holds
-// it to fp32: what comes before is left to 2^-20 there, and its own error of
-// half a bf16 step to 2^-28.  (Exact throughout: 8192 tokens, 64 heads of 128:
-// 121 us against 118, where the heads that forget least decide.)
+// it to fp32: what comes before is left to 2^-10 there, and its own error of 2^-18
+// to 2^-28.
 __device__ __forceinline__ int exact_from(const AttnArgs &a, const SlotLoc &loc, const Way &way, float g2) {
   const Span sp = seq_span(a.s, loc.n);
-  const float near = 20.f / fmaxf(-g2, 1e-7f);  // tokens from the end
+  const float near = 10.f / fmaxf(-g2, 1e-7f);  // tokens from the end
   // from the pass's first token to the sequence's end on its way
   const int64_t all = way.rev ? way.t0 + way.nt - sp.first : sp.end - way.t0;
   if (!(near < (float)all)) return 0;
@@ -471,7 +469,7 @@ __device__ __forceinline__ int exact_from(const AttnArgs &a, const SlotLoc &loc,
 // output is DC.  EXACT: some return their state.
 template <int DA, int VS, bool EXACT, bool PART>
 __global__ __launch_bounds__(768, 3) void mma_kernel(AttnArgs a, Layout w, int first, int kinds, int DC) {
-  __shared__ __align__(16) Lds<DA, VS, true, EXACT ? 3 : 1> lds;
+  __shared__ __align__(16) Lds<DA, VS, true, EXACT ? 3 : 2> lds;
   const Place at = place(a, a.seg, a.slots, first, kinds, DC / VS, VS);
   if (!at.loc.used) return;
   const Pass p = make_pass<bf16>(a, w, at.kind, at.loc, at.h);
