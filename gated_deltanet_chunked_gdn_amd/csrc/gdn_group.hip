@@ -165,7 +165,7 @@ template <typename E, int VEC, int TPG, int NV>
 __global__ __launch_bounds__(TPG > 256 ? TPG : 256) void bwd_kernel(GroupArgs a) {
   using H = Held<VEC, TPG, NV>;
   __shared__ float red[32];
-  __shared__ float cols[H::T * NV * VEC];
+  __shared__ float cols[H::T * NV * VEC], more[H::T];
   const H at(a);
   const int64_t sample = a.S * a.G * a.Dg;
   const float inv = 1.f / ((float)a.S * (float)a.Dg);
@@ -245,18 +245,35 @@ __global__ __launch_bounds__(TPG > 256 ? TPG : 256) void bwd_kernel(GroupArgs a)
     return;
   }
   constexpr int W = TPG * NV * VEC;  // a group's values, in the order of its positions
+  // a channel's positions are shared by up to 32 lanes (one: 9 of 22 us with 333
+  // positions of 7 channels), whose sums are added in order
+  int share = TPG / a.Dg;
+  share = share < 1 ? 1 : share > 32 ? 32 : share;
+  const int d0 = at.lane / share, q = at.lane - d0 * share, step = TPG / share;
+  float *own = cols + at.sub * W;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) cols[at.sub * W + (v * TPG + at.lane) * VEC + i] = k ? db[v][i] : dw[v][i];
+      for (int i = 0; i < VEC; ++i) own[(v * TPG + at.lane) * VEC + i] = k ? db[v][i] : dw[v][i];
     __syncthreads();
-    for (int d = at.lane; d < a.Dg; d += TPG) {
+    for (int d = d0; d < a.Dg && d0 < step; d += step) {
       float s = 0.f;
-      for (int p = 0; p < a.S; ++p) s += cols[at.sub * W + p * a.Dg + d];
-      part[k * C + d] = s;
+      for (int p = q; p < a.S; p += share) s += own[p * a.Dg + d];
+      if (share == 1)
+        part[k * C + d] = s;
+      else
+        more[at.sub * TPG + d * share + q] = s;  // (share > 1: a lane has one channel)
+    }
+    if (share == 1) continue;
+    __syncthreads();
+    if (at.lane < a.Dg) {
+      const int n = share < a.S ? share : (int)a.S;
+      float s = 0.f;
+      for (int j = 0; j < n; ++j) s += more[at.sub * TPG + at.lane * share + j];
+      part[k * C + at.lane] = s;
     }
   }
 }
@@ -284,27 +301,28 @@ __device__ __forceinline__ Tile tile_of(const GroupArgs &a, int64_t blocks, int6
   t.r1 = t.r0 + per < a.S ? t.r0 + per : a.S;
   return t;
 }
-// `put` of what the threads of a column have, one after the other, in thread ty = 0
-template <int VEC, typename F>
-__device__ __forceinline__ void join_rows(const Tile &t, const float (&u)[VEC], const float (&v)[VEC], float (*lu)[256], float (*lv)[256], F put) {
+// What the threads have of their channels into LDS, in the order [row of threads][channel]
+template <int VEC>
+__device__ __forceinline__ void to_lds(const Tile &t, const float (&u)[VEC], const float (&v)[VEC], float *lu, float *lv) {
+  if (t.ty < t.ty_n) {
+    const int at = (t.ty * t.px + t.tx) * VEC;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    lu[i][threadIdx.x] = u[i];
-    lv[i][threadIdx.x] = v[i];
+    for (int i = 0; i < VEC; ++i) {
+      lu[at + i] = u[i];
+      lv[at + i] = v[i];
+    }
   }
   __syncthreads();
-  if (t.ty == 0 && t.in)
-    for (int y = 0; y < t.ty_n; ++y)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) put(y, i, lu[i][y * t.px + t.tx], lv[i][y * t.px + t.tx]);
 }
 
 constexpr int kRows = 4;  // rows a thread has in flight
 
-// [N blocks][2][C]: mean of a block's rows, and the squares about it
+// [N blocks][2][C]: mean of a block's rows, and the squares about it; by_group:
+// [N blocks][2][G], of all channels of a group
 template <typename E, int VEC>
-__global__ __launch_bounds__(256) void stats_kernel(GroupArgs a, int64_t blocks, int64_t per) {
-  __shared__ float lu[VEC][256], lv[VEC][256];
+__global__ __launch_bounds__(256) void stats_kernel(GroupArgs a, int64_t blocks, int64_t per, bool by_group) {
+  constexpr int ROWS = 2 * kRows;
+  __shared__ float lu[VEC * 256], lv[VEC * 256];
   const Tile t = tile_of<VEC>(a, blocks, per);
   const int64_t C = (int64_t)a.G * a.Dg;
   const E *x = static_cast<const E *>(a.x) + t.n * a.S * C + t.c;
@@ -312,12 +330,12 @@ __global__ __launch_bounds__(256) void stats_kernel(GroupArgs a, int64_t blocks,
 #pragma unroll
   for (int i = 0; i < VEC; ++i) first[i] = s[i] = q[i] = 0.f;
   const int64_t own = t.in && t.r0 + t.ty < t.r1 ? (t.r1 - t.r0 - t.ty + t.ty_n - 1) / t.ty_n : 0;
-  for (int64_t k = 0; k < own; k += kRows) {
-    Raw<E, VEC> r[kRows];
+  for (int64_t k = 0; k < own; k += ROWS) {
+    Raw<E, VEC> r[ROWS];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) r[j].load(x + (t.r0 + t.ty + (k + j < own ? k + j : own - 1) * t.ty_n) * C);
+    for (int j = 0; j < ROWS; ++j) r[j].load(x + (t.r0 + t.ty + (k + j < own ? k + j : own - 1) * t.ty_n) * C);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+    for (int j = 0; j < ROWS; ++j) {
       const Vec<E, VEC> v = r[j].f();
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -335,24 +353,42 @@ __global__ __launch_bounds__(256) void stats_kernel(GroupArgs a, int64_t blocks,
     mean[i] = first[i] + s[i] * inv;
     m2[i] = q[i] - s[i] * (s[i] * inv);
   }
-  float count = 0.f, jm[VEC], j2[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) jm[i] = j2[i] = 0.f;
-  join_rows<VEC>(t, mean, m2, lu, lv, [&](int y, int i, float m, float v) {
-    const int64_t left = t.r1 - t.r0 - y;
-    const float k = left > 0 ? (float)((left + t.ty_n - 1) / t.ty_n) : 0.f;
-    if (i == 0) count += k;
-    if (k == 0.f) return;
-    const float d = m - jm[i], part = k / count;
-    jm[i] += d * part;
-    j2[i] += v + d * d * (count - k) * part;
-  });
-  if (t.ty != 0 || !t.in) return;
-  float *part = reinterpret_cast<float *>(a.ws) + (int64_t)blockIdx.x * 2 * C + t.c;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    part[i] = jm[i];
-    part[C + i] = j2[i];
+  to_lds<VEC>(t, mean, m2, lu, lv);
+  // a thread a channel: the mean of the threads' means, then the squares about it
+  const int width = t.px * VEC, rows = (int)(t.r1 - t.r0), even = rows / t.ty_n, odd = rows - even * t.ty_n;
+  const float inv_rows = 1.f / (float)rows;
+  float *part = reinterpret_cast<float *>(a.ws) + (int64_t)blockIdx.x * 2 * (by_group ? a.G : C);
+  for (int c = threadIdx.x; c < width; c += 256) {
+    float m = 0.f, q = 0.f;
+    for (int y = 0; y < t.ty_n; ++y) m += (float)(even + (y < odd)) * lu[y * width + c];
+    m *= inv_rows;
+    for (int y = 0; y < t.ty_n; ++y) {
+      const float d = lu[y * width + c] - m;
+      q += lv[y * width + c] + (float)(even + (y < odd)) * d * d;
+    }
+    if (by_group) {
+      lu[c] = m;  // (row 0 of its own channel)
+      lv[c] = q;
+    } else {
+      const int64_t at = (int64_t)blockIdx.y * width + c;
+      if (at < C) part[at] = m, part[C + at] = q;
+    }
+  }
+  if (!by_group) return;
+  // (one workgroup has all channels: C <= 256 VEC.)  They have as many rows each:
+  // the group's mean is that of their means.
+  __syncthreads();
+  const float inv_ch = 1.f / (float)a.Dg;
+  for (int g = threadIdx.x; g < a.G; g += 256) {
+    float m = 0.f, q = 0.f;
+    for (int d = 0; d < a.Dg; ++d) m += lu[g * a.Dg + d];
+    m *= inv_ch;
+    for (int d = 0; d < a.Dg; ++d) {
+      const float e = lu[g * a.Dg + d] - m;
+      q += lv[g * a.Dg + d] + (float)rows * e * e;
+    }
+    part[g] = m;
+    part[a.G + g] = q;
   }
 }
 
@@ -366,24 +402,30 @@ __device__ __forceinline__ double block_sum(double v, double *red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// mean and rstd of a sample's group from its blocks
-__global__ __launch_bounds__(256) void stats_join_kernel(GroupArgs a, int64_t blocks, int64_t per) {
+// mean and rstd of a sample's group from its blocks, each with `width` of its
+// values (Dg, or 1 of all channels)
+__global__ __launch_bounds__(256) void stats_join_kernel(GroupArgs a, int64_t blocks, int64_t per, int width) {
   __shared__ double red[4];
   const int g = blockIdx.x % a.G;
-  const int64_t n = blockIdx.x / a.G, C = (int64_t)a.G * a.Dg, items = blocks * a.Dg;
-  const float *part = reinterpret_cast<const float *>(a.ws) + n * blocks * 2 * C + (int64_t)g * a.Dg;
-  const double count = (double)a.S * a.Dg;
+  const int64_t n = blockIdx.x / a.G, C = (int64_t)a.G * width;
+  const uint32_t items = (uint32_t)(blocks * width);
+  const float *part = reinterpret_cast<const float *>(a.ws) + n * blocks * 2 * C + (int64_t)g * width;
+  const double count = (double)a.S * width;
   auto rows = [&](int64_t b) { return (double)((b + 1) * per < a.S ? per : a.S - b * per); };
   double s = 0.;
-  for (int64_t i = threadIdx.x; i < items; i += 256) s += rows(i / a.Dg) * part[i / a.Dg * 2 * C + i % a.Dg];
+  for (uint32_t i = threadIdx.x; i < items; i += 256) {
+    const uint32_t b = i / (uint32_t)width;
+    s += rows(b) * part[b * 2 * C + (i - b * width)];
+  }
   const double mean = block_sum(s, red) / count;
   double q = 0.;
-  for (int64_t i = threadIdx.x; i < items; i += 256) {
-    const float *p = part + i / a.Dg * 2 * C + i % a.Dg;
+  for (uint32_t i = threadIdx.x; i < items; i += 256) {
+    const uint32_t b = i / (uint32_t)width;
+    const float *p = part + b * 2 * C + (i - b * width);
     const double d = p[0] - mean;
-    q += p[C] + rows(i / a.Dg) * d * d;
+    q += p[C] + rows(b) * d * d * (width == 1 ? (double)a.Dg : 1.);
   }
-  q = block_sum(q, red) / count;
+  q = block_sum(q, red) / ((double)a.S * a.Dg);
   if (threadIdx.x == 0) {
     a.mean[blockIdx.x] = (float)mean;
     a.rstd[blockIdx.x] = (float)(1. / sqrt(q + (double)a.eps));
@@ -435,10 +477,22 @@ __global__ __launch_bounds__(256) void apply_kernel(GroupArgs a, int64_t blocks,
   }
 }
 
+// dw, db of 32 columns from the partials, added in order
+__device__ __forceinline__ void sum_columns(const GroupArgs &a, int64_t parts, int64_t block) {
+  const int64_t C = (int64_t)a.G * a.Dg;
+  sum_parts(reinterpret_cast<const float *>(a.ws), parts, 2 * C, [&](int64_t i, float v) {
+    if (i < C) {
+      if (a.dw) store_w(a.dw, i, v, a.wdtype);
+    } else if (a.db) {
+      store_w(a.db, i - C, v, a.wdtype);
+    }
+  }, block);
+}
+
 // [N blocks][2][C]: sums of dz xh and dz over a block's rows
 template <typename E, int VEC>
 __global__ __launch_bounds__(256) void sums_kernel(GroupArgs a, int64_t blocks, int64_t per) {
-  __shared__ float lu[VEC][256], lv[VEC][256];
+  __shared__ float lu[VEC * 256], lv[VEC * 256];
   const Tile t = tile_of<VEC>(a, blocks, per);
   const int64_t C = (int64_t)a.G * a.Dg, base = t.n * a.S * C + t.c;
   float dw[VEC], db[VEC];
@@ -472,42 +526,52 @@ __global__ __launch_bounds__(256) void sums_kernel(GroupArgs a, int64_t blocks, 
       }
     }
   }
-  float sw[VEC], sb[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) sw[i] = sb[i] = 0.f;
-  join_rows<VEC>(t, dw, db, lu, lv, [&](int, int i, float u, float v) {
-    sw[i] += u;
-    sb[i] += v;
-  });
-  if (t.ty != 0 || !t.in) return;
-  float *part = reinterpret_cast<float *>(a.ws) + (int64_t)blockIdx.x * 2 * C + t.c;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    part[i] = sw[i];
-    part[C + i] = sb[i];
+  to_lds<VEC>(t, dw, db, lu, lv);
+  const int width = t.px * VEC;
+  float *part = reinterpret_cast<float *>(a.ws) + (int64_t)blockIdx.x * 2 * C;
+  for (int c = threadIdx.x; c < width; c += 256) {
+    float u = 0.f, v = 0.f;
+    for (int y = 0; y < t.ty_n; ++y) {
+      u += lu[y * width + c];
+      v += lv[y * width + c];
+    }
+    const int64_t at = (int64_t)blockIdx.y * width + c;
+    if (at < C) part[at] = u, part[C + at] = v;
   }
 }
 
-// [N][G][2]: the means of t and t xh of a sample's group, behind the partials
-__global__ __launch_bounds__(256) void sums_join_kernel(GroupArgs a, float *sums, int64_t blocks) {
-  __shared__ double red[4];
+// [N][G][2]: the means of t and t xh of a sample's group, behind the partials; the
+// workgroups past them have 32 columns of dw and db each (kSumThreads threads all)
+__global__ __launch_bounds__(kSumThreads) void sums_join_kernel(GroupArgs a, float *sums, int64_t blocks, int64_t groups) {
+  __shared__ double red[kSumThreads / 64][2];
+  const int64_t C = (int64_t)a.G * a.Dg;
+  if (blockIdx.x >= groups) {
+    sum_columns(a, a.N * blocks, blockIdx.x - groups);
+    return;
+  }
   const int g = blockIdx.x % a.G;
-  const int64_t n = blockIdx.x / a.G, C = (int64_t)a.G * a.Dg, items = blocks * a.Dg;
+  const int64_t n = blockIdx.x / a.G;
+  const uint32_t items = (uint32_t)(blocks * a.Dg);
   const float *part = reinterpret_cast<const float *>(a.ws) + n * blocks * 2 * C + (int64_t)g * a.Dg;
   double s1 = 0., s2 = 0.;
-  for (int64_t i = threadIdx.x; i < items; i += 256) {
-    const int64_t d = i % a.Dg;
-    const float *p = part + i / a.Dg * 2 * C + d;
+  for (uint32_t i = threadIdx.x; i < items; i += kSumThreads) {
+    const uint32_t b = i / (uint32_t)a.Dg, d = i - b * a.Dg;
+    const float *p = part + b * 2 * C + d;
     const double w = a.w ? load_w(a.w, (int64_t)g * a.Dg + d, a.wdtype) : 1.f;
     s1 += w * p[C];
     s2 += w * p[0];
   }
-  s1 = block_sum(s1, red);
-  s2 = block_sum(s2, red);
-  const double count = (double)a.S * a.Dg;
-  if (threadIdx.x == 0) {
-    sums[2 * (int64_t)blockIdx.x] = (float)(s1 / count);
-    sums[2 * (int64_t)blockIdx.x + 1] = (float)(s2 / count);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    s1 += __shfl_xor(s1, d);
+    s2 += __shfl_xor(s2, d);
+  }
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][0] = s1, red[threadIdx.x >> 6][1] = s2;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    double s = 0.;
+    for (int i = 0; i < kSumThreads / 64; ++i) s += red[i][threadIdx.x];
+    sums[2 * (int64_t)blockIdx.x + threadIdx.x] = (float)(s / ((double)a.S * a.Dg));
   }
 }
 
@@ -555,17 +619,7 @@ __global__ __launch_bounds__(256) void grads_kernel(GroupArgs a, const float *su
   }
 }
 
-// dw, db from the partials, added in order
-__global__ __launch_bounds__(kSumThreads) void sum_kernel(GroupArgs a, int64_t parts) {
-  const int64_t C = (int64_t)a.G * a.Dg;
-  sum_parts(reinterpret_cast<const float *>(a.ws), parts, 2 * C, [&](int64_t i, float v) {
-    if (i < C) {
-      if (a.dw) store_w(a.dw, i, v, a.wdtype);
-    } else if (a.db) {
-      store_w(a.db, i - C, v, a.wdtype);
-    }
-  });
-}
+__global__ __launch_bounds__(kSumThreads) void sum_kernel(GroupArgs a, int64_t parts) { sum_columns(a, parts, blockIdx.x); }
 
 bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -598,14 +652,14 @@ int64_t held_parts(const GroupArgs &a) {
   return held_blocks(a, bwd_want(a)) * ((lanes > 256 ? lanes : 256) / lanes) / a.G;
 }
 
-// Blocks of a sample's rows in the two-pass form: eight workgroups a compute
-// unit, of 32 rows at the least.
+// Blocks of a sample's rows in the two-pass form: six workgroups a compute unit,
+// in whole rounds of their threads' rows in flight.
 int64_t row_blocks(const GroupArgs &a, int64_t *per) {
-  int64_t want = (compute_units() * 8 + a.N - 1) / (a.N ? a.N : 1);
-  const int64_t most = (a.S + 31) / 32;
-  if (want > most) want = most;
+  const int64_t pieces = (int64_t)a.G * a.Dg / (a.G * a.Dg % 8 == 0 ? 8 : 1);  // (as if aligned: the same workspace)
+  const int64_t unit = 2 * kRows * (pieces < 256 ? 256 / pieces : 1), cols = (pieces + 255) / 256;
+  int64_t want = (compute_units() * 6 + a.N * cols - 1) / (a.N * cols);
   if (want < 1) want = 1;
-  *per = (a.S + want - 1) / want;
+  *per = ((a.S + want - 1) / want + unit - 1) / unit * unit;
   return (a.S + *per - 1) / *per;
 }
 size_t part_bytes(const GroupArgs &a) {
@@ -659,8 +713,9 @@ hipError_t tall_fwd(const GroupArgs &a, hipStream_t st) {
   const dim3 grid((unsigned)(a.N * blocks), (unsigned)((pieces + 255) / 256));
   {
     KernelTimer kt("group_stats", st);
-    stats_kernel<E, VEC><<<grid, 256, 0, st>>>(a, blocks, per);
-    stats_join_kernel<<<(unsigned)(a.N * a.G), 256, 0, st>>>(a, blocks, per);
+    const bool by_group = grid.y == 1;
+    stats_kernel<E, VEC><<<grid, 256, 0, st>>>(a, blocks, per, by_group);
+    stats_join_kernel<<<(unsigned)(a.N * a.G), 256, 0, st>>>(a, blocks, per, by_group ? 1 : a.Dg);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -678,7 +733,8 @@ hipError_t tall_bwd(const GroupArgs &a, hipStream_t st) {
   {
     KernelTimer kt("group_sums", st);
     sums_kernel<E, VEC><<<grid, 256, 0, st>>>(a, blocks, per);
-    sums_join_kernel<<<(unsigned)(a.N * a.G), 256, 0, st>>>(a, sums, blocks);
+    const int64_t groups = a.N * a.G;
+    sums_join_kernel<<<(unsigned)(groups + (a.dw || a.db ? sum_blocks(2 * (int64_t)a.G * a.Dg) : 0)), kSumThreads, 0, st>>>(a, sums, blocks, groups);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -720,24 +776,20 @@ hipError_t launch_group_fwd(const GroupArgs &a, hipStream_t st) {
 
 hipError_t launch_group_bwd(const GroupArgs &a, hipStream_t st) {
   using namespace group;
-  hipError_t e = hipSuccess;
-  int64_t parts = 0, per;
+  int64_t parts = 0;
   if (a.N) {
     const int vec = a.dtype == 1 ? 8 : 4;
     const bool to16 = al16(a.x) && al16(a.w) && al16(a.b) && al16(a.dy) && al16(a.gate) && al16(a.dx) && al16(a.dgate);
-    if (held(a)) {
-      parts = held_parts(a);
-      e = held_bwd(a, to16 && a.Dg % vec == 0, st);
-    } else {
-      parts = a.N * row_blocks(a, &per);
+    if (!held(a)) {
       const bool wide = to16 && a.G * a.Dg % vec == 0;
-      if (a.dtype == 1)
-        e = wide ? tall_bwd<bf16, 8>(a, st) : tall_bwd<bf16, 1>(a, st);
-      else
-        e = wide ? tall_bwd<float, 4>(a, st) : tall_bwd<float, 1>(a, st);
+      if (a.dtype == 1) return wide ? tall_bwd<bf16, 8>(a, st) : tall_bwd<bf16, 1>(a, st);
+      return wide ? tall_bwd<float, 4>(a, st) : tall_bwd<float, 1>(a, st);
     }
+    parts = held_parts(a);
+    const hipError_t e = held_bwd(a, to16 && a.Dg % vec == 0, st);
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess || (!a.dw && !a.db)) return e;
+  if (!a.dw && !a.db) return hipSuccess;
   KernelTimer kt("group_sum", st);
   sum_kernel<<<sum_blocks(2 * (int64_t)a.G * a.Dg), kSumThreads, 0, st>>>(a, parts);
   return hipGetLastError();

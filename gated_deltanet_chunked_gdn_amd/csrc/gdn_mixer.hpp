@@ -175,10 +175,10 @@ __device__ __forceinline__ void load_taps(float (&w)[W][VEC], float (&b)[VEC], c
 constexpr int kSumThreads = 512;
 __host__ __device__ inline unsigned sum_blocks(int64_t n) { return (unsigned)((n + 31) / 32); }
 template <typename F>
-__device__ __forceinline__ void sum_parts(const float *part, int64_t parts, int64_t n, F put) {
+__device__ __forceinline__ void sum_parts(const float *part, int64_t parts, int64_t n, F put, int64_t block = blockIdx.x) {
   __shared__ float red[16][32];
   const int col = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * 32 + col;
+  const int64_t i = block * 32 + col;
   float v = 0.f;
   if (i < n) {
 #pragma unroll 4
