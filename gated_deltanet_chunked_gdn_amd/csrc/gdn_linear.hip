@@ -27,18 +27,18 @@ struct Lds {
 };
 
 // A chunk's rows of COLS columns in the registers of a workgroup; rows past
-// its end are zeros.
-template <typename E, int COLS>
+// its end lie past the buffer's, and read as zeros.
+template <int COLS>
 struct Rows {
-  static constexpr int PER = 16 / (int)sizeof(E), PIECES = C * COLS / PER, N = (PIECES + kThreads - 1) / kThreads;
+  static constexpr int PER = 4, PIECES = C * COLS / PER, N = (PIECES + kThreads - 1) / kThreads;
   uint4 r[N];
-  __device__ __forceinline__ void load(const E *p, int64_t stride, int rows, int tid) {
-    const uint32_t bytes = rows > 0 ? (uint32_t)(((rows - 1) * stride + COLS) * sizeof(E)) : 0u;
+  __device__ __forceinline__ void load(const float *p, int64_t stride, int rows, int tid) {
+    const uint32_t bytes = rows > 0 ? (uint32_t)(((rows - 1) * stride + COLS) * 4) : 0u;
     const auto rsrc = raw_buffer(p, bytes);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int pc = tid + i * kThreads, row = pc / (COLS / PER), col = pc % (COLS / PER);
-      r[i] = buf_load16(rsrc, row < rows ? (uint32_t)(row * stride * sizeof(E) + col * 16) : 0xFFFFFFF0u);
+      r[i] = buf_load16(rsrc, (uint32_t)(row * stride * 4 + col * 16));
     }
   }
   __device__ __forceinline__ void store(float *lds, int pitch, int tid) const {
@@ -46,11 +46,7 @@ struct Rows {
     for (int i = 0; i < N; ++i) {
       const int pc = tid + i * kThreads, row = pc / (COLS / PER), col = pc % (COLS / PER);
       if (PIECES % kThreads != 0 && pc >= PIECES) continue;
-      const E *e = reinterpret_cast<const E *>(&r[i]);
-#pragma unroll
-      for (int j = 0; j < PER; j += 4)
-        *reinterpret_cast<f32x4 *>(lds + row * pitch + col * PER + j) =
-            f32x4{to_f32(e[j]), to_f32(e[j + 1]), to_f32(e[j + 2]), to_f32(e[j + 3])};
+      *reinterpret_cast<uint4 *>(lds + row * pitch + col * PER) = r[i];
     }
   }
 };
@@ -63,7 +59,7 @@ __device__ __forceinline__ f32x4 prod(const f32x4 &x, const f32x4 &y, f32x4 c) {
 
 // DA: width of a and b, DC: of c and the output, of which the workgroup has
 // 32 columns from c0.
-template <typename E, int DA, int DC, bool OUT>
+template <int DA, int DC, bool OUT>
 __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const SlotLoc &loc, float *state, int h, int c0, Lds<DA> &lds) {
   constexpr int P = Lds<DA>::P, KT = DA / 32;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), l16 = lane & 15, q = lane >> 4;
@@ -96,19 +92,17 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
   }
   const int nt = (int)(loc.t1 - loc.t0), nc = (nt + C - 1) / C;
   struct In {
-    Rows<E, DA> a, b;
-    Rows<E, 32> c;
+    Rows<DA> a, b;
+    Rows<32> c;
   };
   auto fetch = [&](In &r, int step) {
     const int ch = p.rev ? nc - 1 - step : step;
     const int64_t t = loc.t0 + (int64_t)C * ch;
     const int rows = nt - C * ch < C ? nt - C * ch : C;
-    if (OUT) r.a.load(static_cast<const E *>(p.a) + t * p.as, p.as, rows, tid);
-    r.b.load(static_cast<const E *>(p.b) + t * p.bs, p.bs, rows, tid);
-    r.c.load(static_cast<const E *>(p.c) + t * p.cs + c0, p.cs, rows, tid);
+    if (OUT) r.a.load(static_cast<const float *>(p.a) + t * p.as, p.as, rows, tid);
+    r.b.load(static_cast<const float *>(p.b) + t * p.bs, p.bs, rows, tid);
+    r.c.load(static_cast<const float *>(p.c) + t * p.cs + c0, p.cs, rows, tid);
   };
-  // (what multiplies into the state lies with a's columns in o and dv: the rows
-  // b of o and dq, a of dk and dv, whose tokens run backwards)
   In in;
   if (nc > 0) fetch(in, 0);
   for (int step = 0; step < nc; ++step) {
@@ -160,11 +154,7 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * it + 4 * q + e;
         const int64_t at = (loc.t0 + (int64_t)C * ch + i) * p.os + c0 + 16 * jt + l16;
-        if (i >= n) continue;
-        if (p.part)
-          static_cast<float *>(p.out)[at] = O[e];
-        else
-          static_cast<E *>(p.out)[at] = from_f32<E>(O[e]);
+        if (i < n) static_cast<float *>(p.out)[at] = O[e];
       }
     }
     // S = l^n S + sum_j u_j b_j c_j^T
@@ -196,7 +186,7 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
     state_io(S, p.last, true);
 }
 
-template <typename E, int K, int V, int WHAT>
+template <int K, int V, int WHAT>
 __global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, int64_t slots, int64_t per) {
   constexpr int D = K > V ? K : V;
   __shared__ __align__(16) char mem[sizeof(Lds<(WHAT == kGrads ? D : K)>)];
@@ -214,19 +204,19 @@ __global__ __launch_bounds__(kThreads) void pass_kernel(AttnArgs a, Layout w, in
   constexpr bool LOCAL = WHAT == kLocal || WHAT == kLocals;
   const SlotLoc loc = locate(a.s, LOCAL ? a.seg / a.parts : a.seg, slot);
   if (!loc.used) return;
-  Pass p = make_pass<E>(a, w, kind, loc, h);
+  Pass p = make_pass<float>(a, w, kind, loc, h);
   if constexpr (LOCAL) {
     if (!carried(a, loc, p.rev)) return;
     // the state is built of b and c
     float *dst = (p.rev ? w.zend(a) : w.start(a)) + (slot * a.Hv + h) * (int64_t)K * V;
-    sweep<E, K, V, false>(a, p, loc, dst, h, c0, *reinterpret_cast<Lds<K> *>(mem));
+    sweep<K, V, false>(a, p, loc, dst, h, c0, *reinterpret_cast<Lds<K> *>(mem));
   } else if constexpr (WHAT == kForward) {
-    sweep<E, K, V, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<K> *>(mem));
+    sweep<K, V, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<K> *>(mem));
   } else {
     if (tr)
-      sweep<E, V, K, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<V> *>(mem));
+      sweep<V, K, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<V> *>(mem));
     else
-      sweep<E, K, V, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<K> *>(mem));
+      sweep<K, V, true>(a, p, loc, nullptr, h, c0, *reinterpret_cast<Lds<K> *>(mem));
   }
 }
 
@@ -300,33 +290,33 @@ __global__ __launch_bounds__(256) void group_kernel(AttnArgs a, Layout w) {
   st4(static_cast<E *>(a.dk) + 4 * i, k[0], k[1], k[2], k[3]);
 }
 
-template <typename E, int K, int V, int WHAT>
+template <int K, int V, int WHAT>
 hipError_t go(const AttnArgs &a, const Layout &w, hipStream_t st) {
   const int most = WHAT == kGrads && K > V ? K : V;
   const int64_t slots = WHAT == kLocal || WHAT == kLocals ? scan::slots_of(a.s, a.seg / a.parts) : a.slots;
   const int64_t per = slots * a.Hv * (most / 32);
   const int parts = WHAT == kGrads ? 3 : WHAT == kLocals ? 2 : 1;
   KernelTimer kt(WHAT == kGrads ? "attn_grads" : WHAT == kForward ? "attn_out" : "attn_local", st);
-  pass_kernel<E, K, V, WHAT><<<(unsigned)(per * parts), kThreads, 0, st>>>(a, w, slots, per);
+  pass_kernel<K, V, WHAT><<<(unsigned)(per * parts), kThreads, 0, st>>>(a, w, slots, per);
   return hipGetLastError();
 }
-template <typename E, int WHAT>
+template <int WHAT>
 hipError_t pick(const AttnArgs &a, const Layout &w, hipStream_t st) {
   switch (a.K * 1000 + a.V) {
-    case 32032: return go<E, 32, 32, WHAT>(a, w, st);
-    case 32064: return go<E, 32, 64, WHAT>(a, w, st);
-    case 32128: return go<E, 32, 128, WHAT>(a, w, st);
-    case 64032: return go<E, 64, 32, WHAT>(a, w, st);
-    case 64064: return go<E, 64, 64, WHAT>(a, w, st);
-    case 64128: return go<E, 64, 128, WHAT>(a, w, st);
-    case 128032: return go<E, 128, 32, WHAT>(a, w, st);
-    case 128064: return go<E, 128, 64, WHAT>(a, w, st);
-    default: return go<E, 128, 128, WHAT>(a, w, st);
+    case 32032: return go<32, 32, WHAT>(a, w, st);
+    case 32064: return go<32, 64, WHAT>(a, w, st);
+    case 32128: return go<32, 128, WHAT>(a, w, st);
+    case 64032: return go<64, 32, WHAT>(a, w, st);
+    case 64064: return go<64, 64, WHAT>(a, w, st);
+    case 64128: return go<64, 128, WHAT>(a, w, st);
+    case 128032: return go<128, 32, WHAT>(a, w, st);
+    case 128064: return go<128, 64, WHAT>(a, w, st);
+    default: return go<128, 128, WHAT>(a, w, st);
   }
 }
 template <int WHAT>
 hipError_t pass(const AttnArgs &a, const Layout &w, hipStream_t st) {
-  if (a.dtype != 1) return pick<float, WHAT>(a, w, st);
+  if (a.dtype != 1) return pick<WHAT>(a, w, st);
   if (WHAT == kForward) return launch_mma_out(a, w, st);
   if (WHAT == kGrads) return launch_mma_grads(a, w, st);
   return launch_mma_local(a, w, WHAT == kLocals, st);

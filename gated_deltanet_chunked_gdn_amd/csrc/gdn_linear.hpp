@@ -110,8 +110,9 @@ __device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, in
   p.scale_in = p.rev ? 1.f : a.scale;
   p.scale_up = p.rev ? a.scale : 1.f;
   const float *given = p.rev ? a.dht : a.h0;
-  // (where the sequence begins, what the call gives; the carry writes the others')
-  if (p.rev ? loc.last : loc.index == 0) {
+  // (where the sequence begins, what the call gives; the carry writes the others'.
+  // With one segment there is none, whatever the device's lengths say.)
+  if (a.one_seg || (p.rev ? loc.last : loc.index == 0)) {
     p.start = given ? given + state : nullptr;
   } else {
     const int sub = a.seg / a.parts;

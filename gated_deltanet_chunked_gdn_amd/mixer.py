@@ -481,7 +481,8 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, initial_state=None, cu_
     float32 holds.  States float32 [N, Hv, K, V]; K, V in {32, 64, 128}.  The
     token rows of q, k and v may be slices of a wider tensor.  A NaN or an
     infinity in a token reaches the tokens of its 64-token chunk, earlier ones
-    too, and all later ones of its sequence; no other sequence."""
+    too, and the later ones of its sequence, at least as far as its decay is
+    not 0 in float32; no other sequence."""
     p, q, k, v, log_decay = _attn_problem(q, k, v, log_decay, scale, 2)
     dev = q.device
     sq = _Seqs(cu_seqlens, p.B, p.T, dev, check_cu_seqlens)
@@ -506,8 +507,8 @@ def linear_attention_bwd(q, k, v, log_decay, do, dht=None, scale=None, initial_s
     """Backward of linear_attention_fwd.  Returns (dq, dk, dv, dh0): dq, dk
     summed over the v-heads of a group, dh0 None without initial_state.
     log_decay has no gradient (a decay that is learned: selective_scan_fwd's
-    A, with dt = 1).  A NaN or an infinity in a token reaches dq of its chunk
-    and later tokens, dk and dv of its chunk and earlier ones."""
+    A, with dt = 1).  A NaN or an infinity in a token reaches, so far, dq of
+    its chunk and later tokens, dk and dv of its chunk and earlier ones."""
     p, q, k, v, log_decay = _attn_problem(q, k, v, log_decay, scale, 2)
     if do is None or do.shape != v.shape or do.dtype != v.dtype:
         raise ValueError(f"do must have v's shape {list(v.shape)} and dtype {v.dtype}")

@@ -164,8 +164,8 @@ size_t gdn_chunk_fwd_noalloc_max_bytes(void);
  * The operators around the chunked gated delta rule in a sequence mixer: the
  * short causal convolution in front of it, the selective state-space scan
  * that takes the same place, the norm behind it, and all of them (and the
- * delta rule itself) for single tokens; and linear attention with a decay for
- * each head, which takes that place too, with the group norm over its heads.
+ * delta rule itself) for single tokens; linear attention with a decay for each
+ * head, which takes that place too, and the group norm.
  *
  * Layouts are token-major as above, T the total packed tokens with
  * cu_seqlens.  Weights and their gradients are in the type that
@@ -284,10 +284,11 @@ int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, co
  * step) below 2^24 elements.
  * Held in fp32: the decays, the states and every sum over tokens.  In bf16
  * problems the products inside a 64-token chunk and the state and its gradient
- * as operands of o, dq, dk and dv are rounded to bf16.  A NaN or an infinity
- * in a token's inputs reaches the other tokens of its chunk, earlier ones too,
- * and all later ones of its sequence (backwards: all earlier ones); never
- * another sequence. */
+ * as operands of o, dq, dk and dv are rounded to bf16; the state in between is
+ * held to 16 bits, and to fp32 for what a returned state sees of it.  A NaN or
+ * an infinity in a token's inputs reaches the other tokens of its chunk, earlier
+ * ones too, and the later ones of its sequence (backwards: the earlier ones) as
+ * far as its decay is not 0 in fp32, at least; never another sequence. */
 typedef struct {
   int32_t B, T, Hq, Hv, K, V, N, dtype;
   float scale;
