@@ -288,7 +288,8 @@ int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, co
  * held to 16 bits, and to fp32 for what a returned state sees of it.  A NaN or
  * an infinity in a token's inputs reaches the other tokens of its chunk, earlier
  * ones too, and the later ones of its sequence (backwards: the earlier ones) as
- * far as its decay is not 0 in fp32, at least; never another sequence. */
+ * far as its decay is not 0 in fp32, at least; never another sequence.  Outputs
+ * overlap neither inputs nor each other (final_state not initial_state either). */
 typedef struct {
   int32_t B, T, Hq, Hv, K, V, N, dtype;
   float scale;
@@ -341,7 +342,8 @@ int gdn_layer_norm_bwd(const gdn_norm_t *p, const void *dy, const void *x, const
  * a token).
  *   x, gate, y, dy, dx, dgate [N, S, C] problem dtype, contiguous, C = G Dg
  *   weight, bias [C] weight_dtype or NULL; dweight, dbias as these
- *   mean, rstd [N, G] fp32 */
+ *   mean, rstd [N, G] fp32
+ * Outputs overlap neither inputs nor each other. */
 typedef struct {
   int64_t N, S;
   int32_t G, Dg, dtype, weight_dtype, silu;
