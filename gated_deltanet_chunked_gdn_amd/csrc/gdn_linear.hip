@@ -5,10 +5,11 @@
 // A workgroup has a segment of one head and 32 of the output's columns; chunks
 // of 32 tokens.  The state is in accumulators and, for the chunk that reads
 // it, in LDS.  Operands and sums are fp32 throughout.  Short batches are bound by launches
-// and by the chain of chunks: three launches (states that segments add, carry,
-// outputs), segments as short as gives each compute unit two workgroups.  7
-// packed prompts, 1277 tokens, 8 heads, K = V = 64: 7.7 + 3.8 + 10.8 us, 23 a call;
-// backward of 5, 1901 tokens, 8 heads (4 of q and k): 11 + 9 + 27 + 4 us, 47 a call.
+// and by the chain of chunks: segments as short as gives each compute unit two
+// workgroups, their states summed up by the outputs' pass itself where they are few
+// (plan_f32).  7 packed prompts, 1277 tokens, 8 heads, K = V = 64: 20 us a call (25
+// with a carry between); backward of 5, 1901 tokens, 8 heads (4 of q and k): states
+// 11, carry 9, gradients 27, shared heads 4 us, 48 a call.
 #include "gdn_internal.h"
 #include "gdn_linear.hpp"
 
@@ -19,6 +20,7 @@ namespace {
 constexpr int C = 32;        // tokens a chunk
 constexpr int kAhead = 8;    // segments whose states a carry has in flight
 constexpr int kThreads = 256;
+constexpr int kJoinAhead = 4;  // segments whose states the outputs' pass has in flight where it joins them
 
 // What a launch does: the state a segment adds (forwards; or forwards and
 // backwards, for the backward), o, or the three gradients.
@@ -77,9 +79,13 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
       const int r = 16 * kt(i) + 4 * q, c = c0 + 16 * ct + l16;
+      if (p.tr) {  // never stored: dq and dk return no state
+        S[i] = *reinterpret_cast<const f32x4 *>(ptr + (int64_t)c * DA + r);
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float *at = ptr + (p.tr ? (int64_t)c * DA + r + e : (int64_t)(r + e) * DC + c);
+        float *at = ptr + (int64_t)(r + e) * DC + c;
         if (store)
           *at = S[i][e];
         else
@@ -93,6 +99,21 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
   } else {
 #pragma unroll
     for (int i = 0; i < KT; ++i) S[i] = zero4();
+  }
+  if (OUT) {
+    for (int s0 = 0; s0 < p.before; s0 += kJoinAhead) {
+      f32x4 add[kJoinAhead][KT];
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j)
+        if (s0 + j < p.before) state_io(add[j], const_cast<float *>(p.added + (s0 + j) * p.step), false);
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j) {
+        if (s0 + j >= p.before) break;
+        const float d = power(g2, s0 + j == 0 ? p.nt0 : args.seg);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) S[i] = S[i] * d + add[j][i];
+      }
+    }
   }
   const int nt = (int)(loc.t1 - loc.t0), nc = (nt + C - 1) / C;
   struct In {
@@ -326,8 +347,12 @@ hipError_t pass(const AttnArgs &a, const Layout &w, hipStream_t st) {
   return launch_mma_local(a, w, WHAT == kLocals, st);
 }
 
-unsigned carry_blocks(const AttnArgs &a) {
-  return (unsigned)(((int64_t)a.s.N * a.Hv * a.K * a.V / 4 + 255) / 256);
+// of S, and with two ways of Z
+hipError_t run_carry(const AttnArgs &a, const Layout &w, int ways, hipStream_t st) {
+  const int64_t blocks = ((int64_t)a.s.N * a.Hv * a.K * a.V / 4 + 255) / 256;
+  KernelTimer kt("attn_carry", st);
+  carry_kernel<<<(unsigned)(ways * blocks), 256, 0, st>>>(a, w, blocks);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -377,8 +402,13 @@ AttnPlan plan_mma(const AttnArgs &a, bool bwd) {
   return best;
 }
 // fp32: segments as long as the whole batch unless that leaves compute units
-// without two workgroups each.
-AttnPlan plan_f32(const AttnArgs &a) {
+// without two workgroups each.  The outputs' pass sums up the segments before its
+// own where they are few, and no carry is launched; backwards three passes do so
+// with less work beside it, and lose sooner.  (8 heads, K = V = 64, joined and
+// with a carry, us a call: forward of 16 segments 19 and 22, of 32 23 and 27; backward
+// of 8 segments 25 and 28, of 32 54 and 43.  K = V = 128: forward of 8 segments 20
+// and 24, of 16 28 and 32; backward of 8 39 and 40, of 16 75 and 67.)
+AttnPlan plan_f32(const AttnArgs &a, bool bwd) {
   const int64_t per = (int64_t)a.Hv * (a.V / 32);  // workgroups a segment
   const int64_t want = (compute_units() * 2 + per - 1) / per;
   int64_t seg = ((a.s.tokens + want - 1) / want + 63) / 64 * 64;
@@ -387,6 +417,7 @@ AttnPlan plan_f32(const AttnArgs &a) {
   p.parts = 1;
   p.cols = 32;
   p.one_seg = a.longest <= p.seg;
+  p.joined = a.longest <= (int64_t)(bwd ? 8 : 32) * p.seg;
   return p;
 }
 
@@ -395,11 +426,12 @@ AttnPlan plan_f32(const AttnArgs &a) {
 
 AttnPlan attn_plan(const AttnArgs &a0, bool bwd) {
   AttnArgs a = a0;
-  AttnPlan p = a.dtype == 1 ? attn::plan_mma(a, bwd) : attn::plan_f32(a);
+  AttnPlan p = a.dtype == 1 ? attn::plan_mma(a, bwd) : attn::plan_f32(a, bwd);
   a.seg = p.seg;
   a.parts = p.parts;
   a.slots = p.slots = scan::slots_of(a.s, p.seg);
   a.one_seg = p.one_seg;
+  a.joined = p.joined;
   p.ws = attn::layout(a, bwd).total;
   return p;
 }
@@ -410,9 +442,7 @@ hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t st) {
   if (!a.one_seg) {
     hipError_t e = pass<kLocal>(a, w, st);
     if (e != hipSuccess) return e;
-    KernelTimer kt("attn_carry", st);
-    carry_kernel<<<carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (!a.joined && (e = run_carry(a, w, 1, st)) != hipSuccess) return e;
   }
   return pass<kForward>(a, w, st);
 }
@@ -423,9 +453,7 @@ hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t st) {
   hipError_t e;
   if (!a.one_seg) {
     if ((e = pass<kLocals>(a, w, st)) != hipSuccess) return e;
-    KernelTimer kt("attn_carry", st);
-    carry_kernel<<<2 * carry_blocks(a), 256, 0, st>>>(a, w, carry_blocks(a));
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (!a.joined && (e = run_carry(a, w, 2, st)) != hipSuccess) return e;
   }
   if ((e = pass<kGrads>(a, w, st)) != hipSuccess) return e;
   if (a.Hv == a.Hq || a.s.tokens == 0) return hipSuccess;

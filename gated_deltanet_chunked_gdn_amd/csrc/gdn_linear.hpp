@@ -93,6 +93,11 @@ struct Pass {
   float scale_p, scale_in, scale_up;  // of the pairs, the state's share and its update
   const float *start;         // the state to begin with, or null: 0
   float *last;                // where the sequence's last state goes, or null
+  // without a carry: what the segments before this one add, `before` of them from
+  // `added` on in steps of `step`, the first of `nt0` tokens
+  const float *added;
+  int64_t step;
+  int before, nt0;
 };
 
 template <typename E>
@@ -112,8 +117,17 @@ __device__ __forceinline__ Pass make_pass(const AttnArgs &a, const Layout &w, in
   const float *given = p.rev ? a.dht : a.h0;
   // (where the sequence begins, what the call gives; the carry writes the others'.
   // With one segment there is none, whatever the device's lengths say.)
+  p.before = 0;
   if (a.one_seg || (p.rev ? loc.last : loc.index == 0)) {
     p.start = given ? given + state : nullptr;
+  } else if (a.joined) {
+    const Span sp = seq_span(a.s, loc.n);
+    const int64_t ns = segs_of(sp, a.seg), first = first_slot(a.s, sp, loc.n, a.seg) + (p.rev ? ns - 1 : 0);
+    p.start = given ? given + state : nullptr;
+    p.added = (p.rev ? w.zend(a) : w.start(a)) + (first * a.Hv + h) * kv;
+    p.step = (p.rev ? -1 : 1) * a.Hv * kv;
+    p.before = (int)(p.rev ? ns - 1 - loc.index : loc.index);
+    p.nt0 = p.rev ? (int)(sp.end - sp.first - (ns - 1) * a.seg) : a.seg;
   } else {
     const int sub = a.seg / a.parts;
     const int64_t at = first_slot(a.s, seq_span(a.s, loc.n), loc.n, sub) + (p.rev ? (loc.index + 1) * a.parts - 1 : loc.index * a.parts);

@@ -110,6 +110,7 @@ struct AttnArgs {
   int cols;            // of a state that a workgroup of the bf16 passes has, at the most
   int64_t slots;
   bool one_seg;        // no sequence has two segments
+  bool joined;         // the outputs' pass joins the segments' states itself
   float scale;
   int64_t qs, ks, vs;  // elements from one token to the next of q, k, v
   const void *q, *k, *v, *dO;
@@ -121,7 +122,7 @@ struct AttnArgs {
 struct AttnPlan {
   int seg, parts, cols;
   int64_t slots;
-  bool one_seg;
+  bool one_seg, joined;
   size_t ws;
 };
 AttnPlan attn_plan(const AttnArgs &a, bool bwd);

@@ -588,6 +588,7 @@ int gdn_linear_attention_fwd(const gdn_attn_t *p, const void *q, const void *k, 
   a.cols = pl.cols;
   a.slots = pl.slots;
   a.one_seg = pl.one_seg;
+  a.joined = pl.joined;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -619,6 +620,7 @@ int gdn_linear_attention_bwd(const gdn_attn_t *p, const void *q, const void *k, 
   a.cols = pl.cols;
   a.slots = pl.slots;
   a.one_seg = pl.one_seg;
+  a.joined = pl.joined;
   a.q = q;
   a.k = k;
   a.v = v;

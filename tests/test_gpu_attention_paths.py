@@ -34,6 +34,25 @@ def test_attention_in_segments(gdn, dtype, case):  # noqa: F811
     check_attention(gdn, dtype, attn_inputs(dtype, case, seed=11))
 
 
+@pytest.mark.parametrize("T", [65, 300, 512, 513, 1000, 2048, 2049])
+@pytest.mark.parametrize("K,V", [(32, 64), (128, 32)])
+def test_attention_f32_joins_segments(gdn, T, K, V):  # noqa: F811
+    """fp32 sequences of 2 to 33 segments of 64 tokens: few are joined by the passes that read them, more by
+    one between; and packed, with lengths that the host does not know."""
+    announce(f"attention f32 joined {T} {K} {V}")
+    check_attention(gdn, "f32", attn_inputs("f32", (1, T, 1, 2, K, V, None, True, None, -0.05, -0.001), seed=T))
+    q, k, v, decay, h0, do, dht, cu, scale = attn_inputs(
+        "f32", (1, 0, 1, 1, K, V, [T // 2, 0, 1, T - T // 2 - 1], True, None, -0.02, -0.02), seed=T + 1)
+    ro, rht = form(decay, cu, None, K)(dbl(q), dbl(k), dbl(v), dbl(h0))
+    o, ht = gdn.linear_attention_fwd(q, k, v, decay, initial_state=h0, cu_seqlens=cu.cuda(), check_cu_seqlens=False)
+    near("o", o, ro, PAIRS["f32"])
+    near("ht", ht, rht, F32)
+    want = gdn.linear_attention_bwd(q, k, v, decay, do, dht=dht, initial_state=h0, cu_seqlens=cu)
+    got = gdn.linear_attention_bwd(q, k, v, decay, do, dht=dht, initial_state=h0, cu_seqlens=cu.cuda(), check_cu_seqlens=False)
+    for n, x, y in zip(("dq", "dk", "dv", "dh0"), got, want):
+        near(n, x, dbl(y), 2 * F32)  # both within F32 of the formula's
+
+
 def test_attention_in_parts_of_segments(gdn):  # noqa: F811
     """Segments of 512 tokens and more are summed up in four parts; a decay that sees through many of them and
     one that ends inside a part."""
