@@ -264,19 +264,20 @@ __device__ __forceinline__ void carry(const AttnArgs &a, const Layout &w, int64_
   const float g2 = log2_decay(a.g[h]), whole = power(g2, sub);
   // of the first part on the way: backwards the sequence's last
   float d = REV ? power(g2, (int)(sp.end - sp.first - (ns - 1) * sub)) : whole;
-  // a part is read before a state takes its place
+  // a part is read before a state takes its place (reading on at the last one past
+  // it: branches around loads make each waited for)
   f32x4 add[kAhead + 1];
   add[kAhead] = at[0];
   for (int64_t s0 = 0; s0 < last; s0 += kAhead) {
     add[0] = add[kAhead];
 #pragma unroll
-    for (int j = 1; j <= kAhead; ++j) add[j] = s0 + j < last ? at[(s0 + j) * step] : zero4();
+    for (int j = 1; j <= kAhead; ++j) add[j] = at[(s0 + j < last ? s0 + j : last) * step];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int64_t s = s0 + j + 1;  // the part that follows
       if (s > last) break;
       cur = cur * d + add[j];
-      if ((REV ? ns - s : s) % a.parts == 0) at[s * step] = cur;
+      if (((REV ? ns - s : s) & (a.parts - 1)) == 0) at[s * step] = cur;
       d = whole;
     }
   }
