@@ -180,3 +180,65 @@ def test_two_graphs_of_segments(gdn, dtype):  # noqa: F811
             torch.cuda.synchronize()
             for a, b in zip(outs, want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_broadcast_and_turned_inputs(gdn, dtype):  # noqa: F811
+    """Inputs without memory of their own (one head, token or row for all, as a sum's gradient comes) and with
+    other orders of dimensions give the bits of their copies, and are left as they were."""
+    announce(f"attention of broadcast inputs {dtype}")
+    B, T, H, D = 2, 77, 4, 64
+    q, k, v, decay, h0, do, dht, cu, scale = attn_inputs(dtype, (B, T, H, H, D, D, None, True, None, -0.5, -0.01), seed=3)
+    views = {
+        "head": lambda x: x[:, :, :1].expand(B, T, H, D),
+        "token": lambda x: x[:, :1].expand(B, T, H, D),
+        "row": lambda x: x[:1].expand(B, T, H, D),
+        "all": lambda x: x[:1, :1, :1, :1].expand(B, T, H, D),
+        "turned": lambda x: x.transpose(1, 2).contiguous().transpose(1, 2),
+        "across": lambda x: x.transpose(2, 3).contiguous().transpose(2, 3),
+    }
+    state = dht[:1, :1].expand(B, H, D, D)
+    for name, view in views.items():
+        announce(f"  {name}")
+        a = [view(x) for x in (q, k, v, do)]
+        c = [x.contiguous() for x in a]
+        kept = [x.clone() for x in a]
+        want = gdn.linear_attention_fwd(*c[:3], decay, initial_state=state.contiguous())
+        got = gdn.linear_attention_fwd(*a[:3], decay, initial_state=state)
+        want += gdn.linear_attention_bwd(*c[:3], decay, c[3], dht=state.contiguous(), initial_state=h0)
+        got += gdn.linear_attention_bwd(*a[:3], decay, a[3], dht=state, initial_state=h0)
+        s0, s1 = h0.clone(), h0.clone()
+        want += (gdn.linear_attention_step(*(x[:, 0].contiguous() for x in c[:3]), decay, s0), s0)
+        got += (gdn.linear_attention_step(*(x[:, 0] for x in a[:3]), decay, s1), s1)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), name
+        assert all(torch.equal(x, y) for x, y in zip(a, kept)), name
+        w, b = torch.ones(D, device="cuda"), torch.zeros(D, device="cuda")
+        x, dy = a[2], a[3]
+        ref = gdn.group_norm_fwd(c[2], 8, w, b)
+        fwd = gdn.group_norm_fwd(x, 8, w, b)
+        ref += gdn.group_norm_bwd(c[3], c[2], 8, w, b, *ref[1:])[:3]
+        fwd += gdn.group_norm_bwd(dy, x, 8, w, b, *fwd[1:])[:3]
+        for x, y in zip(fwd, ref):
+            assert torch.equal(x, y), name
+
+
+@pytest.mark.parametrize("S,C,G", [(1, 4096, 32), (16384, 96, 8)])
+def test_group_norm_of_more_than_2_31_values(gdn, S, C, G):  # noqa: F811
+    """The last samples of a tensor that 32-bit offsets do not reach, against a call for them alone."""
+    announce(f"group norm of far samples {S} {C}")
+    N = (1 << 31) // (S * C) + 5
+    x = torch.empty(N, S, C, device="cuda", dtype=torch.bfloat16).normal_()
+    w, b = torch.randn(C, device="cuda"), torch.randn(C, device="cuda")
+    y, mean, rstd = gdn.group_norm_fwd(x, G, w, b, activation="silu")
+    # the sums' order goes by the number of samples: fp32 sums, and bf16 steps where one falls the other way
+    ys, ms, rs = gdn.group_norm_fwd(x[-3:], G, w, b, activation="silu")
+    near("y", y[-3:], dbl(ys), 2.0 ** -8)
+    near("mean", mean[-3:], dbl(ms), 1e-4 if S == 1 else 1e-3)  # (means near 0 of values near 1)
+    near("rstd", rstd[-3:], dbl(rs), F32)
+    del y
+    dy = x.flip(0)
+    dx, dw, db, _ = gdn.group_norm_bwd(dy, x, G, w, b, mean, rstd, activation="silu")
+    dxs, _, _, _ = gdn.group_norm_bwd(dy[-3:], x[-3:], G, w, b, ms, rs, activation="silu")
+    near("dx", dx[-3:], dbl(dxs), 2.0 ** -8)
+    assert bool(torch.isfinite(dw).all()) and bool(torch.isfinite(db).all())
