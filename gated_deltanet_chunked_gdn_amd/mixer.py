@@ -449,24 +449,31 @@ def gated_delta_rule_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_
 
 
 def _attn_problem(q, k, v, log_decay, scale, lead):
-    what = "[B, T, Hq, K]" if lead == 2 else "[B, Hq, K]"
-    if q.dim() != lead + 2 or k.shape != q.shape or v.dim() != lead + 2 or v.shape[:lead] != q.shape[:lead]:
+    # (single tokens wait for this: shapes are taken out of their tensors once)
+    qn, vn, dtype = tuple(q.shape), tuple(v.shape), q.dtype
+    if len(qn) != lead + 2 or tuple(k.shape) != qn or len(vn) != lead + 2 or vn[:lead] != qn[:lead]:
+        what = "[B, T, Hq, K]" if lead == 2 else "[B, Hq, K]"
         raise ValueError(f"q, k must be {what} and v as them over the v-heads")
-    if not (q.dtype == k.dtype == v.dtype):
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must share one dtype")
-    _sizes(*q.shape, *v.shape)
-    Hv = v.shape[lead]
+    _sizes(*qn, *vn)
+    (Hq, K), (Hv, V) = qn[lead:], vn[lead:]
     if log_decay is None or log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (Hv,):
         raise ValueError(f"log_decay must be float32 [{Hv}]")
-    K = q.shape[lead + 1]
     dt = _dtype(q, "q, k and v")
-    if scale is None and K == 0:
-        raise ValueError("K must be positive")
-    most = (1 << 24) - 1 if lead == 2 else 1 << 62
-    (qr, qs), (kr, ks), (vr, vs) = (_rows(t, lead, True, most) for t in (q, k, v))
-    p = AttnProblem(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[lead], Hv, K, v.shape[lead + 1], q.shape[0], dt,
-                    float(K ** -0.5 if scale is None else scale), qs, ks, vs, None, None)
-    return p, qr, kr, vr, log_decay.contiguous()
+    if scale is None:
+        if K == 0:
+            raise ValueError("K must be positive")
+        scale = K ** -0.5
+    strides = []
+    for t, width in ((q, Hq * K), (k, Hq * K), (v, Hv * V)):
+        if t.is_contiguous() and t.data_ptr() % 16 == 0:
+            strides.append((t, width))
+        else:
+            strides.append(_rows(t, lead, True, (1 << 24) - 1 if lead == 2 else 1 << 62))
+    (q, qs), (k, ks), (v, vs) = strides
+    p = AttnProblem(qn[0], qn[1] if lead == 2 else 1, Hq, Hv, K, V, qn[0], dt, float(scale), qs, ks, vs, None, None)
+    return p, q, k, v, log_decay.contiguous()
 
 
 def linear_attention_fwd(q, k, v, log_decay, scale=None, initial_state=None, cu_seqlens=None,
