@@ -70,7 +70,8 @@ __device__ __forceinline__ void sweep(const AttnArgs &args, const Pass &p, const
   constexpr int P = Lds<DA>::P, KT = DA / 32;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_of(tid), l16 = lane & 15, q = lane >> 4;
   const float g2 = log2_decay(args.g[h]);
-  if (tid <= C) lds.pw[tid] = power(g2, tid);
+  // (finite with the pass's scale as well)
+  if (tid <= C) lds.pw[tid] = finite(power(g2, tid), 0.9999f * __FLT_MAX__ / fmaxf(1.f, fabsf(args.scale)));
 
   // this wave's tiles of the state: rows 16 kt + 4 q + e of column 16 ct + l16
   auto kt = [&](int i) { return (wave + 4 * i) >> 1; };

@@ -67,9 +67,13 @@ inline Layout layout(const AttnArgs &a, bool bwd) {
 }
 
 // l^n as 2^(g2 n), g2 = log2 of the decay.  (A decay of 0 is as good as one of
-// e^-10000, whose powers but the 0th are 0; -inf would give NaN there.)
-__device__ __forceinline__ float log2_decay(float g) { return (g < -1e4f ? -1e4f : g) * 1.44269504088896340736f; }
-__device__ __forceinline__ float power(float g2, int n) { return __builtin_amdgcn_exp2f(g2 * (float)n); }
+// e^-10000, whose powers but the 0th are 0; -inf would give NaN there, as inf would.)
+__device__ __forceinline__ float log2_decay(float g) { return (g < -1e4f ? -1e4f : g > 1e4f ? 1e4f : g) * 1.44269504088896340736f; }
+// x within +-`most`, NaN as it is.  No factor is infinite: chunks are multiplied
+// out whole, and what is 0 there (rows behind a sequence's end, tokens of zeros, a
+// state that has not begun) stays 0 under any power of a decay that grows.
+__device__ __forceinline__ float finite(float x, float most = __FLT_MAX__) { return x > most ? most : x < -most ? -most : x; }
+__device__ __forceinline__ float power(float g2, int n) { return finite(__builtin_amdgcn_exp2f(g2 * (float)n)); }
 
 enum PassKind { kO, kDq, kDk, kDv };
 

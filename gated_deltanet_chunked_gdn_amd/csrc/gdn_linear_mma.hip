@@ -121,7 +121,7 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int far = 16 * d + (rev ? 4 * g + r - l16 : l16 - 4 * g - r);
-      wt[d][r] = far >= 0 ? power(g2, far) * p.scale_p : 0.f;
+      wt[d][r] = far >= 0 ? finite(power(g2, far) * p.scale_p) : 0.f;
     }
   struct In {
     uint4 q[KS];
@@ -135,8 +135,8 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
     for (int s = 0; s < KS; ++s) in.q[s] = buf_load16(r, (uint32_t)(a_off + 64 * s));
   };
   // the state's decay to token i: of a whole chunk, and of the last
-  const float in_whole = power(g2, rev ? 63 - i : i + 1) * p.scale_in;
-  const float in_rest = rev ? power(g2, way.rest() - 1 - i > 0 ? way.rest() - 1 - i : 0) * p.scale_in : in_whole;
+  const float in_whole = finite(power(g2, rev ? 63 - i : i + 1) * p.scale_in);
+  const float in_rest = rev ? finite(power(g2, way.rest() - 1 - i > 0 ? way.rest() - 1 - i : 0) * p.scale_in) : in_whole;
   auto work = [&](In &in, int step) {
     const bf16 *b = lds.b[step & 1], *c = lds.c[step & 1], *s = lds.s[step & 1];
     f32x4 O[OT], pd[ND];
@@ -306,7 +306,7 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
   };
   // from this thread's token of c to the state behind the chunk, whole or last; of all the chunk
   const int up = rev ? crow + 1 : 63 - crow, up_rest = rev ? up : up - (64 - way.rest());
-  const float u_whole = power(g2, up) * p.scale_up, u_rest = power(g2, up_rest > 0 ? up_rest : 0) * p.scale_up;
+  const float u_whole = finite(power(g2, up) * p.scale_up), u_rest = finite(power(g2, up_rest > 0 ? up_rest : 0) * p.scale_up);
   const float all_whole = power(g2, 64), all_rest = power(g2, way.rest());
   auto commit = [&](const In &in, int step) {
     const int buf = OUT ? step & 1 : 0;

@@ -123,7 +123,8 @@ __global__ __launch_bounds__(64 * kMostWaves) void step_kernel(StepArgs a) {
       out[i] = a.scale * (decay * sq[i] + qk * u[i]);
     }
   } else if (RULE == kStepDecay) {
-    decay = expf(a.g[h]);
+    const float most = expf(a.g[h]);
+    decay = most > __FLT_MAX__ ? __FLT_MAX__ : most;  // a state of 0 stays 0
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u[i] = v[i];

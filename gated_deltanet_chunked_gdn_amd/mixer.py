@@ -485,7 +485,8 @@ def linear_attention_fwd(q, k, v, log_decay, scale=None, initial_state=None, cu_
     (read by v-head h at head h // (Hv // Hq)), v [B, T, Hv, V] in one dtype;
     log_decay float32 [Hv], a constant of the layer: 0 keeps everything, -inf
     nothing, and a state that grows (above 0) is computed as it is, up to what
-    float32 holds.  States float32 [N, Hv, K, V]; K, V in {32, 64, 128}.  The
+    float32 holds (a power of the decay beyond counts as float32's largest
+    number, so that what is 0 stays 0).  States float32 [N, Hv, K, V]; K, V in {32, 64, 128}.  The
     token rows of q, k and v may be slices of a wider tensor.  A NaN or an
     infinity in a token reaches the tokens of its 64-token chunk, earlier ones
     too, and the later ones of its sequence, at least as far as its decay is

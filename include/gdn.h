@@ -277,7 +277,9 @@ int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, co
  *   v, o, do, dv  [B, T, Hv, V]   problem dtype
  *   log_decay     [Hv] fp32, a constant of the layer (no gradient): 0 keeps
  *                 everything, -inf nothing; above 0 the state grows, and is
- *                 computed as it is up to what fp32 holds
+ *                 computed as it is up to what fp32 holds: a power of the
+ *                 decay beyond counts as fp32's largest number, so that what
+ *                 is 0 stays 0
  *   initial_state, final_state, dht, dh0 [N, Hv, K, V] fp32
  * K, V in {32, 64, 128}.  q, k, v, o, do, dq, dk, dv and the states are 16-byte
  * aligned, q_stride, k_stride, v_stride multiples of 16 bytes and (but for the
