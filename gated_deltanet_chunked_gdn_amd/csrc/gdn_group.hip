@@ -758,12 +758,14 @@ hipError_t tall_bwd(const GroupArgs &a, hipStream_t st) {
 }  // namespace
 }  // namespace group
 
-bool group_fits(const GroupArgs &a) {
+bool group_fits(const GroupArgs &a, bool bwd) {
   if (a.N == 0 || group::held(a)) return true;
   int64_t per;
-  const int64_t blocks = a.N * group::row_blocks(a, &per), cols = ((int64_t)a.G * a.Dg + 255) / 256;
-  constexpr int64_t most = (int64_t)1 << 24;
-  return cols < 65536 && blocks < most && blocks * cols < most && a.N * a.G < most;
+  const int64_t blocks = a.N * group::row_blocks(a, &per), channels = (int64_t)a.G * a.Dg, cols = (channels + 255) / 256;
+  constexpr int64_t most = (int64_t)1 << 24;  // workgroups of 256
+  // a workgroup joins each group's blocks; the backward's have kSumThreads, and sum up dw and db beside that
+  const int64_t joins = bwd ? (a.N * a.G + sum_blocks(2 * channels)) * (kSumThreads / 256) : a.N * a.G;
+  return cols < 65536 && blocks < most && blocks * cols < most && joins < most;
 }
 size_t group_fwd_bytes(const GroupArgs &a) {
   const size_t n = group::held(a) || a.N == 0 ? 0 : group::part_bytes(a);

@@ -139,7 +139,7 @@ struct GroupArgs {
   float *mean, *rstd;  // [N][G], written by the forward, read by the backward
   char *ws;
 };
-bool group_fits(const GroupArgs &a);  // into launches of less than 2^32 threads
+bool group_fits(const GroupArgs &a, bool bwd);  // into launches of less than 2^32 threads
 size_t group_fwd_bytes(const GroupArgs &a);
 size_t group_bwd_bytes(const GroupArgs &a);
 hipError_t launch_group_fwd(const GroupArgs &a, hipStream_t st);

@@ -230,7 +230,7 @@ int check_attn(const gdn_attn_t *p, bool step, bool bwd, gdn::AttnArgs *a) {
 }
 
 // ---- group norm
-int check_group(const gdn_group_t *p, gdn::GroupArgs *a) {
+int check_group(const gdn_group_t *p, bool bwd, gdn::GroupArgs *a) {
   if (!p) return set_error(GDN_ERR_INVALID_ARG, "problem descriptor is NULL");
   if (p->N < 0 || p->S <= 0 || p->G <= 0 || p->Dg <= 0)
     return set_error(GDN_ERR_INVALID_ARG, "dimensions must be positive (N=%lld S=%lld G=%d Dg=%d)", (long long)p->N,
@@ -252,7 +252,7 @@ int check_group(const gdn_group_t *p, gdn::GroupArgs *a) {
   a->wdtype = p->weight_dtype;
   a->silu = p->silu;
   a->eps = p->eps;
-  if (!gdn::group_fits(*a)) return set_error(GDN_ERR_UNSUPPORTED, "problem too large for the launch grid");
+  if (!gdn::group_fits(*a, bwd)) return set_error(GDN_ERR_UNSUPPORTED, "problem too large for the launch grid");
   return GDN_OK;
 }
 
@@ -673,19 +673,19 @@ int gdn_linear_attention_step(const gdn_attn_t *p, const void *q, const void *k,
 size_t gdn_group_norm_fwd_workspace_size(const gdn_group_t *p) {
   gdn::clear_error();
   gdn::GroupArgs a;
-  return check_group(p, &a) == GDN_OK ? gdn::group_fwd_bytes(a) : 0;
+  return check_group(p, false, &a) == GDN_OK ? gdn::group_fwd_bytes(a) : 0;
 }
 size_t gdn_group_norm_bwd_workspace_size(const gdn_group_t *p) {
   gdn::clear_error();
   gdn::GroupArgs a;
-  return check_group(p, &a) == GDN_OK ? gdn::group_bwd_bytes(a) : 0;
+  return check_group(p, true, &a) == GDN_OK ? gdn::group_bwd_bytes(a) : 0;
 }
 
 int gdn_group_norm_fwd(const gdn_group_t *p, const void *x, const void *weight, const void *bias, const void *gate,
                        void *y, float *mean, float *rstd, void *workspace, size_t ws_bytes, void *stream) {
   gdn::clear_error();
   gdn::GroupArgs a;
-  int rc = check_group(p, &a);
+  int rc = check_group(p, false, &a);
   if (rc != GDN_OK) return rc;
   if (p->N > 0 && (!x || !y || !mean || !rstd))
     return set_error(GDN_ERR_INVALID_ARG, "x, y, mean and rstd are required");
@@ -711,7 +711,7 @@ int gdn_group_norm_bwd(const gdn_group_t *p, const void *dy, const void *x, cons
                        void *dgate, void *workspace, size_t ws_bytes, void *stream) {
   gdn::clear_error();
   gdn::GroupArgs a;
-  int rc = check_group(p, &a);
+  int rc = check_group(p, true, &a);
   if (rc != GDN_OK) return rc;
   if (p->N > 0 && (!dy || !x || !mean || !rstd || !dx || (gate && !dgate)))
     return set_error(GDN_ERR_INVALID_ARG, "dy, x, mean, rstd, dx and dgate (with gate) are required");
