@@ -54,6 +54,10 @@ int check_slots(const int32_t *idx, int slots, int B) {
 
 constexpr int64_t kGrid = (int64_t)1 << 31;  // workgroups of a launch
 
+// A step has a wave for 32 columns of a row's head, up to four a workgroup (and a
+// launch has fewer than 2^32 threads).
+bool step_fits(int B, int Hv, int V) { return (double)B * Hv * (V / 32) <= (double)((1 << 26) - 4); }
+
 // ---- convolution
 int check_conv(const gdn_conv_t *p, gdn::ConvArgs *a) {
   if (!p) return set_error(GDN_ERR_INVALID_ARG, "problem descriptor is NULL");
@@ -132,7 +136,7 @@ int check_scan(const gdn_scan_t *p, bool step, gdn::ScanArgs *a) {
     return set_error(GDN_ERR_LAYOUT, "c, b and x strides must be multiples of 16 bytes");
   const int64_t tokens = (int64_t)p->B * p->T;
   if (tokens * (p->Hv > p->Hq ? p->Hv : p->Hq) * 128 > ((int64_t)1 << 40) ||
-      (tokens / 16 + p->N) * p->Hv * 4 >= kGrid || (int64_t)p->B * p->Hv >= kGrid)
+      (tokens / 16 + p->N) * p->Hv * 4 >= kGrid || (step && !step_fits(p->B, p->Hv, p->V)))
     return set_error(GDN_ERR_UNSUPPORTED, "problem too large");
   *a = gdn::ScanArgs{};
   a->s = gdn::Seqs{p->cu_seqlens, p->cu_seqlens ? p->N : p->B, p->T, tokens};
@@ -224,6 +228,7 @@ int check_attn(const gdn_attn_t *p, bool step, bool bwd, gdn::AttnArgs *a) {
   constexpr int64_t kBlocks = (int64_t)1 << 24;
   const int64_t heads = (int64_t)p->Hv * (step ? 0 : gdn::attn_plan(*a, bwd).slots);
   if (a->s.tokens * p->Hv * 128 > ((int64_t)1 << 40) || (int64_t)a->s.N * p->Hv >= kGrid || heads * 36 >= kBlocks ||
+      (step && !step_fits(p->B, p->Hv, p->V)) ||
       (!step && ((int64_t)a->s.N * p->Hv * p->K * p->V / 512 >= kBlocks || (bwd && a->s.tokens * p->Hq * p->K / 1024 >= kBlocks))))
     return set_error(GDN_ERR_UNSUPPORTED, "problem too large");
   return GDN_OK;
