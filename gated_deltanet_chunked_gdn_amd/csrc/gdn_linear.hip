@@ -376,7 +376,7 @@ namespace {
 AttnPlan plan_mma(const AttnArgs &a, bool bwd) {
   const double cus = (double)compute_units(), steps = (double)a.s.tokens / 64, passes = bwd ? 3 : 1;
   double longest = (double)a.longest;
-  if (a.s.cu && a.longest == a.s.T && longest > 4. * a.s.T / a.s.N) longest = 4. * a.s.T / a.s.N;
+  if (!a.known && longest > 4. * a.s.T / a.s.N) longest = 4. * a.s.T / a.s.N;
   AttnPlan best = {};
   double least = 1e300;
   for (int cols = a.V < 64 ? 32 : 64; cols >= 32; cols /= 2) {

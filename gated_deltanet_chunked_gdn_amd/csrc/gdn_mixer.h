@@ -106,6 +106,7 @@ struct AttnArgs {
   Seqs s;
   int Hq, Hv, K, V, dtype;
   int64_t longest;     // sequence, as far as the host knows
+  bool known;          // the host knows
   int seg, parts;      // tokens of a segment, and the parts (1 or 4) it is taken in where states are summed up
   int cols;            // of a state that a workgroup of the bf16 passes has, at the most
   int64_t slots;

@@ -216,6 +216,7 @@ int check_attn(const gdn_attn_t *p, bool step, bool bwd, gdn::AttnArgs *a) {
   a->ks = ks;
   a->vs = vs;
   a->longest = p->T;
+  a->known = !p->cu_seqlens || p->cu_seqlens_host;
   if (p->cu_seqlens_host) {
     a->longest = 0;
     for (int n = 0; n < p->N; ++n) {
