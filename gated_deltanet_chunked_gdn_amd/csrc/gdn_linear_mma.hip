@@ -21,10 +21,15 @@
 // that a lane ends with eight in a row.
 //
 // Roundings to bf16: P and the state as operands of the outputs, which are bf16
-// themselves.  The state is held in fp32.  Its update takes the weighted c, an
-// fp32 number, as two bf16 parts (off by 2^-17), and as three, which lose
-// nothing, where a returned or carried state sees the step; one part left dq and
-// dk 1.6 times as far from 64 bits as rounding the output alone.
+// themselves; o is 1.25 times, dq and dk 1.4 times as far from 64 bits as rounding
+// the output alone.  Not so for a way of one chunk, whose P may be few numbers (one
+// for a token alone: dq and dk up to 3.2 times): there both are taken as two bf16
+// parts, off by 2^-17, the state's second one in the buffer that no second chunk
+// needs.  (P in two parts throughout: 1.14 and 1.3 times, the passes 2 to 4 % longer.)
+// The state is held in fp32.  Its update takes the weighted c, an fp32 number, as
+// two bf16 parts (off by 2^-17), and as three, which lose nothing, where a returned
+// or carried state sees the step; one part left dq and dk 1.6 times as far from 64
+// bits as rounding the output alone.
 //
 // What bounds it: the chunks of a sequence follow one another, one workgroup a
 // compute unit (LDS), 1.2 us a chunk of 32 columns and 1.6 of 64, between the
@@ -58,6 +63,12 @@ __device__ __forceinline__ bf16x8 join(const bf16x4 &a, const bf16x4 &b) {
 // t is column 32 (t / 2) + 8 q + 4 (t % 2) + e, so that a lane ends with runs of
 // eight.  Row of a column in this order:
 __device__ __forceinline__ int dealt(int v) { return 32 * (v >> 5) + 16 * ((v >> 2) & 1) + 4 * ((v >> 3) & 3) + (v & 3); }
+
+// What bf16 leaves of x (nothing of an infinity).
+__device__ __forceinline__ float left_of(float x) {
+  const float l = x - (float)(bf16)x;
+  return __builtin_isfinite(l) ? l : 0.f;
+}
 
 // A pass's two chunks.  s: the state that enters it, a column a row, dealt; w: u c
 // in PARTS bf16 numbers.
@@ -137,7 +148,8 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
   // the state's decay to token i: of a whole chunk, and of the last
   const float in_whole = finite(power(g2, rev ? 63 - i : i + 1) * p.scale_in);
   const float in_rest = rev ? finite(power(g2, way.rest() - 1 - i > 0 ? way.rest() - 1 - i : 0) * p.scale_in) : in_whole;
-  auto work = [&](In &in, int step) {
+  auto work = [&](In &in, int step, auto lone) {
+    constexpr bool LONE = decltype(lone)::value;  // the way's one chunk
     const bf16 *b = lds.b[step & 1], *c = lds.c[step & 1], *s = lds.s[step & 1];
     f32x4 O[OT], pd[ND];
 #pragma unroll
@@ -178,7 +190,15 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
       for (int t = 0; t < OT; ++t) O[t] = M::mma(m[k & 1][ND + t], q, O[t]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    fetch(in);
+    if constexpr (LONE) {  // the rest of the state
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < OT; ++t)
+          O[t] = M::mma(M::ld(lds.s[1] + (16 * t + l16) * P + 32 * k + 8 * g), __builtin_bit_cast(bf16x8, in.q[k]), O[t]);
+    } else {
+      fetch(in);
+    }
     const float pin = way.part(step) ? in_rest : in_whole;
 #pragma unroll
     for (int t = 0; t < OT; ++t)
@@ -187,13 +207,21 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
 #pragma unroll
     for (int d = 0; d < ND; d += 2) {
       bf16x8 w;
+      float f[8];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        w[r] = (bf16)(pd[d][r] * wt[d][r]);
-        w[4 + r] = d + 1 < ND ? (bf16)(pd[d + 1 < ND ? d + 1 : d][r] * wt[d + 1 < ND ? d + 1 : d][r]) : (bf16)0.f;
+      for (int r = 0; r < 8; ++r) {
+        const int e = d + (r >> 2);
+        f[r] = e < ND ? pd[e < ND ? e : d][r & 3] * wt[e < ND ? e : d][r & 3] : 0.f;
+        w[r] = (bf16)f[r];
       }
 #pragma unroll
       for (int t = 0; t < OT; ++t) O[t] = M::mma(cf[d / 2][t], w, O[t]);
+      if constexpr (LONE) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) w[r] = (bf16)left_of(f[r]);
+#pragma unroll
+        for (int t = 0; t < OT; ++t) O[t] = M::mma(cf[d / 2][t], w, O[t]);
+      }
     }
     const auto r = to.next();
     if constexpr (PART) {
@@ -235,13 +263,16 @@ __device__ __forceinline__ void outputs(const Pass &p, const Way &way, float g2,
   // (with a way out between the two, the compiler sees one back to the loop's
   // head there too, and waits at the head for the loads of the second half)
   for (int step = 0; step + 1 < way.nc; step += 2) {
-    work(x, step);
+    work(x, step, std::false_type());
     __syncthreads();
-    work(y, step + 1);
+    work(y, step + 1, std::false_type());
     __syncthreads();
   }
-  if (way.nc & 1) {
-    work(x, way.nc - 1);
+  if (way.nc == 1) {
+    work(x, 0, std::true_type());
+    __syncthreads();
+  } else if (way.nc & 1) {
+    work(x, way.nc - 1, std::false_type());
     __syncthreads();
   }
 }
@@ -340,7 +371,7 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
     }
   };
   f32x4 S[KT][CT];
-  auto show = [&](int buf) {
+  auto show = [&](const f32x4(&S)[KT][CT], int buf) {
     if (!OUT || !tiles) return;
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
@@ -358,7 +389,17 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
     for (int j = 0; j < CT; ++j) S[i][j] = zero4();
   if (OUT && p.start) state_io(S, const_cast<float *>(p.start), false);
   commit(x, 0);
-  show(0);
+  show(S, 0);
+  if (OUT && way.nc == 1) {  // and what bf16 leaves of it, where the next state would lie
+    f32x4 low[KT][CT];
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) low[i][j][e] = left_of(S[i][j][e]);
+    show(low, 1);
+  }
   __syncthreads();
   // `in` is free, `next` has the chunk after this one
   auto work = [&](In &in, const In &next, int step) {
@@ -411,7 +452,7 @@ __device__ __forceinline__ void states(const Pass &p, const Way &way, float g2, 
       add(1);
       add(0);
     }
-    show((step + 1) & 1);
+    if (way.nc > 1) show(S, (step + 1) & 1);
   };
   for (int step = 0; step + 1 < way.nc; step += 2) {
     work(x, y, step);

@@ -286,12 +286,13 @@ int gdn_delta_rule_step(const gdn_problem_t *p, const void *q, const void *k, co
  * step) below 2^24 elements.
  * Held in fp32: the decays, the states and every sum over tokens.  In bf16
  * problems the products inside a 64-token chunk and the state and its gradient
- * as operands of o, dq, dk and dv are rounded to bf16; the state in between is
- * held to 16 bits, and to fp32 for what a returned state sees of it.  A NaN or
- * an infinity in a token's inputs reaches the other tokens of its chunk, earlier
- * ones too, and the later ones of its sequence (backwards: the earlier ones) as
- * far as its decay is not 0 in fp32, at least; never another sequence.  Outputs
- * overlap neither inputs nor each other (final_state not initial_state either). */
+ * as operands of o, dq, dk and dv are rounded to bf16 (where a sequence is one
+ * chunk, to two bf16 numbers: 2^-17); the state in between is held to 16 bits,
+ * and to fp32 for what a returned state sees of it.  A NaN or an infinity in a
+ * token's inputs reaches the other tokens of its chunk, earlier ones too, and the
+ * later ones of its sequence (backwards: the earlier ones) as far as its decay is
+ * not 0 in fp32, at least; never another sequence.  Outputs overlap neither
+ * inputs nor each other (final_state not initial_state either). */
 typedef struct {
   int32_t B, T, Hq, Hv, K, V, N, dtype;
   float scale;

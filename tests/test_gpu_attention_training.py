@@ -17,8 +17,8 @@ import pytest
 import torch
 
 from tests.gpu_util import announce
-from tests.mixer_ref import dbl, near, spans
-from tests.test_gpu_attention import F32, PAIRS, attn_inputs, gdn  # noqa: F401
+from tests.mixer_ref import dbl, grads, near, spans
+from tests.test_gpu_attention import F32, PAIRS, attn_inputs, form, gdn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -105,6 +105,37 @@ def test_forward_of_both_widths(gdn, case, last):  # noqa: F811
     near_rounding("o", o, ro)
     if last:
         near("ht", ht, rht, F32)
+
+
+@pytest.mark.parametrize("Hq,Hv,K,V", [(1, 1, 32, 32), (1, 4, 64, 64), (2, 2, 128, 64), (3, 9, 32, 128)])
+@pytest.mark.parametrize("lens", [[1], [2], [0, 1, 1, 3], [6], [17, 40], [64], [63, 1, 0, 48]])
+@pytest.mark.parametrize("state", [False, True])
+def test_sequences_of_one_chunk_lose_nothing(gdn, lens, state, Hq, Hv, K, V):  # noqa: F811
+    """A few pairs of tokens, or a state alone, decide every output: their roundings do not average out, and those of
+    v-heads that share a q-head are not small beside a sum that cancels.  They are held to 2^-17, which beside the
+    output's own 2^-9 is nothing: within 5 % of rounding the output alone."""
+    announce(f"attention one chunk {lens} {state} {Hq} {Hv} {K} {V}")
+    q, k, v, decay, h0, do, dht, cu, scale = attn_inputs("bf16", (1, 0, Hq, Hv, K, V, lens, state, None, -1.0, -0.01), seed=sum(lens))
+    f = form(decay, cu, None, K)
+    o, ht = gdn.linear_attention_fwd(q, k, v, decay, initial_state=h0, cu_seqlens=cu)
+    ro, rht = f(dbl(q), dbl(k), dbl(v), dbl(h0))
+    near_rounding("o", o, ro, 1.05)
+    near("ht", ht, rht, F32)
+    got = gdn.linear_attention_bwd(q, k, v, decay, do, dht=dht, initial_state=h0, cu_seqlens=cu)
+    for n, a, r in zip(("dq", "dk", "dv"), got, grads(f, [q, k, v, h0], [do, dht])):
+        near_rounding(n, a, r, 1.05)
+
+
+def test_infinities_of_one_chunk(gdn):  # noqa: F811
+    """An infinite state or pair stays what it is: the outputs it does not meet are finite, the others are not."""
+    q, k, v, decay, h0, do, dht, cu, scale = attn_inputs("bf16", (2, 5, 1, 2, 32, 64, None, True, None, -0.1, -0.01), seed=3)
+    q, k = q.abs() + 0.1, k.abs() + 0.1
+    h0[1, 1, 3, 7] = float("inf")
+    o, ht = gdn.linear_attention_fwd(q, k, v, decay, initial_state=h0)
+    hit = torch.zeros(o.shape, dtype=torch.bool)
+    hit[1, :, 1, 7] = True
+    assert torch.isfinite(o.cpu()[~hit]).all() and (o.cpu()[hit] == float("inf")).all()
+    assert ht[1, 1, 3, 7] == float("inf") and int((~torch.isfinite(ht)).sum()) == 1
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
