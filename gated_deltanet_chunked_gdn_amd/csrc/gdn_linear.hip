@@ -357,17 +357,14 @@ hipError_t run_carry(const AttnArgs &a, const Layout &w, int ways, hipStream_t s
   return hipGetLastError();
 }
 
-}  // namespace
-}  // namespace attn
-
-namespace attn {
-namespace {
-
 // Segments of bf16 problems, and the columns that a workgroup has: what takes the
-// least by a model of the passes' time in us (measured at K = V = 128).  A step of
-// 64 tokens takes a workgroup, one a compute unit, 1.6 with 64 columns and 1.2 with
-// 32, as long as the longest segment has steps or the work fills the chip;
-// cutting sequences costs the launches for the states and reading k and v again.
+// least by a model of the passes' time in us.  A step of 64 tokens takes a
+// workgroup, one a compute unit, 1.6 with 64 columns and 1.2 with 32, as long as the
+// longest segment has steps or the work fills the chip; cutting sequences costs the
+// launches for the states and reading k and v again.  The four numbers are of K = V
+// = 128 and taken for the smaller heads too.  The work is spread evenly: whole
+// rounds of workgroups are not counted, nor what long sequences leave at a round's
+// end, so that a few heads more than fill the chip are modelled too short.
 // (8192 tokens, 64 heads: 64 columns, one segment 185 and two 171, 32 columns one
 // segment 162, two 222.  2 x 4096 tokens, 32 heads, backward: 64 columns, one
 // segment 178 and two 223, 32 columns 229.  Packed, 16 sequences, 32 heads: 64

@@ -185,3 +185,25 @@ def test_group_norm_sums_over_more_than_2_31_values(gdn, S, C, G):  # noqa: F811
         rb += dz.sum((0, 1))
     near("dw", dw, rw, F32)
     near("db", db, rb, F32)
+
+
+def test_more_than_2_31_elements(gdn):  # noqa: F811
+    """One sequence whose rows of v, o and their gradients 32-bit offsets do not reach, heads in pairs; with a decay
+    that forgets within some 300 tokens its two ends are those of the ends alone."""
+    announce("attention of more than 2^31 elements")
+    T, Hq, Hv, K, V, n = 263000, 32, 64, 32, 128, 1500
+    assert T * Hv * V > 1 << 31
+    mk = lambda H, D: torch.empty(1, T, H, D, device="cuda", dtype=torch.bfloat16).normal_()  # noqa: E731
+    q, k, v, do = mk(Hq, K), mk(Hq, K), mk(Hv, V), mk(Hv, V)
+    decay = torch.full((Hv,), -0.1, device="cuda")
+    o, ht = gdn.linear_attention_fwd(q, k, v, decay)
+    dq, dk, dv, _ = gdn.linear_attention_bwd(q, k, v, decay, do)
+    ends = []
+    for part in (slice(0, n), slice(T - n, T)):
+        x = [t[:, part].contiguous() for t in (q, k, v, do)]
+        ends.append((*gdn.linear_attention_fwd(*x[:3], decay), *gdn.linear_attention_bwd(*x[:3], decay, x[3])))
+    # (tokens 1000 and more from the cut, e^-100; steps of bf16 where a sum falls the other way)
+    for name, whole, i in (("o", o, 0), ("dq", dq, 2), ("dk", dk, 3), ("dv", dv, 4)):
+        near(name + " begins", whole[:, :500], dbl(ends[0][i][:, :500]), PAIRS["bf16"])
+        near(name + " ends", whole[:, -500:], dbl(ends[1][i][:, -500:]), PAIRS["bf16"])
+    near("ht", ht, dbl(ends[1][1]), F32)
