@@ -19,12 +19,14 @@
 // their means (which are taken from the thread's first value of the channel, so
 // that a mean far from zero costs them no bits).
 //
-// Measured (a large copy: 5.1 TB/s).  Held, 8192 tokens, 64 heads of 128, bf16
-// with a gate: forward 81 us, 5.0 TB/s; backward 124 and 5 for dw and db, 5.4
-// TB/s.  By rows, bf16 with SiLU: 8 maps of 9216 x 320, 32 groups, sums 12, join 3,
-// outputs 16 us; backward of 6 maps of 4096 x 512 13 + 5.5 + 14.  The second
-// reading comes from the last-level cache; the launch between the two large ones
-// is as long as small launches are.
+// Measured (a large copy: 5.1 TB/s; kernels in a trace, calls that follow each
+// other).  Held, 8192 tokens, 64 heads of 128, bf16 with a gate: forward 81 us, 5.0
+// TB/s; backward 135 and 5 for dw and db, the call 140, 4.8 TB/s.  By rows, bf16 with
+// SiLU: 8 maps of 9216 x 320, 32 groups, sums 13, join 4, outputs 17, the call 32;
+// backward of 6 maps of 4096 x 512 14 + 6 + 15, the call 33.  The second reading
+// comes from the last-level cache; the launch between the two large ones is as long
+// as small launches are.  Which groups are held goes by what registers hold; with
+// several positions of few channels the rows' form was not measured against it.
 #include "gdn_internal.h"
 #include "gdn_mixer.hpp"
 

@@ -7,9 +7,9 @@
 // it, in LDS.  Operands and sums are fp32 throughout.  Short batches are bound by launches
 // and by the chain of chunks: segments as short as gives each compute unit two
 // workgroups, their states summed up by the outputs' pass itself where they are few
-// (plan_f32).  7 packed prompts, 1277 tokens, 8 heads, K = V = 64: 20 us a call (25
-// with a carry between); backward of 5, 1901 tokens, 8 heads (4 of q and k): states
-// 11, carry 9, gradients 27, shared heads 4 us, 48 a call.
+// (plan_f32).  7 packed prompts, 1277 tokens, 8 heads, K = V = 64: 18 us a call (5
+// more with a carry between); backward of 5, 1901 tokens, 8 heads (4 of q and k): 47
+// a call, in a trace states 12, carry 7.5, gradients 27.5, shared heads 4.5.
 #include "gdn_internal.h"
 #include "gdn_linear.hpp"
 

@@ -34,11 +34,14 @@
 // What bounds it: the chunks of a sequence follow one another, one workgroup a
 // compute unit (LDS), 1.2 us a chunk of 32 columns and 1.6 of 64, between the
 // barriers LDS reads, products and the commits of the next chunk, each waited for;
-// HBM would take half of that.  K = V = 128: 8192 tokens x 64 heads forward 160
-// us (3.4 TB/s of its inputs and outputs once each); 16384 packed tokens x 32 heads
-// in 16 sequences 167 us; backward of 2 x 4096 x 32 heads 185 us, its three passes
-// side by side in one launch.  Waves of their own for P (sixteen, a read twice)
-// 210 us against 161; a through LDS the same within noise.
+// HBM would take half of that.  One workgroup, because b, c, u c and the state lie
+// in LDS twice; a step moves some 280 KB through it at 64 columns.  K = V = 128: 8192
+// tokens x 64 heads forward 160 to 164 us (3.3 TB/s of its inputs and outputs once
+// each); 16384 packed tokens x 32 heads in 16 sequences 167 us, at their end the
+// longest prompts of the last heads alone; backward of 2 x 4096 x 32 heads 187 us, its
+// three passes side by side in one launch, 384 workgroups, one and a half rounds.
+// Waves of their own for P (sixteen, a read twice) 210 us against 161; a through LDS
+// the same within noise.
 #include <type_traits>
 
 #include "gdn_internal.h"
